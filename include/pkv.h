@@ -354,6 +354,155 @@ pkv_status pkv_paged_prefill_append_host(const pkv_pool_desc* pool, void* k_pool
 pkv_status pkv_copy_blocks(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
                            const int32_t* pairs, int num_pairs, void* stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ * A row's first rotary_dim elements are pairs turned by the angle
+ * position * inv_freq[i] of their pair i:
+ *   y_a = attn_scale * (x_a cos - x_b sin),  y_b = attn_scale * (x_b cos + x_a sin),
+ * a = i, b = i + rotary_dim / 2 (interleaved == 0) or a = 2 i, b = 2 i + 1
+ * (interleaved != 0); elements from rotary_dim on pass unchanged.  Keys go into the cache
+ * turned, so the position is the token's place in its sequence, not in the cache: after an
+ * eviction (pkv_evict) the two differ.  The angle is taken modulo one turn in 64-bit
+ * integers, so far positions cost no accuracy; the row is turned in fp32 and rounded once.
+ *
+ * pkv_rope_frequencies fills host inv_freq[rotary_dim / 2] with theta^(-2 i / rotary_dim),
+ * scaled for contexts longer than the trained one as `scaling` says (NULL: plain), and
+ * *attn_scale (may be NULL) with the scale that goes with it (1, or for PKV_ROPE_YARN
+ * 0.1 ln(factor) + 1).  rotary_dim even, theta > 0, factor >= 1, 0 <= low < high,
+ * original_context > 0: PKV_ERR_INVALID otherwise.  With n_i = original_context * f_i /
+ * (2 pi) turns over the trained context, PKV_ROPE_LLAMA3 and PKV_ROPE_YARN divide a
+ * frequency by `factor` where n_i <= low, keep it where n_i >= high, and blend the two
+ * linearly in n_i between. */
+typedef enum pkv_rope_kind {
+    PKV_ROPE_PLAIN = 0,
+    PKV_ROPE_LINEAR = 1, /* every frequency divided by factor */
+    PKV_ROPE_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)) */
+    PKV_ROPE_LLAMA3 = 3, /* by bands of n_i (usual: low 1, high 4) */
+    PKV_ROPE_YARN = 4    /* by bands of n_i (usual: low 1, high 32), with an attn_scale */
+} pkv_rope_kind;
+typedef struct pkv_rope_scaling {
+    int32_t kind; /* pkv_rope_kind */
+    double factor, low, high, original_context;
+} pkv_rope_scaling;
+pkv_status pkv_rope_frequencies(double* inv_freq, float* attn_scale, int rotary_dim, double theta,
+                                const pkv_rope_scaling* scaling);
+
+/* Rows x [num_tokens][num_heads][head_dim] -> out, turned by their token's position.
+ *   x, out      device, dtype (pkv_dtype), 16-byte aligned; token t's heads start at element
+ *               t * stride (a multiple of 16 bytes; heads of a token contiguous), so a slice
+ *               of a fused projection is read in place.  out_stride >= num_heads * head_dim.
+ *               out may be x itself (same address and stride), else must not overlap it.
+ *   positions   device int32 [num_tokens] (negative ones turn the other way).
+ *   inv_freq    device double [rotary_dim / 2], radians per position.
+ *   rotary_dim  a multiple of 16, 16 .. head_dim; head_dim 64 or 128 (PKV_ERR_UNSUPPORTED).
+ *   inverse     nonzero: the opposite turn.  It undoes the turn for attn_scale 1, and is its
+ *               gradient: d loss / d x is the inverse turn, same attn_scale, of d loss / d out. */
+pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int64_t x_stride,
+                    const int32_t* positions, const double* inv_freq, int rotary_dim,
+                    int interleaved, int inverse, float attn_scale, int64_t num_tokens,
+                    int num_heads, int head_dim, void* stream);
+
+/* pkv_rope of a step's q rows into q_out, and pkv_kv_append of its k rows, turned, and v
+ * rows, in one launch.  q, k, v: [num_tokens][heads][head_dim] with token strides as above
+ * (q has num_q_heads heads, k and v the pool's); q_out may be q itself (same stride).
+ * Slots as pkv_kv_append: a negative one skips the token's K and V (its q is turned all the
+ * same), one past the pool raises PKV_ERR_OOB in the device status word. */
+pkv_status pkv_rope_append(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
+                           const int64_t* slot_mapping, void* q_out, int64_t q_out_stride,
+                           const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* positions,
+                           const double* inv_freq, int rotary_dim, int interleaved,
+                           float attn_scale, int64_t num_tokens, int num_q_heads, void* stream);
+
+/* ---------------------------------------------------------------- accumulated attention weights
+ * What eviction goes by: how much attention each cached token has received.
+ *   weights   device fp32 [num_rows][num_kv_heads][weights_stride], updated in place for the
+ *             L cached tokens of each sequence:
+ *               weights[row][kvh][j] = decay * weights[row][kvh][j] + sum of p_hj
+ *             over the query heads h of kv head kvh (and the query tokens of the call), p the
+ *             softmax probabilities.  Entries from L on are left as they are: zero a row
+ *             before its sequence's first call (pkv_evict keeps the rest at zero).
+ *   row_ids   device int32 [num_seqs], the row of each sequence, each its own; a negative one
+ *             leaves the weights alone (padding); NULL: sequence s has row s.  A row >=
+ *             num_rows raises PKV_ERR_OOB in the device status word and is not touched.
+ *   weights_stride >= max_context.
+ *   decay     in [0, 1]; 1 adds up, 0 overwrites (what was there is not read).
+ * Every weight is summed by one thread in a fixed order: the same call gives the same bits.
+ *
+ * pkv_paged_decode_weights is pkv_paged_decode (k_new and v_new NULL) or
+ * pkv_paged_decode_append (both given), with the same output, and the weights of the step's
+ * one query token per sequence.  The scores are kept in the workspace on the way, 4 bytes
+ * per query head and token. */
+size_t pkv_paged_decode_weights_workspace_bytes(const pkv_pool_desc* pool, int num_seqs,
+                                                int num_q_heads, int max_context,
+                                                int partition_blocks);
+pkv_status pkv_paged_decode_weights(const pkv_pool_desc* pool, void* out, const void* q,
+                                    void* k_pool, void* v_pool, const void* k_new,
+                                    const void* v_new, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* context_lens,
+                                    int max_context, int num_seqs, int num_q_heads, float scale,
+                                    int partition_blocks, float* weights, int64_t weights_stride,
+                                    const int32_t* row_ids, int num_rows, float decay,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* The weights of a prompt chunk, beside pkv_paged_prefill: the last `window` new tokens of
+ * each request (0, or more than it has: all of them) attend causally, query i of request r to
+ * keys 0 .. cached_lens[r] + i, and their probabilities are summed per key.  K must be in the
+ * pool; V is not read.  A request without new tokens is left alone.  One whose lengths are out
+ * of range (cached < 0, new > max_new, cached + new > max_context, q rows outside
+ * [0, total_new)) raises PKV_ERR_OOB in the device status word and is skipped, as is a block
+ * id outside the pool (that request's weights are then not valid).
+ *   max_context  host upper bound of cached + new, at most max_blocks_per_seq * block_size.
+ *   workspace    16-byte aligned, clobbered.  Other arguments as pkv_paged_prefill. */
+size_t pkv_paged_prefill_weights_workspace_bytes(const pkv_pool_desc* pool, int num_reqs,
+                                                 int num_q_heads, int max_new, int max_context,
+                                                 int window);
+pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, const void* k_pool,
+                                     const int32_t* block_tables, int max_blocks_per_seq,
+                                     const int32_t* cached_lens, const int32_t* new_lens,
+                                     const int32_t* q_offsets, int num_reqs, int total_new,
+                                     int max_new, int max_context, int num_q_heads, float scale,
+                                     int window, float* weights, int64_t weights_stride,
+                                     const int32_t* row_ids, int num_rows, float decay,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- evict
+ * Shrinks each sequence s with more than budgets[s] cached tokens to that many, per kv head:
+ * entries whose original position is below `sinks` or among the last `recent` seen come first,
+ * then the larger accumulated weight, then the lower index (-0 equals 0; NaN last).  Kept
+ * entries past the budget move, K and V rows, weight and position, into the places freed below
+ * it, the k-th of them into the k-th place; the others stay.  The heads of a sequence keep
+ * different tokens; attention over the first new_lens[s] entries is attention over the kept
+ * ones, in any order.  Afterwards the blocks past ceil(new_lens[s] / B) are free to return
+ * (pkv_alloc_truncate), and new tokens append at index new_lens[s].
+ *   context_lens  device int32 [num_seqs], cached tokens L (<= max_context); 0: nothing to do.
+ *   budgets       device int32 [num_seqs]; negative: no limit.
+ *   positions     device int32 [num_rows][num_kv_heads][weights_stride]: original positions of
+ *                 the entries [0, tracked_lens[s]).  Entries from there on are the newest in
+ *                 order: entry j has position seen_lens[s] - L + j.  Nothing to initialise.
+ *   seen_lens     device int32 [num_seqs], tokens the sequence has had in all; NULL: L.
+ *   tracked_lens  device int32 [num_seqs], new_lens of the sequence's last pkv_evict, 0 before
+ *                 the first; NULL: zeros.
+ *   weights_out, positions_out  where the shrunk rows go: the inputs themselves (in place) or
+ *                 buffers that do not overlap them.  Weights from new_lens[s] to L become 0;
+ *                 positions_out holds new_lens[s] entries per head, the rest is not written.
+ *   new_lens      device int32 [num_seqs], written; must not be one of the input arrays.
+ *   row_ids       as above; a negative one leaves the sequence as it is (new_lens = L).
+ *   sinks, recent >= 0.  weights_stride >= max_context.
+ *   workspace     >= pkv_evict_workspace_bytes(...), 16-byte aligned, clobbered.
+ * Blocks below the budget are written: they must belong to the sequence alone
+ * (pkv_alloc_privatize; the blocks past it may be shared).  A length beyond max_context or the
+ * table, a row >= num_rows or a block id outside the pool raises PKV_ERR_OOB in the device
+ * status word; the first two leave the sequence as it is, the last skips the rows concerned. */
+size_t pkv_evict_workspace_bytes(const pkv_pool_desc* pool, int num_seqs, int max_context);
+pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, int max_context, int num_seqs,
+                     const int32_t* budgets, int sinks, int recent, const int32_t* seen_lens,
+                     const int32_t* tracked_lens, const float* weights, float* weights_out,
+                     const int32_t* positions, int32_t* positions_out, int64_t weights_stride,
+                     const int32_t* row_ids, int num_rows, int32_t* new_lens, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- device status
  * Synchronises `stream`, returns in *status_out the first error any kernel of this
  * library raised on the current device since the last read (PKV_OK if none), and
@@ -407,6 +556,19 @@ pkv_status pkv_alloc_block_table(const pkv_alloc* a, const int64_t* seq_ids, int
  * not allocated or num_shared exceeds the blocks num_tokens needs. */
 pkv_status pkv_alloc_add_seq_shared(pkv_alloc* a, int64_t seq_id, const int32_t* shared_blocks,
                                     int num_shared, int64_t num_tokens);
+
+/* Copy-on-write ahead of writes into seq_id's first num_tokens tokens (an eviction moves rows
+ * into them): each of their blocks that others reference is replaced by a private one, and the
+ * pair (old, new) written to cow_pairs_out[2 i .. 2 i + 1], *num_cow_out pairs in all, for
+ * pkv_copy_blocks.  PKV_ERR_INVALID if num_tokens is negative or more than seq_id holds, or
+ * more than max_pairs pairs are needed; PKV_ERR_NOMEM without enough free blocks; neither
+ * changes anything. */
+pkv_status pkv_alloc_privatize(pkv_alloc* a, int64_t seq_id, int64_t num_tokens,
+                               int32_t* cow_pairs_out, int max_pairs, int* num_cow_out);
+
+/* seq_id holds its first num_tokens (0 .. its length) tokens from now on; the blocks past
+ * ceil(num_tokens / B) lose its reference. */
+pkv_status pkv_alloc_truncate(pkv_alloc* a, int64_t seq_id, int64_t num_tokens);
 
 int64_t pkv_alloc_num_free(const pkv_alloc* a);
 int pkv_alloc_refcount(const pkv_alloc* a, int64_t block);            /* -1 if out of range */

@@ -54,6 +54,12 @@ class StepLayout(ctypes.Structure):
                 ("bytes", ctypes.c_uint64)]
 
 
+class RopeScaling(ctypes.Structure):
+    """How rotary frequencies are scaled (pkv_rope_scaling)."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original_context", ctypes.c_double)]
+
+
 _lib = None
 
 
@@ -146,6 +152,34 @@ def _load():
     lib.pkv_paged_decode_cascade.argtypes = [P(PoolDesc), vp, vp, vp, vp, vp, ctypes.c_int, vp,
                                              ctypes.c_int, vp, ctypes.c_int, ctypes.c_int,
                                              ctypes.c_int, f32, ctypes.c_int, vp, sz, vp]
+    ci = ctypes.c_int
+    lib.pkv_rope_frequencies.restype = ci
+    lib.pkv_rope_frequencies.argtypes = [P(ctypes.c_double), P(f32), ci, ctypes.c_double,
+                                         P(RopeScaling)]
+    lib.pkv_rope.restype = ci
+    lib.pkv_rope.argtypes = [ci, vp, i64, vp, i64, vp, vp, ci, ci, ci, f32, i64, ci, ci, vp]
+    lib.pkv_rope_append.restype = ci
+    lib.pkv_rope_append.argtypes = [P(PoolDesc), vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64,
+                                    vp, vp, ci, ci, f32, i64, ci, vp]
+    lib.pkv_paged_decode_weights_workspace_bytes.restype = sz
+    lib.pkv_paged_decode_weights_workspace_bytes.argtypes = [P(PoolDesc)] + [ci] * 4
+    lib.pkv_paged_decode_weights.restype = ci
+    lib.pkv_paged_decode_weights.argtypes = [P(PoolDesc), vp, vp, vp, vp, vp, vp, vp, ci, vp, ci,
+                                             ci, ci, f32, ci, vp, i64, vp, ci, f32, vp, sz, vp]
+    lib.pkv_paged_prefill_weights_workspace_bytes.restype = sz
+    lib.pkv_paged_prefill_weights_workspace_bytes.argtypes = [P(PoolDesc)] + [ci] * 5
+    lib.pkv_paged_prefill_weights.restype = ci
+    lib.pkv_paged_prefill_weights.argtypes = [P(PoolDesc), vp, vp, vp, ci, vp, vp, vp, ci, ci, ci,
+                                              ci, ci, f32, ci, vp, i64, vp, ci, f32, vp, sz, vp]
+    lib.pkv_evict_workspace_bytes.restype = sz
+    lib.pkv_evict_workspace_bytes.argtypes = [P(PoolDesc), ci, ci]
+    lib.pkv_evict.restype = ci
+    lib.pkv_evict.argtypes = [P(PoolDesc), vp, vp, vp, ci, vp, ci, ci, vp, ci, ci, vp, vp, vp, vp,
+                              vp, vp, i64, vp, ci, vp, vp, sz, vp]
+    lib.pkv_alloc_privatize.restype = ci
+    lib.pkv_alloc_privatize.argtypes = [vp, i64, i64, P(i32), ci, P(ci)]
+    lib.pkv_alloc_truncate.restype = ci
+    lib.pkv_alloc_truncate.argtypes = [vp, i64, i64]
     u64 = ctypes.c_uint64
     lib.pkv_block_hash.restype = u64
     lib.pkv_block_hash.argtypes = [u64, u64, P(i32), ctypes.c_int, u64]
@@ -522,6 +556,289 @@ def paged_prefill(q, k_pool, v_pool, block_tables, cached_lens, new_lens, q_offs
     return out
 
 
+def _arg(t: torch.Tensor, name: str, dev, dtype, shape) -> int:
+    """Address of a contiguous tensor that must be of this device, dtype and shape."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}, the pools' and current device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dev, dtype, shape):
+    return None if t is None else _arg(t, name, dev, dtype, shape)
+
+
+def _rows_arg(t: torch.Tensor, name: str, dev, dtype, shape):
+    """(address, token stride) of [tokens, heads, head_dim] rows whose tokens may be apart
+    (a slice of a fused projection)."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}, the current device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    tokens, heads, dim = shape
+    st = t.stride()
+    if tokens == 0 or heads == 0:
+        return t.data_ptr(), heads * dim
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (st[0] if tokens > 1 else heads * dim)
+
+
+def _device(t: torch.Tensor, name: str):
+    """The CUDA device of the call: `t`'s, which must be the current one (the library's
+    streams and status word are the current device's)."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, not on the current device")
+    return dev
+
+
+def _fresh(shape, dtype, dev, stream):
+    """A tensor the call writes, allocated on the stream that will use it, so that its memory
+    is not handed on while that stream still works in it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace_arg(ws, need, dev, stream):
+    """(tensor, address, bytes) of the given workspace, or of one made here."""
+    if ws is None:
+        ws = _fresh((max(need(), 16),), torch.uint8, dev, stream)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _pools(k_pool, v_pool):
+    """(descriptor, device, K address, V address) of a pair of pools."""
+    if k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    dev = _device(k_pool, "k_pool")
+    shape = k_pool.shape
+    return (pool_desc(k_pool), dev, _arg(k_pool, "k_pool", dev, k_pool.dtype, shape),
+            _arg(v_pool, "v_pool", dev, k_pool.dtype, shape))
+
+
+def _weights_arg(weights, dev, dtype, hkv, name="weights"):
+    """(address, rows, stride) of a [rows, Hkv, stride] array."""
+    if weights.dim() != 3 or weights.shape[1] != hkv:
+        raise ValueError(f"{name} must be [num_rows, num_kv_heads, stride]")
+    return _arg(weights, name, dev, dtype, weights.shape), weights.shape[0], weights.shape[2]
+
+
+ROPE_KINDS = {None: 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+
+
+def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, low=None, high=None,
+                     original_context=0, device="cuda"):
+    """Rotary frequencies (float64 [rotary_dim / 2] on `device`) and the attention scale that
+    goes with them.  `scaling`: None, "linear", "ntk", "llama3" (low 1, high 4 unless given) or
+    "yarn" (low 1, high 32), the last two over a trained context of `original_context`."""
+    if scaling not in ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {list(ROPE_KINDS)}")
+    sc = RopeScaling(ROPE_KINDS[scaling], float(factor), float(1 if low is None else low),
+                     float((32 if scaling == "yarn" else 4) if high is None else high),
+                     float(original_context))
+    out = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    scale = ctypes.c_float(1.0)
+    _check("pkv_rope_frequencies", _load().pkv_rope_frequencies(
+        ctypes.cast(out.data_ptr(), ctypes.POINTER(ctypes.c_double)), ctypes.byref(scale),
+        int(rotary_dim), float(theta), ctypes.byref(sc)))
+    return out.to(device), scale.value
+
+
+def rope(x, positions, inv_freq, *, interleaved=False, inverse=False, attn_scale=1.0, out=None,
+         stream=None):
+    """Rows x [T, H, D] turned by their token's position (int32 [T]); returns out (a new
+    contiguous tensor, or the one given, which may be x itself).
+
+    The first 2 * len(inv_freq) elements of a row turn (inv_freq float64, radians per
+    position: rope_frequencies).  x may be a slice of a fused projection: its tokens any
+    multiple of 16 bytes apart.  `inverse` turns the other way: it undoes the turn, and takes
+    a gradient with respect to the output to one with respect to x.
+    """
+    dev = _device(x, "x")
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError("x must be [tokens, heads, head_dim]")
+    T, H, D = shape
+    xp, xs = _rows_arg(x, "x", dev, x.dtype, shape)
+    if out is None:
+        out = _fresh(shape, x.dtype, dev, stream)
+    op, os_ = _rows_arg(out, "out", dev, x.dtype, shape)
+    half = inv_freq.numel()
+    st = _load().pkv_rope(_dtype_code(x), op, os_, xp, xs,
+                          _arg(positions, "positions", dev, torch.int32, (T,)),
+                          _arg(inv_freq, "inv_freq", dev, torch.float64, (half,)), 2 * half,
+                          bool(interleaved), bool(inverse), attn_scale, T, H, D, _stream(stream))
+    if st != 0:
+        raise PkvError("pkv_rope", st)
+    return out
+
+
+def rope_append(q, k, v, k_pool, v_pool, slot_mapping, positions, inv_freq, *, interleaved=False,
+                attn_scale=1.0, q_out=None, stream=None):
+    """One launch for a step's new tokens: q [T, Hq, D] turned into q_out (returned), k [T, Hkv,
+    D] turned and v [T, Hkv, D] as it is stored into their pool slots (slot < 0 = skip).
+    Arguments as rope and kv_append; q, k and v may be slices of one fused projection."""
+    d, dev, kp, vp_ = _pools(k_pool, v_pool)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    T, Hq, _ = q.shape
+    dt, D = k_pool.dtype, d.head_dim
+    qp, qs = _rows_arg(q, "q", dev, dt, (T, Hq, D))
+    kr, ks = _rows_arg(k, "k", dev, dt, (T, d.num_kv_heads, D))
+    vr, vs = _rows_arg(v, "v", dev, dt, (T, d.num_kv_heads, D))
+    if q_out is None:
+        q_out = _fresh((T, Hq, D), dt, dev, stream)
+    op, os_ = _rows_arg(q_out, "q_out", dev, dt, (T, Hq, D))
+    half = inv_freq.numel()
+    st = _load().pkv_rope_append(ctypes.byref(d), kp, vp_,
+                                 _arg(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), op,
+                                 os_, qp, qs, kr, ks, vr, vs,
+                                 _arg(positions, "positions", dev, torch.int32, (T,)),
+                                 _arg(inv_freq, "inv_freq", dev, torch.float64, (half,)),
+                                 2 * half, bool(interleaved), attn_scale, T, Hq, _stream(stream))
+    if st != 0:
+        raise PkvError("pkv_rope_append", st)
+    return q_out
+
+
+def decode_weights_workspace_bytes(k_pool, num_seqs, num_q_heads, max_context,
+                                   partition_blocks=0) -> int:
+    """Workspace of paged_decode_weights (partials, and every score: 4 bytes per query head
+    and token)."""
+    return int(_load().pkv_paged_decode_weights_workspace_bytes(
+        ctypes.byref(pool_desc(k_pool)), num_seqs, num_q_heads, max_context, partition_blocks))
+
+
+def paged_decode_weights(q, k_pool, v_pool, block_tables, context_lens, scale, weights, *,
+                         max_context, k_new=None, v_new=None, row_ids=None, decay=1.0, out=None,
+                         partition_blocks=0, workspace=None, stream=None):
+    """paged_decode (or, with k_new / v_new [S, Hkv, D], paged_decode_append) that also adds up
+    the attention each cached token receives: weights [rows, Hkv, stride] (fp32, in place)
+    becomes decay * weights + the probabilities summed over the kv head's query heads, in row
+    row_ids[s] (default s; negative: not counted).  Returns out [S, Hq, D]."""
+    d, dev, kp, vp_ = _pools(k_pool, v_pool)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [num_seqs, heads, head_dim], block_tables [num_seqs, blocks]")
+    S, Hq, _ = q.shape
+    dt, D, Hkv = k_pool.dtype, d.head_dim, d.num_kv_heads
+    if out is None:
+        out = _fresh((S, Hq, D), dt, dev, stream)
+    wp, rows, stride = _weights_arg(weights, dev, torch.float32, Hkv)
+    _, ws, wsb = _keep = _workspace_arg(
+        workspace, lambda: decode_weights_workspace_bytes(k_pool, S, Hq, max_context,
+                                                          partition_blocks), dev, stream)
+    st = _load().pkv_paged_decode_weights(
+        ctypes.byref(d), _arg(out, "out", dev, dt, (S, Hq, D)), _arg(q, "q", dev, dt, (S, Hq, D)),
+        kp, vp_, _opt(k_new, "k_new", dev, dt, (S, Hkv, D)),
+        _opt(v_new, "v_new", dev, dt, (S, Hkv, D)),
+        _arg(block_tables, "block_tables", dev, torch.int32, (S, block_tables.shape[1])),
+        block_tables.shape[1], _arg(context_lens, "context_lens", dev, torch.int32, (S,)),
+        max_context, S, Hq, scale, partition_blocks, wp, stride,
+        _opt(row_ids, "row_ids", dev, torch.int32, (S,)), rows, decay, ws, wsb, _stream(stream))
+    if st != 0:
+        raise PkvError("pkv_paged_decode_weights", st)
+    return out
+
+
+def prefill_weights_workspace_bytes(k_pool, num_reqs, num_q_heads, max_new, max_context,
+                                    window=0) -> int:
+    """Workspace of paged_prefill_weights (the query rows' softmax statistics)."""
+    return int(_load().pkv_paged_prefill_weights_workspace_bytes(
+        ctypes.byref(pool_desc(k_pool)), num_reqs, num_q_heads, max_new, max_context, window))
+
+
+def paged_prefill_weights(q, k_pool, block_tables, cached_lens, new_lens, q_offsets, scale,
+                          weights, *, max_new, max_context, window=0, row_ids=None, decay=1.0,
+                          workspace=None, stream=None):
+    """The attention that each cached token receives from the last `window` new tokens of its
+    request (0: all of them), added to weights [rows, Hkv, stride] (fp32, in place) as
+    paged_decode_weights does; q and the lengths as paged_prefill.  Returns weights."""
+    if k_pool.dim() != 4 or q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [tokens, heads, head_dim], block_tables [num_reqs, blocks], "
+                         "k_pool [num_blocks, num_kv_heads, block_size, head_dim]")
+    dev = _device(k_pool, "k_pool")
+    d = pool_desc(k_pool)
+    N, Hq, _ = q.shape
+    R = block_tables.shape[0]
+    dt = k_pool.dtype
+    wp, rows, stride = _weights_arg(weights, dev, torch.float32, d.num_kv_heads)
+    _, ws, wsb = _keep = _workspace_arg(
+        workspace, lambda: prefill_weights_workspace_bytes(k_pool, R, Hq, max_new, max_context,
+                                                           window), dev, stream)
+    st = _load().pkv_paged_prefill_weights(
+        ctypes.byref(d), _arg(q, "q", dev, dt, (N, Hq, d.head_dim)),
+        _arg(k_pool, "k_pool", dev, dt, k_pool.shape),
+        _arg(block_tables, "block_tables", dev, torch.int32, block_tables.shape),
+        block_tables.shape[1], _arg(cached_lens, "cached_lens", dev, torch.int32, (R,)),
+        _arg(new_lens, "new_lens", dev, torch.int32, (R,)),
+        _arg(q_offsets, "q_offsets", dev, torch.int32, (R + 1,)), R, N, max_new, max_context, Hq,
+        scale, window, wp, stride, _opt(row_ids, "row_ids", dev, torch.int32, (R,)), rows, decay,
+        ws, wsb, _stream(stream))
+    if st != 0:
+        raise PkvError("pkv_paged_prefill_weights", st)
+    return weights
+
+
+def evict_workspace_bytes(k_pool, num_seqs, max_context) -> int:
+    return int(_load().pkv_evict_workspace_bytes(ctypes.byref(pool_desc(k_pool)), num_seqs,
+                                                 max_context))
+
+
+def evict(k_pool, v_pool, block_tables, context_lens, budgets, weights, positions, *, max_context,
+          sinks=0, recent=0, seen_lens=None, tracked_lens=None, row_ids=None, weights_out=None,
+          positions_out=None, new_lens=None, workspace=None, stream=None):
+    """Shrink sequences with more than budgets[s] cached tokens to that many per kv head:
+    the first `sinks` and last `recent` positions are kept, then the largest weights (ties:
+    lowest index); kept rows past the budget move into the freed places below it.
+
+    weights (fp32) and positions (int32), [rows, Hkv, stride], shrink along: in place, or into
+    weights_out / positions_out.  seen_lens: tokens each sequence has had in all (default
+    context_lens); tracked_lens: the new_lens of its last eviction (default zeros).  Returns
+    new_lens (int32 [S]).  The blocks below a budget must be the sequence's own
+    (BlockAllocator.privatize); those past it can go back (BlockAllocator.truncate)."""
+    d, dev, kp, vp_ = _pools(k_pool, v_pool)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, blocks]")
+    S = block_tables.shape[0]
+    i32, one = torch.int32, (S,)
+    wp, rows, stride = _weights_arg(weights, dev, torch.float32, d.num_kv_heads)
+    pp = _arg(positions, "positions", dev, i32, weights.shape)
+    wo = wp if weights_out is None else _arg(weights_out, "weights_out", dev, torch.float32,
+                                             weights.shape)
+    po = pp if positions_out is None else _arg(positions_out, "positions_out", dev, i32,
+                                               weights.shape)
+    if new_lens is None:
+        new_lens = _fresh(one, i32, dev, stream)
+    _, ws, wsb = _keep = _workspace_arg(
+        workspace, lambda: evict_workspace_bytes(k_pool, S, max_context), dev, stream)
+    st = _load().pkv_evict(
+        ctypes.byref(d), kp, vp_, _arg(block_tables, "block_tables", dev, i32, block_tables.shape),
+        block_tables.shape[1], _arg(context_lens, "context_lens", dev, i32, one), max_context, S,
+        _arg(budgets, "budgets", dev, i32, one), sinks, recent,
+        _opt(seen_lens, "seen_lens", dev, i32, one),
+        _opt(tracked_lens, "tracked_lens", dev, i32, one), wp, wo, pp, po, stride,
+        _opt(row_ids, "row_ids", dev, i32, one), rows, _arg(new_lens, "new_lens", dev, i32, one),
+        ws, wsb, _stream(stream))
+    if st != 0:
+        raise PkvError("pkv_evict", st)
+    return new_lens
+
+
 def copy_blocks(k_pool, v_pool, pairs, stream=None) -> None:
     """pool[dst] = pool[src] for each row (src, dst) of int32 pairs [P, 2]."""
     d = pool_desc(k_pool)
@@ -582,6 +899,20 @@ class BlockAllocator:
         _check("pkv_alloc_append", self._lib.pkv_alloc_append(self._h, seq_id, n, slots, pairs,
                                                               ctypes.byref(ncow)))
         return list(slots[:n]), ((pairs[0], pairs[1]) if ncow.value else None)
+
+    def privatize(self, seq_id: int, num_tokens: int):
+        """Private copies of the blocks of the first num_tokens tokens that others reference;
+        returns the (old, new) pairs for copy_blocks."""
+        most = max(-(-num_tokens // self.block_size), 0)
+        pairs = (ctypes.c_int32 * max(2 * most, 1))()
+        n = ctypes.c_int(0)
+        _check("pkv_alloc_privatize", self._lib.pkv_alloc_privatize(self._h, seq_id, num_tokens,
+                                                                    pairs, most, ctypes.byref(n)))
+        return [(pairs[2 * i], pairs[2 * i + 1]) for i in range(n.value)]
+
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """Keep the sequence's first num_tokens tokens; blocks past them lose its reference."""
+        _check("pkv_alloc_truncate", self._lib.pkv_alloc_truncate(self._h, seq_id, num_tokens))
 
     def free_seq(self, seq_id: int) -> None:
         _check("pkv_alloc_free_seq", self._lib.pkv_alloc_free_seq(self._h, seq_id))

@@ -165,6 +165,48 @@ pkv_status pkv_alloc_block_table(const pkv_alloc* a, const int64_t* seq_ids, int
     return PKV_OK;
 }
 
+pkv_status pkv_alloc_privatize(pkv_alloc* a, int64_t seq_id, int64_t num_tokens,
+                               int32_t* cow_pairs_out, int max_pairs, int* num_cow_out) {
+    if (!a || num_tokens < 0 || max_pairs < 0 || !num_cow_out || (max_pairs > 0 && !cow_pairs_out))
+        return PKV_ERR_INVALID;
+    auto it = a->seqs.find(seq_id);
+    if (it == a->seqs.end()) return PKV_ERR_NOT_FOUND;
+    pkv_alloc::Seq& s = it->second;
+    *num_cow_out = 0;
+    if (num_tokens > s.num_tokens) return PKV_ERR_INVALID;
+    const int64_t n = blocks_for(num_tokens, a->block_size);
+    int64_t shared = 0;
+    for (int64_t i = 0; i < n; ++i) shared += a->refcount[s.blocks[static_cast<size_t>(i)]] > 1;
+    if (shared > max_pairs) return PKV_ERR_INVALID;
+    if (shared > static_cast<int64_t>(a->free_list.size())) return PKV_ERR_NOMEM;
+    for (int64_t i = 0; i < n; ++i) {
+        int32_t& b = s.blocks[static_cast<size_t>(i)];
+        if (a->refcount[b] <= 1) continue;
+        const int32_t mine = a->take();
+        a->release(b);
+        cow_pairs_out[2 * *num_cow_out] = b;
+        cow_pairs_out[2 * *num_cow_out + 1] = mine;
+        ++*num_cow_out;
+        b = mine;
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_alloc_truncate(pkv_alloc* a, int64_t seq_id, int64_t num_tokens) {
+    if (!a || num_tokens < 0) return PKV_ERR_INVALID;
+    auto it = a->seqs.find(seq_id);
+    if (it == a->seqs.end()) return PKV_ERR_NOT_FOUND;
+    pkv_alloc::Seq& s = it->second;
+    if (num_tokens > s.num_tokens) return PKV_ERR_INVALID;
+    const size_t n = static_cast<size_t>(blocks_for(num_tokens, a->block_size));
+    while (s.blocks.size() > n) {
+        a->release(s.blocks.back());
+        s.blocks.pop_back();
+    }
+    s.num_tokens = num_tokens;
+    return PKV_OK;
+}
+
 int64_t pkv_alloc_num_free(const pkv_alloc* a) {
     return a ? static_cast<int64_t>(a->free_list.size()) : -1;
 }

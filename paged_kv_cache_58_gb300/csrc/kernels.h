@@ -83,6 +83,18 @@ struct DecodeArgs {
     // the append has not reached yet).
     const void* k_new;
     const void* v_new;
+    // Accumulated attention weights (pkv_paged_decode_weights): non-null `scores` makes
+    // the split kernels keep every score, scale * log2(e) * q.k, in
+    // scores[S][Hkv][score_tokens][G] and every partition's m / l (also where there is
+    // one partition), from which the finishing launch adds each cached token's weight to
+    // weights[row][kvh][token].
+    float* scores;
+    int score_tokens;         // tokens per (sequence, kv head) in `scores`
+    float* weights;
+    const int32_t* row_ids;   // weight row of each sequence (null: its index)
+    int64_t weights_stride;   // floats between the rows of two kv heads
+    int num_rows;
+    float decay;
 };
 
 #ifdef __CUDACC__
@@ -105,6 +117,10 @@ cudaError_t launch_paged_decode(const DecodeArgs& a, int dtype, int head_dim, in
 // Tensor-core decode for bf16 pools (warp-level MMA): split kernel + combine.
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int head_dim, int group,
                                    cudaStream_t stream);
+// Log-sum-exp merge of the split-KV partials into `out`, and, beside it in the same
+// launch, the accumulated attention weights (a.scores set).
+cudaError_t launch_decode_finish(const DecodeArgs& a, int dtype, int head_dim, int group,
+                                 cudaStream_t stream);
 // Log-sum-exp merge of the split-KV partials into `out`.
 cudaError_t launch_decode_combine(const DecodeArgs& a, int dtype, int head_dim,
                                   cudaStream_t stream);
@@ -171,5 +187,95 @@ struct PrefillArgs {
 };
 
 cudaError_t launch_paged_prefill(const PrefillArgs& a, int group, cudaStream_t stream);
+
+// Rotary positions of q rows (k_pool null), or of q and k rows with k and v stored into
+// their pool slots.  Strides are elements per token.
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_pool;
+    void* v_pool;
+    const int64_t* slot_mapping;
+    const int32_t* positions;
+    const double* inv_freq;   // [rotary_dim / 2], radians per position
+    int* status;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    int64_t num_tokens;
+    int64_t num_slots;
+    int num_q_heads;
+    int num_kv_heads;
+    int rotary_dim;    // a multiple of 16, at most the head dim
+    int block_shift;   // log2(block_size)
+    int interleaved;
+    int inverse;
+    float attn_scale;
+};
+cudaError_t launch_rope(const RopeArgs& a, int dtype, int head_dim, cudaStream_t stream);
+
+// Accumulated attention weights of the requests' last `window` new tokens.
+struct PrefillWeightsArgs {
+    const void* q;
+    const void* k_pool;
+    const int32_t* block_tables;
+    const int32_t* cached_lens;
+    const int32_t* new_lens;
+    const int32_t* q_offsets;
+    const int32_t* row_ids;   // weight row of each request (null: its index)
+    float* weights;           // [num_rows][Hkv][weights_stride]
+    float2* stats;            // workspace: (max, sum) [R][Hkv][splits][rows_pad]
+    int* status;
+    int64_t num_blocks;
+    int64_t weights_stride;
+    int num_rows;
+    int max_blocks_per_seq;
+    int block_shift;
+    int num_reqs;
+    int total_new;
+    int max_new;
+    int max_rows;      // tokens that count per request at most: max_new, or the window
+    int max_context;
+    int num_q_heads;
+    int num_kv_heads;
+    int window;        // 0: every new token
+    int splits;        // parts the keys of a query tile are split into in pass 1
+    int rows_pad;      // rows of one (request, kv head, split) in `stats`
+    float scale_log2;
+    float decay;
+};
+cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int dtype, int head_dim, int group,
+                                   cudaStream_t stream);
+
+// Eviction by accumulated weight.
+struct EvictArgs {
+    void* k_pool;
+    void* v_pool;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* budgets;
+    const int32_t* seen_lens;      // null: context_lens
+    const int32_t* tracked_lens;   // null: zeros
+    const int32_t* row_ids;        // null: the sequence's index
+    const float* weights;
+    float* weights_out;
+    const int32_t* positions;
+    int32_t* positions_out;
+    int32_t* new_lens;
+    int32_t* moves;   // workspace: [S][Hkv][max_context]
+    int* status;
+    int64_t num_blocks;
+    int64_t weights_stride;
+    int num_rows;
+    int max_blocks_per_seq;
+    int block_shift;
+    int max_context;
+    int num_seqs;
+    int num_kv_heads;
+    int row_bytes;
+    int sinks;
+    int recent;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace pkv

@@ -156,7 +156,8 @@ struct DecodeSmem {
     static constexpr int kTotal = kRing + kMergeAcc + kMergeML + kBars;
 };
 
-template <typename T, int D, int G>
+// W: keep the scores and the partitions' m / l for the accumulated attention weights.
+template <typename T, int D, int G, bool W>
 __global__ void __launch_bounds__(kThreads)
 decode_split_kernel(const DecodeArgs a) {
     using SM = DecodeSmem<T, D, G>;
@@ -315,6 +316,12 @@ decode_split_kernel(const DecodeArgs a) {
             }
             const float full = reduce_scatter16<G>(part_, lane);
             sc[r] = (row < valid) ? full : -INFINITY;
+            if constexpr (W) {   // lane c holds head c / kHeadStride: its first lane stores
+                if (row < valid && c % kHeadStride == 0)
+                    a.scores[((static_cast<size_t>(seq) * a.num_kv_heads + kvh) * a.score_tokens +
+                              static_cast<size_t>(blk) * kBlock + row) * G + c / kHeadStride] =
+                        full;
+            }
         }
 
         float bmax = sc[0];
@@ -405,6 +412,10 @@ decode_split_kernel(const DecodeArgs a) {
         const size_t row = qrow * hq + h;
         if (nparts == 1) {
             store_elem<T>(static_cast<T*>(a.out) + row * D + d, o / l);
+            if (W && d == 0) {
+                a.m_part[row] = M;
+                a.l_part[row] = l;
+            }
         } else {
             const size_t pr = row * nparts + a.extra_parts + part;
             a.o_part[pr * D + d] = o / l;
@@ -424,14 +435,8 @@ decode_split_kernel(const DecodeArgs a) {
 constexpr int kCombineWarps = 4;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCombineWarps * 32)
-decode_combine_kernel(const DecodeArgs a) {
-    griddep_wait();
-    griddep_launch_dependents();
+PKV_DEVINL void combine_row(const DecodeArgs& a, size_t row, int lane) {
     constexpr int EL = D / 32;  // 4 (D 128) or 2 (D 64) elements per lane
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const size_t row = static_cast<size_t>(blockIdx.x) * kCombineWarps + warp;  // seq*Hq + h
     if (row >= static_cast<size_t>(a.num_seqs) * a.num_q_heads) return;
     const int seq = static_cast<int>(row / a.num_q_heads);
     const int L = min(a.context_lens[seq], (a.max_blocks_per_seq << a.chunk_shift) * kBlock);
@@ -510,10 +515,117 @@ decode_combine_kernel(const DecodeArgs a) {
     for (int e = 0; e < EL; ++e) store_elem<T>(dst + e, acc[e] * inv);
 }
 
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineWarps * 32)
+decode_combine_kernel(const DecodeArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    combine_row<T, D>(a, static_cast<size_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5),
+                      threadIdx.x & 31);
+}
+
+// The finishing launch of a decode with accumulated attention weights.  CTAs [0,
+// combine_ctas) merge partitions as decode_combine_kernel does; each CTA after them takes
+// kWeightTile tokens of one (sequence, kv head): it merges the partitions' (m, l) of the
+// G query heads into their softmax statistics, M and 1 / sum, and adds
+//   weights[row][kvh][j] = decay * weights + sum_g 2^(s_gj - M_g) / sum_g
+// from the scores the split kernel kept (mostly still in L2).  One thread owns a token,
+// so no two threads add to the same weight and the sum's order is fixed.
+constexpr int kWeightTile = 512;
+
+// The G scores of a token, in the widest loads their alignment (4 G bytes) allows.
+template <int G>
+PKV_DEVINL void load_scores(const float* p, float (&s)[G]) {
+    if constexpr (G == 1) {
+        s[0] = *p;
+    } else if constexpr (G == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(p);
+        s[0] = f.x; s[1] = f.y;
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; g += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(p + g);
+            s[g] = f.x; s[g + 1] = f.y; s[g + 2] = f.z; s[g + 3] = f.w;
+        }
+    }
+}
+
 template <typename T, int D, int G>
+__global__ void __launch_bounds__(kCombineWarps * 32)
+decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int tiles) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (static_cast<int>(blockIdx.x) < combine_ctas) {
+        combine_row<T, D>(a, static_cast<size_t>(blockIdx.x) * kCombineWarps + warp, lane);
+        return;
+    }
+    constexpr int kThr = kCombineWarps * 32;
+    constexpr int PER = kWeightTile / kThr;
+    __shared__ float coef[2][G];
+    int idx = static_cast<int>(blockIdx.x) - combine_ctas;
+    const int tile = idx % tiles;
+    idx /= tiles;
+    const int kvh = idx % a.num_kv_heads;
+    const int seq = idx / a.num_kv_heads;
+    int L = min(__ldg(a.context_lens + seq), a.score_tokens);
+    L = min(L, (a.max_blocks_per_seq << a.chunk_shift) * kBlock);
+    const int row = a.row_ids ? __ldg(a.row_ids + seq) : seq;
+    const int j0 = tile * kWeightTile;
+    if (row < 0 || j0 >= L) return;   // a padding row, or past the sequence
+    if (row >= a.num_rows || L > a.weights_stride) {
+        if (threadIdx.x == 0) raise_status(a.status, PKV_ERR_OOB);
+        if (row >= a.num_rows) return;
+        L = static_cast<int>(min(static_cast<int64_t>(L), a.weights_stride));
+    }
+    const float* sp = a.scores + (static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
+                                     a.score_tokens * G;
+    float* wp = a.weights + (static_cast<size_t>(row) * a.num_kv_heads + kvh) *
+                                static_cast<size_t>(a.weights_stride);
+    float s[PER][G], w[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {   // loaded beside the statistics
+        const int j = j0 + u * kThr + threadIdx.x;
+        w[u] = (j < L && a.decay != 0.f) ? wp[j] : 0.f;
+        if (j < L) load_scores<G>(sp + static_cast<size_t>(j) * G, s[u]);
+    }
+    const int total = a.max_parts;
+    const int nchunks = (L + kBlock - 1) / kBlock;
+    const int np = min(total, (nchunks + a.partition_chunks - 1) / a.partition_chunks);
+    for (int g = warp; g < G; g += kCombineWarps) {
+        const size_t r = static_cast<size_t>(seq) * a.num_q_heads + kvh * G + g;
+        const float* mp = a.m_part + r * total;
+        const float* lp = a.l_part + r * total;
+        float M = -INFINITY;
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, mp[p]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float W = 0.f;
+        for (int p = lane; p < np; p += 32) W += lp[p] * fast_exp2(mp[p] - M);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+        if (lane == 0) {
+            coef[0][g] = M;
+            coef[1][g] = 1.f / W;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int j = j0 + u * kThr + threadIdx.x;
+        if (j >= L) continue;
+        float p = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) p = fmaf(fast_exp2(s[u][g] - coef[0][g]), coef[1][g], p);
+        wp[j] = a.decay != 0.f ? fmaf(a.decay, w[u], p) : p;
+    }
+}
+
+template <typename T, int D, int G, bool W>
 cudaError_t launch_typed(const DecodeArgs& a, cudaStream_t stream) {
     using SM = DecodeSmem<T, D, G>;
-    auto kern = decode_split_kernel<T, D, G>;
+    auto kern = decode_split_kernel<T, D, G, W>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), SM::kTotal);
     if (e != cudaSuccess) return e;
     if (a.max_parts > 0) {   // zero when a cascade decode has no private suffix at all
@@ -521,6 +633,8 @@ cudaError_t launch_typed(const DecodeArgs& a, cudaStream_t stream) {
         e = launch_maybe_pdl(!a.no_pdl, kern, grid, dim3(kThreads), SM::kTotal, stream, a);
         if (e != cudaSuccess) return e;
     }
+    if constexpr (W)
+        return launch_decode_finish(a, sizeof(T) == 2 ? PKV_BF16 : PKV_F32, D, G, stream);
     if (a.extra_parts == 0 && a.max_parts == 1) return e;  // output written directly
     if (a.defer_combine) return e;
     return launch_decode_combine(a, sizeof(T) == 2 ? PKV_BF16 : PKV_F32, D, stream);
@@ -534,15 +648,50 @@ cudaError_t launch_combine_typed(const DecodeArgs& a, cudaStream_t stream) {
                       stream, a);
 }
 
+template <typename T, int D, int G>
+cudaError_t launch_finish_typed(const DecodeArgs& a, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+    // one partition: the split kernel has written the output, no merge is left
+    const int64_t combine = a.max_parts > 1 ? (rows + kCombineWarps - 1) / kCombineWarps : 0;
+    const int tiles = (a.score_tokens + kWeightTile - 1) / kWeightTile;
+    const int64_t grid = combine + static_cast<int64_t>(tiles) * a.num_kv_heads * a.num_seqs;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_pdl(decode_finish_kernel<T, D, G>, dim3(static_cast<unsigned>(grid)),
+                      dim3(kCombineWarps * 32), 0, stream, a, static_cast<int>(combine), tiles);
+}
+
 template <typename T, int D>
-cudaError_t launch_group(const DecodeArgs& a, int G, cudaStream_t stream) {
+cudaError_t launch_finish_group(const DecodeArgs& a, int G, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_typed<T, D, 1>(a, stream);
-        case 2: return launch_typed<T, D, 2>(a, stream);
-        case 4: return launch_typed<T, D, 4>(a, stream);
-        case 8: return launch_typed<T, D, 8>(a, stream);
+        case 1: return launch_finish_typed<T, D, 1>(a, stream);
+        case 2: return launch_finish_typed<T, D, 2>(a, stream);
+        case 4: return launch_finish_typed<T, D, 4>(a, stream);
+        case 8: return launch_finish_typed<T, D, 8>(a, stream);
         default: return cudaErrorInvalidValue;
     }
+}
+
+template <typename T, int D, bool W>
+cudaError_t launch_group(const DecodeArgs& a, int G, cudaStream_t stream) {
+    switch (G) {
+        case 1: return launch_typed<T, D, 1, W>(a, stream);
+        case 2: return launch_typed<T, D, 2, W>(a, stream);
+        case 4: return launch_typed<T, D, 4, W>(a, stream);
+        case 8: return launch_typed<T, D, 8, W>(a, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T>
+cudaError_t launch_dim(const DecodeArgs& a, int head_dim, int G, cudaStream_t stream) {
+    const bool w = a.scores != nullptr;
+    if (head_dim == 128)
+        return w ? launch_group<T, 128, true>(a, G, stream)
+                 : launch_group<T, 128, false>(a, G, stream);
+    if (head_dim == 64)
+        return w ? launch_group<T, 64, true>(a, G, stream)
+                 : launch_group<T, 64, false>(a, G, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -559,15 +708,22 @@ cudaError_t launch_decode_combine(const DecodeArgs& a, int dtype, int head_dim,
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_decode_finish(const DecodeArgs& a, int dtype, int head_dim, int group,
+                                 cudaStream_t stream) {
+    if (dtype == PKV_BF16) {
+        if (head_dim == 128) return launch_finish_group<uint16_t, 128>(a, group, stream);
+        if (head_dim == 64) return launch_finish_group<uint16_t, 64>(a, group, stream);
+    } else if (dtype == PKV_F32) {
+        if (head_dim == 128) return launch_finish_group<float, 128>(a, group, stream);
+        if (head_dim == 64) return launch_finish_group<float, 64>(a, group, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_paged_decode(const DecodeArgs& a, int dtype, int head_dim, int group,
                                 cudaStream_t stream) {
-    if (dtype == PKV_BF16) {
-        if (head_dim == 128) return launch_group<uint16_t, 128>(a, group, stream);
-        if (head_dim == 64) return launch_group<uint16_t, 64>(a, group, stream);
-    } else if (dtype == PKV_F32) {
-        if (head_dim == 128) return launch_group<float, 128>(a, group, stream);
-        if (head_dim == 64) return launch_group<float, 64>(a, group, stream);
-    }
+    if (dtype == PKV_BF16) return launch_dim<uint16_t>(a, head_dim, group, stream);
+    if (dtype == PKV_F32) return launch_dim<float>(a, head_dim, group, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -96,7 +96,8 @@ struct TcSmem {
     static constexpr int kTotal = kRing + kBars + 1024;   // + alignment slack
 };
 
-template <int D, int G>
+// W: keep the scores and the partitions' m / l for the accumulated attention weights.
+template <int D, int G, bool W>
 __global__ void __launch_bounds__(kThreads)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const DecodeArgs a) {
@@ -309,6 +310,25 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int t = t_lo + ((e & 2) ? 8 : 0);
             s[e] = (t < valid) ? s[e] * sl2 : -INFINITY;
         }
+        if constexpr (W) {
+            // This lane's scores, tokens t_lo and t_lo + 8 of heads 2 (lane % 4) + {0, 1}:
+            // the G heads of a token lie side by side, so a chunk's scores are one run of
+            // 64 G bytes.
+            float* sp = a.scores + ((static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
+                                        a.score_tokens +
+                                    static_cast<size_t>(blk) * kBlk) * G;
+            const int hs = 2 * (lane & 3);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int t = t_lo + 4 * e;
+                if (t < valid && hs < G) {
+                    if constexpr (G >= 2)
+                        *reinterpret_cast<float2*>(sp + t * G + hs) = make_float2(s[e], s[e + 1]);
+                    else
+                        sp[t] = s[e];
+                }
+            }
+        }
         // per-head block max over the 16 tokens (lanes sharing lane % 4)
         float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
 #pragma unroll
@@ -411,6 +431,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (nparts == 1) {
             static_cast<uint16_t*>(a.out)[row * D + d] =
                 static_cast<uint16_t>(pack_bf16x2(o / l, 0.f) & 0xffffu);
+            if (W && d == 0) {
+                a.m_part[row] = M;
+                a.l_part[row] = l;
+            }
         } else {
             const size_t pr = row * nparts + a.extra_parts + part;
             a.o_part[pr * D + d] = o / l;
@@ -422,7 +446,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
 }
 
-template <int D, int G>
+template <int D, int G, bool W>
 cudaError_t launch_tc(const DecodeArgs& a, cudaStream_t stream) {
     using SM = TcSmem<D, G>;
     CUtensorMap mk, mv;
@@ -432,7 +456,7 @@ cudaError_t launch_tc(const DecodeArgs& a, cudaStream_t stream) {
                                   : make_pool_map(&mk, a.k_pool, rows, D) &&
                                         make_pool_map(&mv, a.v_pool, rows, D);
     if (!maps_ok) return cudaErrorInvalidValue;
-    auto kern = decode_tc_kernel<D, G>;
+    auto kern = decode_tc_kernel<D, G, W>;
     cudaError_t e =
         set_smem_once(reinterpret_cast<const void*>(kern), SM::kTotal);
     if (e != cudaSuccess) return e;
@@ -442,18 +466,19 @@ cudaError_t launch_tc(const DecodeArgs& a, cudaStream_t stream) {
                              a);
         if (e != cudaSuccess) return e;
     }
+    if constexpr (W) return launch_decode_finish(a, PKV_BF16, D, G, stream);
     if (a.extra_parts == 0 && a.max_parts == 1) return e;  // output written directly
     if (a.defer_combine) return e;
     return launch_decode_combine(a, PKV_BF16, D, stream);
 }
 
-template <int D>
+template <int D, bool W>
 cudaError_t launch_tc_group(const DecodeArgs& a, int G, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_tc<D, 1>(a, stream);
-        case 2: return launch_tc<D, 2>(a, stream);
-        case 4: return launch_tc<D, 4>(a, stream);
-        case 8: return launch_tc<D, 8>(a, stream);
+        case 1: return launch_tc<D, 1, W>(a, stream);
+        case 2: return launch_tc<D, 2, W>(a, stream);
+        case 4: return launch_tc<D, 4, W>(a, stream);
+        case 8: return launch_tc<D, 8, W>(a, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -462,8 +487,13 @@ cudaError_t launch_tc_group(const DecodeArgs& a, int G, cudaStream_t stream) {
 
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int head_dim, int group,
                                    cudaStream_t stream) {
-    if (head_dim == 128) return launch_tc_group<128>(a, group, stream);
-    if (head_dim == 64) return launch_tc_group<64>(a, group, stream);
+    const bool w = a.scores != nullptr;
+    if (head_dim == 128)
+        return w ? launch_tc_group<128, true>(a, group, stream)
+                 : launch_tc_group<128, false>(a, group, stream);
+    if (head_dim == 64)
+        return w ? launch_tc_group<64, true>(a, group, stream)
+                 : launch_tc_group<64, false>(a, group, stream);
     return cudaErrorInvalidValue;
 }
 

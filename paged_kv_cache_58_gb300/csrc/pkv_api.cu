@@ -270,17 +270,54 @@ size_t pkv_paged_decode_workspace_bytes(int num_seqs, int num_q_heads, int head_
 
 namespace {
 
-// pkv_paged_decode, and with k_new / v_new set pkv_paged_decode_append.
+// Where accumulated attention weights go (see pkv_paged_decode_weights).
+struct WeightsOut {
+    float* weights;
+    int64_t stride;
+    const int32_t* row_ids;
+    int num_rows;
+    float decay;
+};
+
+bool weights_ok(const WeightsOut& w, int num_seqs, int max_context) {
+    return w.weights && w.stride >= max_context && w.num_rows > 0 &&
+           (w.row_ids || w.num_rows >= num_seqs) && w.decay >= 0.f && w.decay <= 1.f &&
+           (reinterpret_cast<uintptr_t>(w.weights) & 3u) == 0;
+}
+
+size_t round16(size_t x) { return (x + 15) / 16 * 16; }
+
+// Workspace of a decode with accumulated weights: the partials' outputs (none for one
+// partition), their m and l, and every score of the partitions' span.
+struct WeightsWorkspace {
+    size_t ml_at, scores_at, bytes;
+    int score_tokens;
+};
+bool weights_workspace(int num_seqs, int num_q_heads, int head_dim, int max_parts,
+                       int partition_chunks, WeightsWorkspace* w) {
+    const int64_t span = static_cast<int64_t>(max_parts) * partition_chunks * kChunk;
+    if (span > INT32_MAX) return false;
+    const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
+    w->score_tokens = static_cast<int>(span);
+    w->ml_at = max_parts > 1 ? rows * max_parts * head_dim * sizeof(float) : 0;
+    w->scores_at = w->ml_at + 2 * round16(rows * max_parts * sizeof(float));
+    w->bytes = w->scores_at + rows * static_cast<size_t>(span) * sizeof(float);
+    return true;
+}
+
+// pkv_paged_decode; with k_new / v_new set pkv_paged_decode_append; with `wo` set
+// pkv_paged_decode_weights.
 pkv_status decode_impl(const pkv_pool_desc* pool, void* out, const void* q, const void* k_pool,
                        const void* v_pool, const int32_t* block_tables, int max_blocks_per_seq,
                        const int32_t* context_lens, int max_context, int num_seqs,
                        int num_q_heads, float scale, int partition_blocks, void* workspace,
                        size_t workspace_bytes, const void* k_new, const void* v_new,
-                       void* stream) {
+                       void* stream, const WeightsOut* wo = nullptr) {
     pkv_status st = check_pool(pool);
     if (st != PKV_OK) return st;
     if (num_seqs < 0 || num_q_heads <= 0 || partition_blocks < 0) return PKV_ERR_INVALID;
     if (num_seqs == 0) return PKV_OK;
+    if (wo && !weights_ok(*wo, num_seqs, max_context)) return PKV_ERR_INVALID;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens)
         return PKV_ERR_INVALID;
     const int B = pool->block_size;
@@ -298,7 +335,14 @@ pkv_status decode_impl(const pkv_pool_desc* pool, void* out, const void* q, cons
                                     : auto_partition(num_seqs, num_q_heads, max_context, B);
     const int max_parts = ceil_div(ceil_div(max_context, B), pb);
     if (max_parts > pkv::kMaxParts) return PKV_ERR_UNSUPPORTED;
-    const size_t need = decode_workspace(num_seqs, num_q_heads, pool->head_dim, max_parts);
+    size_t need = decode_workspace(num_seqs, num_q_heads, pool->head_dim, max_parts);
+    WeightsWorkspace ww{};
+    if (wo) {
+        if (!weights_workspace(num_seqs, num_q_heads, pool->head_dim, max_parts,
+                               pb << chunk_shift(B), &ww))
+            return PKV_ERR_UNSUPPORTED;
+        need = ww.bytes;
+    }
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return PKV_ERR_NOMEM;
     int* status = status_word();
@@ -330,6 +374,19 @@ pkv_status decode_impl(const pkv_pool_desc* pool, void* out, const void* q, cons
         a.o_part = reinterpret_cast<float*>(w);
         a.m_part = reinterpret_cast<float*>(w + rows * pool->head_dim * sizeof(float));
         a.l_part = reinterpret_cast<float*>(w + rows * pool->head_dim * sizeof(float) + ml);
+    }
+    if (wo) {
+        const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * max_parts;
+        char* w = static_cast<char*>(workspace);
+        a.m_part = reinterpret_cast<float*>(w + ww.ml_at);
+        a.l_part = reinterpret_cast<float*>(w + ww.ml_at + round16(rows * sizeof(float)));
+        a.scores = reinterpret_cast<float*>(w + ww.scores_at);
+        a.score_tokens = ww.score_tokens;
+        a.weights = wo->weights;
+        a.row_ids = wo->row_ids;
+        a.weights_stride = wo->stride;
+        a.num_rows = wo->num_rows;
+        a.decay = wo->decay;
     }
     const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
     a.test_stall = decode_test_stall();
@@ -945,6 +1002,322 @@ pkv_status pkv_paged_prefill_append_host(const pkv_pool_desc* pool, void* k_pool
             return PKV_ERR_CUDA;
     }
     return PKV_OK;
+}
+
+size_t pkv_paged_decode_weights_workspace_bytes(const pkv_pool_desc* pool, int num_seqs,
+                                                int num_q_heads, int max_context,
+                                                int partition_blocks) {
+    if (check_pool(pool) != PKV_OK || num_seqs <= 0 || num_q_heads <= 0 || max_context <= 0 ||
+        partition_blocks < 0)
+        return 0;
+    const int B = pool->block_size;
+    const int pb = partition_blocks ? partition_blocks
+                                    : auto_partition(num_seqs, num_q_heads, max_context, B);
+    WeightsWorkspace w;
+    return weights_workspace(num_seqs, num_q_heads, pool->head_dim,
+                             ceil_div(ceil_div(max_context, B), pb), pb << chunk_shift(B), &w)
+               ? w.bytes
+               : 0;
+}
+
+pkv_status pkv_paged_decode_weights(const pkv_pool_desc* pool, void* out, const void* q,
+                                    void* k_pool, void* v_pool, const void* k_new,
+                                    const void* v_new, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* context_lens,
+                                    int max_context, int num_seqs, int num_q_heads, float scale,
+                                    int partition_blocks, float* weights, int64_t weights_stride,
+                                    const int32_t* row_ids, int num_rows, float decay,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range("pkv_paged_decode_weights");
+    if (num_seqs > 0 && (!k_new != !v_new || !aligned16(k_new) || !aligned16(v_new)))
+        return PKV_ERR_INVALID;
+    const WeightsOut wo{weights, weights_stride, row_ids, num_rows, decay};
+    return decode_impl(pool, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq,
+                       context_lens, max_context, num_seqs, num_q_heads, scale,
+                       partition_blocks, workspace, workspace_bytes, k_new, v_new, stream, &wo);
+}
+
+namespace {
+
+int block_shift(int block_size) { return 4 + chunk_shift(block_size); }
+
+// Token stride of a row array: whole 16-byte chunks.
+bool stride_ok(int64_t stride, int64_t least, int es) {
+    return stride >= least && (stride * es) % 16 == 0;
+}
+
+}  // namespace
+
+pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int64_t x_stride,
+                    const int32_t* positions, const double* inv_freq, int rotary_dim,
+                    int interleaved, int inverse, float attn_scale, int64_t num_tokens,
+                    int num_heads, int head_dim, void* stream) {
+    CallRange range("pkv_rope");
+    if (num_tokens < 0 || num_heads <= 0 || head_dim <= 0 || rotary_dim <= 0)
+        return PKV_ERR_INVALID;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if ((head_dim != 64 && head_dim != 128) || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (rotary_dim > head_dim) return PKV_ERR_INVALID;
+    if (num_tokens == 0) return PKV_OK;
+    if (num_tokens > INT32_MAX || num_heads > 1 << 20) return PKV_ERR_UNSUPPORTED;
+    if (!out || !x || !positions || !inv_freq || !aligned16(out) || !aligned16(x))
+        return PKV_ERR_INVALID;
+    const int es = elem_bytes(dtype);
+    if (!stride_ok(out_stride, static_cast<int64_t>(num_heads) * head_dim, es) ||
+        !stride_ok(x_stride, 0, es))
+        return PKV_ERR_INVALID;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::RopeArgs a{};
+    a.q = x;
+    a.k = x;
+    a.v = x;
+    a.q_out = out;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.status = status;
+    a.q_stride = x_stride;
+    a.q_out_stride = out_stride;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = num_heads;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved != 0;
+    a.inverse = inverse != 0;
+    a.attn_scale = attn_scale;
+    return from_cuda(
+        pkv::launch_rope(a, dtype, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_rope_append(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
+                           const int64_t* slot_mapping, void* q_out, int64_t q_out_stride,
+                           const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* positions,
+                           const double* inv_freq, int rotary_dim, int interleaved,
+                           float attn_scale, int64_t num_tokens, int num_q_heads, void* stream) {
+    CallRange range("pkv_rope_append");
+    pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0 || num_q_heads <= 0 || rotary_dim <= 0) return PKV_ERR_INVALID;
+    if (rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (rotary_dim > pool->head_dim) return PKV_ERR_INVALID;
+    if (num_tokens == 0) return PKV_OK;
+    if (num_tokens > INT32_MAX || num_q_heads > 1 << 20) return PKV_ERR_UNSUPPORTED;
+    if (!k_pool || !v_pool || !slot_mapping || !q_out || !q || !k || !v || !positions || !inv_freq)
+        return PKV_ERR_INVALID;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(q_out) || !aligned16(q) ||
+        !aligned16(k) || !aligned16(v))
+        return PKV_ERR_INVALID;
+    const int es = elem_bytes(pool->dtype);
+    if (!stride_ok(q_out_stride, static_cast<int64_t>(num_q_heads) * pool->head_dim, es) ||
+        !stride_ok(q_stride, 0, es) || !stride_ok(k_stride, 0, es) || !stride_ok(v_stride, 0, es))
+        return PKV_ERR_INVALID;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::RopeArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.slot_mapping = slot_mapping;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.status = status;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.num_tokens = num_tokens;
+    a.num_slots = pool->num_blocks * pool->block_size;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = pool->num_kv_heads;
+    a.rotary_dim = rotary_dim;
+    a.block_shift = block_shift(pool->block_size);
+    a.interleaved = interleaved != 0;
+    a.attn_scale = attn_scale;
+    return from_cuda(pkv::launch_rope(a, pool->dtype, pool->head_dim,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Query tokens of a request that count, at most.
+int window_rows(int max_new, int window) {
+    return window > 0 && window < max_new ? window : max_new;
+}
+
+// Parts that pass 1 splits a query tile's keys into, so that about four CTAs per SM have
+// work where there are few query tiles; a part has at least 8 tiles of 128 keys.
+int prefill_weights_splits(int num_reqs, int num_kv_heads, int rows, int max_context) {
+    const int64_t tiles = static_cast<int64_t>(num_reqs) * num_kv_heads * ceil_div(rows, 128);
+    const int64_t want = (4 * 152 + tiles - 1) / tiles;
+    const int64_t most = std::max(1, ceil_div(max_context, 8 * 128));
+    return static_cast<int>(std::min<int64_t>(std::min(want, most), 32));
+}
+
+}  // namespace
+
+size_t pkv_paged_prefill_weights_workspace_bytes(const pkv_pool_desc* pool, int num_reqs,
+                                                 int num_q_heads, int max_new, int max_context,
+                                                 int window) {
+    if (check_pool(pool) != PKV_OK || num_reqs <= 0 || num_q_heads <= 0 || max_new <= 0 ||
+        max_context <= 0 || window < 0 || num_q_heads % pool->num_kv_heads != 0)
+        return 0;
+    const int64_t rows = static_cast<int64_t>(window_rows(max_new, window)) *
+                         (num_q_heads / pool->num_kv_heads);
+    if (rows > INT32_MAX - 128) return 0;
+    const int splits = prefill_weights_splits(num_reqs, pool->num_kv_heads,
+                                              static_cast<int>(rows), max_context);
+    const size_t pad = static_cast<size_t>((rows + 127) / 128 * 128);
+    return static_cast<size_t>(num_reqs) * pool->num_kv_heads * splits * pad * sizeof(float2);
+}
+
+pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, const void* k_pool,
+                                     const int32_t* block_tables, int max_blocks_per_seq,
+                                     const int32_t* cached_lens, const int32_t* new_lens,
+                                     const int32_t* q_offsets, int num_reqs, int total_new,
+                                     int max_new, int max_context, int num_q_heads, float scale,
+                                     int window, float* weights, int64_t weights_stride,
+                                     const int32_t* row_ids, int num_rows, float decay,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range("pkv_paged_prefill_weights");
+    pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    if (num_reqs < 0 || total_new < 0 || max_new < 0 || num_q_heads <= 0 || window < 0 ||
+        !(scale > 0.f))
+        return PKV_ERR_INVALID;
+    if (num_reqs == 0 || total_new == 0 || max_new == 0) return PKV_OK;
+    if (!q || !k_pool || !block_tables || !cached_lens || !new_lens || !q_offsets ||
+        max_blocks_per_seq <= 0 || max_context <= 0 || !aligned16(q) || !aligned16(k_pool))
+        return PKV_ERR_INVALID;
+    if (static_cast<int64_t>(max_context) >
+        static_cast<int64_t>(max_blocks_per_seq) * pool->block_size)
+        return PKV_ERR_INVALID;
+    const WeightsOut wo{weights, weights_stride, row_ids, num_rows, decay};
+    if (!weights_ok(wo, num_reqs, max_context)) return PKV_ERR_INVALID;
+    if (num_q_heads % pool->num_kv_heads != 0) return PKV_ERR_INVALID;
+    const int group = num_q_heads / pool->num_kv_heads;
+    if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
+    if (num_reqs > 65535) return PKV_ERR_UNSUPPORTED;
+    const size_t need = pkv_paged_prefill_weights_workspace_bytes(
+        pool, num_reqs, num_q_heads, max_new, max_context, window);
+    if (need == 0) return PKV_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_NOMEM;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::PrefillWeightsArgs a{};
+    a.q = q;
+    a.k_pool = k_pool;
+    a.block_tables = block_tables;
+    a.cached_lens = cached_lens;
+    a.new_lens = new_lens;
+    a.q_offsets = q_offsets;
+    a.row_ids = row_ids;
+    a.weights = weights;
+    a.stats = static_cast<float2*>(workspace);
+    a.status = status;
+    a.num_blocks = pool->num_blocks;
+    a.weights_stride = weights_stride;
+    a.num_rows = num_rows;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_shift = block_shift(pool->block_size);
+    a.num_reqs = num_reqs;
+    a.total_new = total_new;
+    a.max_new = max_new;
+    a.max_rows = window_rows(max_new, window);
+    a.max_context = max_context;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = pool->num_kv_heads;
+    a.window = window;
+    a.splits = prefill_weights_splits(num_reqs, pool->num_kv_heads, a.max_rows * group,
+                                      max_context);
+    a.rows_pad = (a.max_rows * group + 127) / 128 * 128;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+    a.decay = decay;
+    return from_cuda(pkv::launch_prefill_weights(a, pool->dtype, pool->head_dim, group,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Same array, or no byte in common.
+bool same_or_apart(const void* a, const void* b, uint64_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x == y || x + bytes <= y || y + bytes <= x;
+}
+
+}  // namespace
+
+size_t pkv_evict_workspace_bytes(const pkv_pool_desc* pool, int num_seqs, int max_context) {
+    if (check_pool(pool) != PKV_OK || num_seqs <= 0 || max_context <= 0) return 0;
+    return static_cast<size_t>(num_seqs) * pool->num_kv_heads * max_context * sizeof(int32_t);
+}
+
+pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, int max_context, int num_seqs,
+                     const int32_t* budgets, int sinks, int recent, const int32_t* seen_lens,
+                     const int32_t* tracked_lens, const float* weights, float* weights_out,
+                     const int32_t* positions, int32_t* positions_out, int64_t weights_stride,
+                     const int32_t* row_ids, int num_rows, int32_t* new_lens, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    CallRange range("pkv_evict");
+    pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0 || sinks < 0 || recent < 0) return PKV_ERR_INVALID;
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_pool || !v_pool || !block_tables || !context_lens || !budgets || !weights_out ||
+        !positions || !positions_out || !new_lens || max_blocks_per_seq <= 0 || max_context <= 0)
+        return PKV_ERR_INVALID;
+    if (!aligned16(k_pool) || !aligned16(v_pool)) return PKV_ERR_INVALID;
+    if (static_cast<int64_t>(max_context) >
+        static_cast<int64_t>(max_blocks_per_seq) * pool->block_size)
+        return PKV_ERR_INVALID;
+    const WeightsOut wo{const_cast<float*>(weights), weights_stride, row_ids, num_rows, 1.f};
+    if (!weights_ok(wo, num_seqs, max_context)) return PKV_ERR_INVALID;
+    const uint64_t extent = static_cast<uint64_t>(num_rows) * pool->num_kv_heads *
+                            static_cast<uint64_t>(weights_stride) * 4;
+    if (!same_or_apart(weights, weights_out, extent) ||
+        !same_or_apart(positions, positions_out, extent))
+        return PKV_ERR_INVALID;
+    // the heads of a sequence run at different times: nothing they read may change
+    if (new_lens == context_lens || new_lens == budgets || new_lens == seen_lens ||
+        new_lens == tracked_lens || new_lens == row_ids)
+        return PKV_ERR_INVALID;
+    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    const size_t need = pkv_evict_workspace_bytes(pool, num_seqs, max_context);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_NOMEM;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::EvictArgs a{};
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.budgets = budgets;
+    a.seen_lens = seen_lens;
+    a.tracked_lens = tracked_lens;
+    a.row_ids = row_ids;
+    a.weights = weights;
+    a.weights_out = weights_out;
+    a.positions = positions;
+    a.positions_out = positions_out;
+    a.new_lens = new_lens;
+    a.moves = static_cast<int32_t*>(workspace);
+    a.status = status;
+    a.num_blocks = pool->num_blocks;
+    a.weights_stride = weights_stride;
+    a.num_rows = num_rows;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_shift = block_shift(pool->block_size);
+    a.max_context = max_context;
+    a.num_seqs = num_seqs;
+    a.num_kv_heads = pool->num_kv_heads;
+    a.row_bytes = pool->head_dim * elem_bytes(pool->dtype);
+    a.sinks = sinks;
+    a.recent = recent;
+    return from_cuda(pkv::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_copy_blocks(const pkv_pool_desc* pool, void* k_pool, void* v_pool,

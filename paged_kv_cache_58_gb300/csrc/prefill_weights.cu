@@ -1,0 +1,314 @@
+// Accumulated attention weights of a prompt chunk: how much attention each cached key
+// receives from a request's last `window` new tokens, summed over them and over the
+// query heads of its kv head,
+//   weights[j] = decay * weights[j] + sum_{rows r that see j} 2^(s_rj - M_r) / sum_r,
+// s = scale * log2(e) * q.k.  A row's statistics (M_r, sum_r) need every key before any
+// of its weights is known, and the scores of a chunk (rows x keys, 4 bytes each) are
+// far more than K, so the work is two passes over Q K^T:
+//   pass 1  per 64-row query tile, online (max, sum) of each row over its keys,
+//   pass 2  per 64-key tile, the column sums over all the query tiles that see it.
+// Each pass reads only Q and K.  A key tile of a request and kv head belongs to one CTA,
+// which walks its query tiles in order: no atomics, and the same bits every time.
+//
+// This is the CUDA-core form: a 64 x 64 tile of scores per step, 256 threads of 4 x 4
+// scores each, both operand tiles in shared memory as fp32.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kTile = 64;       // rows, and keys, of a score tile
+constexpr int kThreads = 256;   // 16 x 16 threads, 4 x 4 scores each
+
+// What a request asks for, checked; `rows` = 0: nothing to do.
+struct Request {
+    int n, c, m, rows, qoff, wrow;
+};
+PKV_DEVINL Request request_of(const PrefillWeightsArgs& a, int r, int group, bool report) {
+    Request q;
+    q.n = __ldg(a.new_lens + r);
+    q.c = __ldg(a.cached_lens + r);
+    q.qoff = __ldg(a.q_offsets + r);
+    q.wrow = a.row_ids ? __ldg(a.row_ids + r) : r;
+    q.m = a.window > 0 ? min(a.window, q.n) : q.n;
+    q.rows = 0;
+    if (q.n <= 0 || q.wrow < 0) return q;   // no new tokens, or a padding row
+    const int64_t L = static_cast<int64_t>(q.c) + q.n;
+    if (q.c < 0 || L > a.max_context || q.n > a.max_new || q.wrow >= a.num_rows || q.qoff < 0 ||
+        static_cast<int64_t>(q.qoff) + q.n > a.total_new) {
+        if (report) raise_status(a.status, PKV_ERR_OOB);
+        return q;
+    }
+    q.rows = q.m * group;
+    return q;
+}
+
+PKV_DEVINL float to_f32(float x) { return x; }
+PKV_DEVINL float to_f32(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+
+template <typename T, int D>
+struct Smem {
+    static constexpr int kStride = D + 4;   // 16-byte rows, shifted 4 banks per row
+    float q[kTile][kStride];
+    float k[kTile][kStride];
+    float red[2][kTile][17];
+};
+
+// Rows (i, g) of the window, token-major: row rho is token n - m + rho / G of the
+// request's new tokens, head kvh * G + rho % G.
+template <typename T, int D>
+PKV_DEVINL void load_q(float (*dst)[Smem<T, D>::kStride], const PrefillWeightsArgs& a,
+                       const Request& rq, int group, int kvh, int row0) {
+    constexpr int E = 16 / sizeof(T);
+    for (int t = threadIdx.x; t < kTile * (D / E); t += kThreads) {
+        const int row = t / (D / E), ch = t % (D / E);
+        const int rho = row0 + row;
+        float* d = &dst[row][ch * E];
+        if (rho < rq.rows) {
+            const int64_t tok = static_cast<int64_t>(rq.qoff) + rq.n - rq.m + rho / group;
+            const T* src = static_cast<const T*>(a.q) +
+                           (tok * a.num_q_heads + kvh * group + rho % group) * D + ch * E;
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+            const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[i] = to_f32(e[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[i] = 0.f;
+        }
+    }
+}
+template <typename T, int D>
+PKV_DEVINL void load_k(float (*dst)[Smem<T, D>::kStride], const PrefillWeightsArgs& a, int req,
+                       int kvh, int key0, int keys) {
+    constexpr int E = 16 / sizeof(T);
+    const int32_t* bt = a.block_tables + static_cast<size_t>(req) * a.max_blocks_per_seq;
+    for (int t = threadIdx.x; t < kTile * (D / E); t += kThreads) {
+        const int row = t / (D / E), ch = t % (D / E);
+        const int key = key0 + row;
+        float* d = &dst[row][ch * E];
+        int phys = -1;
+        if (key < keys) {
+            phys = __ldg(bt + (key >> a.block_shift));
+            if (phys < 0 || phys >= a.num_blocks) {
+                raise_status(a.status, PKV_ERR_OOB);
+                phys = -1;
+            }
+        }
+        if (phys >= 0) {
+            const T* src = static_cast<const T*>(a.k_pool) +
+                           (((static_cast<int64_t>(phys) * a.num_kv_heads + kvh)
+                             << a.block_shift) +
+                            (key & ((1 << a.block_shift) - 1))) * D + ch * E;
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+            const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[i] = to_f32(e[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[i] = 0.f;
+        }
+    }
+}
+
+// s[i][j] = q row (ty + 16 i) . k row (tx + 16 j), scaled; 4 x 4 per thread.
+template <typename T, int D>
+PKV_DEVINL void scores(const Smem<T, D>& sm, float scale, float (&s)[4][4]) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const float4*>(&sm.q[ty + 16 * i][d]);
+            y[i] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * i][d]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+                s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+                s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+                s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] *= scale;
+}
+
+// Pass 1.  Grid (query tile x splits, kv head, request); split z of the keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+row_stats_kernel(const PrefillWeightsArgs a, const int group) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    const int kvh = blockIdx.y, req = blockIdx.z;
+    const Request rq = request_of(a, req, group, threadIdx.x == 0 && blockIdx.x == 0);
+    const int row0 = tile * kTile;
+    if (row0 >= rq.rows) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    // keys any row of the tile sees
+    const int last = rq.c + rq.n - rq.m + (min(row0 + kTile, rq.rows) - 1) / group;
+    const int key_tiles = last / kTile + 1;
+    const int per = (key_tiles + a.splits - 1) / a.splits;
+    const int t0 = split * per, t1 = min(key_tiles, t0 + per);
+    load_q<T, D>(sm.q, a, rq, group, kvh, row0);
+    float m[4], l[4];
+    int lim[4];   // last key of each of the thread's rows
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        lim[i] = rq.c + rq.n - rq.m + (row0 + ty + 16 * i) / group;
+    }
+    for (int t = t0; t < t1; ++t) {
+        load_k<T, D>(sm.k, a, req, kvh, t * kTile, last + 1);
+        __syncthreads();
+        float s[4][4];
+        scores<T, D>(sm, a.scale_log2, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (t * kTile + tx + 16 * j > lim[i]) s[i][j] = -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            if (mx > -INFINITY) {   // this thread has seen a key of the row
+                float add = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) add += fast_exp2(s[i][j] - mx);
+                l[i] = l[i] * fast_exp2(m[i] - mx) + add;
+                m[i] = mx;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sm.red[0][ty + 16 * i][tx] = m[i];
+        sm.red[1][ty + 16 * i][tx] = l[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < kTile) {
+        const int row = threadIdx.x;
+        float M = -INFINITY, l_all = 0.f;
+        for (int x = 0; x < 16; ++x) M = fmaxf(M, sm.red[0][row][x]);
+        if (M > -INFINITY)
+            for (int x = 0; x < 16; ++x)
+                l_all += sm.red[1][row][x] * fast_exp2(sm.red[0][row][x] - M);
+        float2* st = a.stats + ((static_cast<size_t>(req) * a.num_kv_heads + kvh) * a.splits +
+                                split) * a.rows_pad;
+        if (row0 + row < rq.rows) st[row0 + row] = make_float2(M, l_all);
+    }
+}
+
+// Pass 2.  Grid (key tile, kv head, request).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+column_sums_kernel(const PrefillWeightsArgs a, const int group) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int kvh = blockIdx.y, req = blockIdx.z;
+    const Request rq = request_of(a, req, group, false);
+    const int key0 = blockIdx.x * kTile;
+    const int keys = rq.c + rq.n;
+    if (rq.rows == 0 || key0 >= keys) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    load_k<T, D>(sm.k, a, req, kvh, key0, keys);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const int base = rq.c + rq.n - rq.m;   // last key of the window's first token
+    const int first = max(0, key0 - base) * group;   // earlier rows see no key of the tile
+    for (int row0 = first / kTile * kTile; row0 < rq.rows; row0 += kTile) {
+        load_q<T, D>(sm.q, a, rq, group, kvh, row0);
+        if (threadIdx.x < kTile) {   // merge the splits' statistics of the tile's rows
+            float M = -INFINITY, l = 0.f;
+            if (row0 + static_cast<int>(threadIdx.x) < rq.rows) {
+                const float2* st =
+                    a.stats + (static_cast<size_t>(req) * a.num_kv_heads + kvh) * a.splits *
+                                  a.rows_pad + row0 + threadIdx.x;
+                for (int z = 0; z < a.splits; ++z) M = fmaxf(M, st[z * a.rows_pad].x);
+                for (int z = 0; z < a.splits; ++z) {
+                    const float2 f = st[z * a.rows_pad];
+                    l += f.y * fast_exp2(f.x - M);
+                }
+            }
+            sm.red[0][threadIdx.x][0] = M;
+            sm.red[1][threadIdx.x][0] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        }
+        __syncthreads();
+        float s[4][4];
+        scores<T, D>(sm, a.scale_log2, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rho = row0 + ty + 16 * i;
+            const int lim = base + rho / group;
+            const float M = sm.red[0][ty + 16 * i][0], inv = sm.red[1][ty + 16 * i][0];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (rho < rq.rows && key0 + tx + 16 * j <= lim)
+                    sum[j] = fmaf(fast_exp2(s[i][j] - M), inv, sum[j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sm.red[0][tx + 16 * j][ty] = sum[j];
+    __syncthreads();
+    if (threadIdx.x < kTile) {
+        const int key = key0 + threadIdx.x;
+        if (key < keys) {
+            float t = 0.f;
+            for (int y = 0; y < 16; ++y) t += sm.red[0][threadIdx.x][y];
+            float* w = a.weights + (static_cast<size_t>(rq.wrow) * a.num_kv_heads + kvh) *
+                                       static_cast<size_t>(a.weights_stride) + key;
+            *w = a.decay != 0.f ? fmaf(a.decay, *w, t) : t;
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const PrefillWeightsArgs& a, int group, cudaStream_t stream) {
+    const int smem = sizeof(Smem<T, D>);
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(row_stats_kernel<T, D>), smem);
+    if (e != cudaSuccess) return e;
+    e = set_smem_once(reinterpret_cast<const void*>(column_sums_kernel<T, D>), smem);
+    if (e != cudaSuccess) return e;
+    const int64_t row_tiles = (static_cast<int64_t>(a.max_rows) * group + kTile - 1) / kTile;
+    const int key_tiles = (a.max_context + kTile - 1) / kTile;
+    if (row_tiles * a.splits > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_pdl(row_stats_kernel<T, D>,
+                   dim3(static_cast<unsigned>(row_tiles * a.splits), a.num_kv_heads, a.num_reqs),
+                   dim3(kThreads), smem, stream, a, group);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(column_sums_kernel<T, D>, dim3(key_tiles, a.num_kv_heads, a.num_reqs),
+                      dim3(kThreads), smem, stream, a, group);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int dtype, int head_dim, int group,
+                                   cudaStream_t stream) {
+    if (dtype == PKV_BF16)
+        return head_dim == 128 ? launch_typed<uint16_t, 128>(a, group, stream)
+                               : launch_typed<uint16_t, 64>(a, group, stream);
+    return head_dim == 128 ? launch_typed<float, 128>(a, group, stream)
+                           : launch_typed<float, 64>(a, group, stream);
+}
+
+}  // namespace pkv
