@@ -224,7 +224,8 @@ struct PrefillWeightsArgs {
     const int32_t* q_offsets;
     const int32_t* row_ids;   // weight row of each request (null: its index)
     float* weights;           // [num_rows][Hkv][weights_stride]
-    float2* stats;            // workspace: (max, sum) [R][Hkv][splits][rows_pad]
+    float2* stats;            // workspace: (reference, sum) [R][Hkv][splits][rows_pad]
+    float* neg_lse;           // workspace (tensor cores): -log2(sum 2^s) [R][Hkv][rows_pad]
     int* status;
     int64_t num_blocks;
     int64_t weights_stride;
@@ -240,12 +241,18 @@ struct PrefillWeightsArgs {
     int num_kv_heads;
     int window;        // 0: every new token
     int splits;        // parts the keys of a query tile are split into in pass 1
-    int rows_pad;      // rows of one (request, kv head, split) in `stats`
+    int chunk_tiles;   // tensor cores: 128-key tiles per split
+    int rows_pad;      // rows of one (request, kv head, split) in `stats`: a multiple of 128
+    int group_shift;   // tensor cores: log2(G)
     float scale_log2;
     float decay;
 };
-cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int dtype, int head_dim, int group,
+// fp32 pools, on the CUDA cores.
+cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int head_dim, int group,
                                    cudaStream_t stream);
+// bf16 pools, on the tensor cores.
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, int head_dim, int group,
+                                      cudaStream_t stream);
 
 // Eviction by accumulated weight.
 struct EvictArgs {

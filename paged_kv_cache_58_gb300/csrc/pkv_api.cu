@@ -1147,13 +1147,28 @@ int window_rows(int max_new, int window) {
     return window > 0 && window < max_new ? window : max_new;
 }
 
-// Parts that pass 1 splits a query tile's keys into, so that about four CTAs per SM have
-// work where there are few query tiles; a part has at least 8 tiles of 128 keys.
-int prefill_weights_splits(int num_reqs, int num_kv_heads, int rows, int max_context) {
-    const int64_t tiles = static_cast<int64_t>(num_reqs) * num_kv_heads * ceil_div(rows, 128);
-    const int64_t want = (4 * 152 + tiles - 1) / tiles;
-    const int64_t most = std::max(1, ceil_div(max_context, 8 * 128));
-    return static_cast<int>(std::min<int64_t>(std::min(want, most), 32));
+// How pass 1 cuts the keys of a query tile, and the workspace that gives.
+struct PrefillWeightsPlan {
+    int rows_pad, splits, chunk_tiles;
+    size_t stats_bytes, bytes;
+};
+bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_heads, int max_new,
+                          int max_context, int window, PrefillWeightsPlan* p) {
+    const int64_t rows = static_cast<int64_t>(window_rows(max_new, window)) *
+                         (num_q_heads / pool->num_kv_heads);
+    if (rows > INT32_MAX - 128) return false;
+    p->rows_pad = static_cast<int>((rows + 127) / 128 * 128);
+    // Enough parts that about eight items per SM exist where there are few query tiles (the
+    // lengths are not known here, only their bound); a part has at least 8 tiles of 128 keys.
+    const int64_t heads = static_cast<int64_t>(num_reqs) * pool->num_kv_heads;
+    const int64_t items = heads * ((p->rows_pad / 128 + 1) / 2);
+    const int tiles = ceil_div(max_context, 128);
+    const int64_t want = std::min<int64_t>((8 * 152 + items - 1) / items, 64);
+    p->chunk_tiles = std::max(8, ceil_div(tiles, want));
+    p->splits = ceil_div(tiles, p->chunk_tiles);
+    p->stats_bytes = static_cast<size_t>(heads) * p->splits * p->rows_pad * sizeof(float2);
+    p->bytes = p->stats_bytes + static_cast<size_t>(heads) * p->rows_pad * sizeof(float);
+    return true;
 }
 
 }  // namespace
@@ -1164,13 +1179,10 @@ size_t pkv_paged_prefill_weights_workspace_bytes(const pkv_pool_desc* pool, int 
     if (check_pool(pool) != PKV_OK || num_reqs <= 0 || num_q_heads <= 0 || max_new <= 0 ||
         max_context <= 0 || window < 0 || num_q_heads % pool->num_kv_heads != 0)
         return 0;
-    const int64_t rows = static_cast<int64_t>(window_rows(max_new, window)) *
-                         (num_q_heads / pool->num_kv_heads);
-    if (rows > INT32_MAX - 128) return 0;
-    const int splits = prefill_weights_splits(num_reqs, pool->num_kv_heads,
-                                              static_cast<int>(rows), max_context);
-    const size_t pad = static_cast<size_t>((rows + 127) / 128 * 128);
-    return static_cast<size_t>(num_reqs) * pool->num_kv_heads * splits * pad * sizeof(float2);
+    PrefillWeightsPlan p;
+    return prefill_weights_plan(pool, num_reqs, num_q_heads, max_new, max_context, window, &p)
+               ? p.bytes
+               : 0;
 }
 
 pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, const void* k_pool,
@@ -1200,10 +1212,10 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     const int group = num_q_heads / pool->num_kv_heads;
     if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
     if (num_reqs > 65535) return PKV_ERR_UNSUPPORTED;
-    const size_t need = pkv_paged_prefill_weights_workspace_bytes(
-        pool, num_reqs, num_q_heads, max_new, max_context, window);
-    if (need == 0) return PKV_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_NOMEM;
+    PrefillWeightsPlan plan;
+    if (!prefill_weights_plan(pool, num_reqs, num_q_heads, max_new, max_context, window, &plan))
+        return PKV_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < plan.bytes || !aligned16(workspace)) return PKV_ERR_NOMEM;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;
     pkv::PrefillWeightsArgs a{};
@@ -1216,6 +1228,7 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     a.row_ids = row_ids;
     a.weights = weights;
     a.stats = static_cast<float2*>(workspace);
+    a.neg_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes);
     a.status = status;
     a.num_blocks = pool->num_blocks;
     a.weights_stride = weights_stride;
@@ -1230,13 +1243,17 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = pool->num_kv_heads;
     a.window = window;
-    a.splits = prefill_weights_splits(num_reqs, pool->num_kv_heads, a.max_rows * group,
-                                      max_context);
-    a.rows_pad = (a.max_rows * group + 127) / 128 * 128;
+    a.splits = plan.splits;
+    a.chunk_tiles = plan.chunk_tiles;
+    a.rows_pad = plan.rows_pad;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
     a.decay = decay;
-    return from_cuda(pkv::launch_prefill_weights(a, pool->dtype, pool->head_dim, group,
-                                                 static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = pool->dtype == PKV_BF16
+                              ? pkv::launch_prefill_weights_tc(a, pool->head_dim, group, st_)
+                              : pkv::launch_prefill_weights(a, pool->head_dim, group, st_);
+    if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
+    return from_cuda(e);
 }
 
 namespace {

@@ -10,8 +10,9 @@
 // Each pass reads only Q and K.  A key tile of a request and kv head belongs to one CTA,
 // which walks its query tiles in order: no atomics, and the same bits every time.
 //
-// This is the CUDA-core form: a 64 x 64 tile of scores per step, 256 threads of 4 x 4
-// scores each, both operand tiles in shared memory as fp32.
+// This is the CUDA-core form, for fp32 pools (the tensor cores would round the operands to
+// tf32; bf16 pools have a tensor-core form in prefill_weights_tc.cu): a 64 x 64 tile of
+// scores per step, 256 threads of 4 x 4 scores each, both operand tiles in shared memory.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -47,10 +48,7 @@ PKV_DEVINL Request request_of(const PrefillWeightsArgs& a, int r, int group, boo
     return q;
 }
 
-PKV_DEVINL float to_f32(float x) { return x; }
-PKV_DEVINL float to_f32(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-
-template <typename T, int D>
+template <int D>
 struct Smem {
     static constexpr int kStride = D + 4;   // 16-byte rows, shifted 4 banks per row
     float q[kTile][kStride];
@@ -60,32 +58,28 @@ struct Smem {
 
 // Rows (i, g) of the window, token-major: row rho is token n - m + rho / G of the
 // request's new tokens, head kvh * G + rho % G.
-template <typename T, int D>
-PKV_DEVINL void load_q(float (*dst)[Smem<T, D>::kStride], const PrefillWeightsArgs& a,
+template <int D>
+PKV_DEVINL void load_q(float (*dst)[Smem<D>::kStride], const PrefillWeightsArgs& a,
                        const Request& rq, int group, int kvh, int row0) {
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = 4;   // floats per 16-byte piece
     for (int t = threadIdx.x; t < kTile * (D / E); t += kThreads) {
         const int row = t / (D / E), ch = t % (D / E);
         const int rho = row0 + row;
         float* d = &dst[row][ch * E];
         if (rho < rq.rows) {
             const int64_t tok = static_cast<int64_t>(rq.qoff) + rq.n - rq.m + rho / group;
-            const T* src = static_cast<const T*>(a.q) +
+            const float* src = static_cast<const float*>(a.q) +
                            (tok * a.num_q_heads + kvh * group + rho % group) * D + ch * E;
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
-            const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-            for (int i = 0; i < E; ++i) d[i] = to_f32(e[i]);
+            *reinterpret_cast<float4*>(d) = __ldg(reinterpret_cast<const float4*>(src));
         } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) d[i] = 0.f;
+            *reinterpret_cast<float4*>(d) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
 }
-template <typename T, int D>
-PKV_DEVINL void load_k(float (*dst)[Smem<T, D>::kStride], const PrefillWeightsArgs& a, int req,
+template <int D>
+PKV_DEVINL void load_k(float (*dst)[Smem<D>::kStride], const PrefillWeightsArgs& a, int req,
                        int kvh, int key0, int keys) {
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = 4;   // floats per 16-byte piece
     const int32_t* bt = a.block_tables + static_cast<size_t>(req) * a.max_blocks_per_seq;
     for (int t = threadIdx.x; t < kTile * (D / E); t += kThreads) {
         const int row = t / (D / E), ch = t % (D / E);
@@ -100,24 +94,20 @@ PKV_DEVINL void load_k(float (*dst)[Smem<T, D>::kStride], const PrefillWeightsAr
             }
         }
         if (phys >= 0) {
-            const T* src = static_cast<const T*>(a.k_pool) +
+            const float* src = static_cast<const float*>(a.k_pool) +
                            (((static_cast<int64_t>(phys) * a.num_kv_heads + kvh)
                              << a.block_shift) +
                             (key & ((1 << a.block_shift) - 1))) * D + ch * E;
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
-            const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-            for (int i = 0; i < E; ++i) d[i] = to_f32(e[i]);
+            *reinterpret_cast<float4*>(d) = __ldg(reinterpret_cast<const float4*>(src));
         } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) d[i] = 0.f;
+            *reinterpret_cast<float4*>(d) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
 }
 
 // s[i][j] = q row (ty + 16 i) . k row (tx + 16 j), scaled; 4 x 4 per thread.
-template <typename T, int D>
-PKV_DEVINL void scores(const Smem<T, D>& sm, float scale, float (&s)[4][4]) {
+template <int D>
+PKV_DEVINL void scores(const Smem<D>& sm, float scale, float (&s)[4][4]) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -148,11 +138,11 @@ PKV_DEVINL void scores(const Smem<T, D>& sm, float scale, float (&s)[4][4]) {
 }
 
 // Pass 1.  Grid (query tile x splits, kv head, request); split z of the keys.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 row_stats_kernel(const PrefillWeightsArgs a, const int group) {
     extern __shared__ __align__(16) uint8_t raw[];
-    Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
     griddep_wait();
     griddep_launch_dependents();
     const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
@@ -166,7 +156,7 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
     const int key_tiles = last / kTile + 1;
     const int per = (key_tiles + a.splits - 1) / a.splits;
     const int t0 = split * per, t1 = min(key_tiles, t0 + per);
-    load_q<T, D>(sm.q, a, rq, group, kvh, row0);
+    load_q<D>(sm.q, a, rq, group, kvh, row0);
     float m[4], l[4];
     int lim[4];   // last key of each of the thread's rows
 #pragma unroll
@@ -176,10 +166,10 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
         lim[i] = rq.c + rq.n - rq.m + (row0 + ty + 16 * i) / group;
     }
     for (int t = t0; t < t1; ++t) {
-        load_k<T, D>(sm.k, a, req, kvh, t * kTile, last + 1);
+        load_k<D>(sm.k, a, req, kvh, t * kTile, last + 1);
         __syncthreads();
         float s[4][4];
-        scores<T, D>(sm, a.scale_log2, s);
+        scores<D>(sm, a.scale_log2, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = m[i];
@@ -218,11 +208,11 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
 }
 
 // Pass 2.  Grid (key tile, kv head, request).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     extern __shared__ __align__(16) uint8_t raw[];
-    Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
     griddep_wait();
     griddep_launch_dependents();
     const int kvh = blockIdx.y, req = blockIdx.z;
@@ -231,12 +221,12 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     const int keys = rq.c + rq.n;
     if (rq.rows == 0 || key0 >= keys) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_k<T, D>(sm.k, a, req, kvh, key0, keys);
+    load_k<D>(sm.k, a, req, kvh, key0, keys);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     const int base = rq.c + rq.n - rq.m;   // last key of the window's first token
     const int first = max(0, key0 - base) * group;   // earlier rows see no key of the tile
     for (int row0 = first / kTile * kTile; row0 < rq.rows; row0 += kTile) {
-        load_q<T, D>(sm.q, a, rq, group, kvh, row0);
+        load_q<D>(sm.q, a, rq, group, kvh, row0);
         if (threadIdx.x < kTile) {   // merge the splits' statistics of the tile's rows
             float M = -INFINITY, l = 0.f;
             if (row0 + static_cast<int>(threadIdx.x) < rq.rows) {
@@ -254,7 +244,7 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
         }
         __syncthreads();
         float s[4][4];
-        scores<T, D>(sm, a.scale_log2, s);
+        scores<D>(sm, a.scale_log2, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int rho = row0 + ty + 16 * i;
@@ -282,33 +272,30 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_typed(const PrefillWeightsArgs& a, int group, cudaStream_t stream) {
-    const int smem = sizeof(Smem<T, D>);
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(row_stats_kernel<T, D>), smem);
+    const int smem = sizeof(Smem<D>);
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(row_stats_kernel<D>), smem);
     if (e != cudaSuccess) return e;
-    e = set_smem_once(reinterpret_cast<const void*>(column_sums_kernel<T, D>), smem);
+    e = set_smem_once(reinterpret_cast<const void*>(column_sums_kernel<D>), smem);
     if (e != cudaSuccess) return e;
     const int64_t row_tiles = (static_cast<int64_t>(a.max_rows) * group + kTile - 1) / kTile;
     const int key_tiles = (a.max_context + kTile - 1) / kTile;
     if (row_tiles * a.splits > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch_pdl(row_stats_kernel<T, D>,
+    e = launch_pdl(row_stats_kernel<D>,
                    dim3(static_cast<unsigned>(row_tiles * a.splits), a.num_kv_heads, a.num_reqs),
                    dim3(kThreads), smem, stream, a, group);
     if (e != cudaSuccess) return e;
-    return launch_pdl(column_sums_kernel<T, D>, dim3(key_tiles, a.num_kv_heads, a.num_reqs),
+    return launch_pdl(column_sums_kernel<D>, dim3(key_tiles, a.num_kv_heads, a.num_reqs),
                       dim3(kThreads), smem, stream, a, group);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int dtype, int head_dim, int group,
+cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int head_dim, int group,
                                    cudaStream_t stream) {
-    if (dtype == PKV_BF16)
-        return head_dim == 128 ? launch_typed<uint16_t, 128>(a, group, stream)
-                               : launch_typed<uint16_t, 64>(a, group, stream);
-    return head_dim == 128 ? launch_typed<float, 128>(a, group, stream)
-                           : launch_typed<float, 64>(a, group, stream);
+    return head_dim == 128 ? launch_typed<128>(a, group, stream)
+                           : launch_typed<64>(a, group, stream);
 }
 
 }  // namespace pkv

@@ -1,0 +1,685 @@
+// Accumulated attention weights of a prompt chunk for bf16 pools, on the tcgen05 tensor
+// cores.  The mathematics, and why there are two passes over Q K^T, is in
+// prefill_weights.cu; here both passes are one kernel skeleton:
+//
+//   pass 1 (row statistics)  S[128 query rows x 128 keys]  = Q K^T    A = Q, B = K
+//   pass 2 (column sums)     S[128 keys x 128 query rows]  = K Q^T    A = K, B = Q
+//
+// The side whose sums are wanted sits on the M side of the product, so it lies along the
+// TMEM lanes: a thread owns a query row (pass 1) or a key (pass 2) and reduces over its
+// own registers, with no exchange between threads in either pass.  An item holds up to
+// two A tiles (256 rows or keys) and streams B tiles past them; every B tile staged
+// serves both, which halves the copies per product.  Warpgroup a of the two consumer
+// warpgroups takes A tile a, in two TMEM buffers of 128 columns each (all 512 columns).
+//
+// Pass 1 keeps the maximum of a row's first tile of the item as its reference and adds
+// 2^(s - m) from there on without looking for a larger one: there is no accumulator to
+// keep in range, only a sum in fp32, whose relative precision does not depend on the
+// reference.  Only a sum past 2^96 (later scores beyond the first tile's maximum by that
+// much) takes the tile again with a new reference.  The keys of a row tile are cut into
+// chunks that different CTAs take; a small launch merges the chunks' (m, sum) into
+// -log2(sum 2^s) per row, which is all that pass 2 needs:
+//   p = 2^(scale_log2 s - lse).
+//
+// Persistent CTAs, one per SM, each walking every gridDim.x-th item: producers run ahead
+// into the next item's tiles while the consumers finish the current one.  Roles: warps
+// 0-3 and 4-7 consumers, warp 8 A tiles, warp 9 B tiles, warp 10 MMA and TMEM.
+#include <atomic>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kChunk = 16;          // tokens per TMA box of K
+constexpr int kBoxes = kTile / kChunk;
+constexpr int kHalf = kTile * 128;  // a 64-column half of a Q tile: 16 KB
+constexpr int kThreads = 384;
+constexpr int kWarpA = 8, kWarpB = 9, kWarpMma = 10;
+constexpr int kMaxReqs = 384;       // requests per launch (the item offsets in shared memory)
+constexpr float kSumLimit = 7.9e28f;   // 2^96
+
+template <int D>
+struct Geom {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kChunkBytes = kChunk * D * 2;
+    static constexpr int kGroupBytes = 8 * D * 2;    // 8 key rows, every half
+    static constexpr int kStagesB = D == 128 ? 3 : 6;
+    static constexpr int kOffA = 0;                   // two pairs of tiles
+    static constexpr int kOffB = 4 * kTileBytes;
+    static constexpr int kOffBar = kOffB + kStagesB * kTileBytes;
+    static constexpr int kBars = 2 + 2 + 2 * kStagesB + 4 + 4 + 1;
+    static constexpr int kOffCtl = kOffBar + kBars * 8;          // TMEM address, abort flag
+    static constexpr int kOffItems = kOffCtl + 16;
+    static constexpr int kBytes = kOffItems + (kMaxReqs + 1) * 4 + 1024;   // + align slack
+    // barriers
+    static constexpr int A_FULL = 0, A_EMPTY = 2, B_FULL = 4, B_EMPTY = 4 + kStagesB,
+                         S_FULL = 4 + 2 * kStagesB, S_FREE = S_FULL + 4, DRAIN = S_FREE + 4;
+};
+static_assert(Geom<128>::kBytes <= 232448, "shared memory of one SM");
+
+struct Ctl {
+    uint64_t* bars;
+    volatile int* abort_flag;
+    int* status;
+};
+
+// Bounded wait of a converged warp; gives up when another role did, or out of time.
+PKV_DEVINL bool wait_bar(const Ctl& c, int idx, uint32_t parity) {
+    uint64_t* bar = &c.bars[idx];
+    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *c.abort_flag != 0)) return false;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitBudgetNs)) {
+            if ((threadIdx.x & 31) == 0) {
+                raise_status(c.status, PKV_ERR_TIMEOUT);
+                *c.abort_flag = 1;
+            }
+            __syncwarp();
+            return false;
+        }
+    }
+}
+
+// Request r's window, or rows = 0: nothing to do (or out of range, which is reported).
+struct Request {
+    int n, c, m, rows, qoff, wrow;
+};
+PKV_DEVINL Request request_of(const PrefillWeightsArgs& a, int r, bool report) {
+    Request q;
+    q.n = __ldg(a.new_lens + r);
+    q.c = __ldg(a.cached_lens + r);
+    q.qoff = __ldg(a.q_offsets + r);
+    q.wrow = a.row_ids ? __ldg(a.row_ids + r) : r;
+    q.m = a.window > 0 ? min(a.window, q.n) : q.n;
+    q.rows = 0;
+    if (q.n <= 0 || q.wrow < 0) return q;
+    if (q.c < 0 || static_cast<int64_t>(q.c) + q.n > a.max_context || q.n > a.max_new ||
+        q.wrow >= a.num_rows || q.qoff < 0 ||
+        static_cast<int64_t>(q.qoff) + q.n > a.total_new) {
+        if (report) raise_status(a.status, PKV_ERR_OOB);
+        return q;
+    }
+    q.rows = q.m << a.group_shift;
+    return q;
+}
+
+PKV_DEVINL int ceil_div(int x, int y) { return (x + y - 1) / y; }
+
+// One item: A tiles a0, a0 + 1 (na of them) against B tiles [b0, b0 + nb).
+struct Item {
+    int r, kvh, chunk, a0, na, b0, nb;
+    int base;   // last key that the window's first token sees
+    Request q;
+};
+
+// The walk over a CTA's items: item k of request r (off[r] <= k < off[r + 1]).
+template <int PASS>
+struct Walk {
+    const PrefillWeightsArgs& a;
+    const int* off;
+    int k, r = 0;
+    PKV_DEVINL Walk(const PrefillWeightsArgs& args, const int* offsets)
+        : a(args), off(offsets), k(blockIdx.x) {}
+    PKV_DEVINL bool next(Item& it) {
+        for (;; k += gridDim.x) {
+            if (k >= off[a.num_reqs]) return false;
+            while (off[r + 1] <= k) ++r;
+            it.r = r;
+            it.q = request_of(a, r, false);
+            it.base = it.q.c + it.q.n - it.q.m;
+            const int keys = it.q.c + it.q.n;
+            int rem = k - off[r];
+            if (PASS == 1) {   // query-tile pair fastest: neighbours read the same keys
+                const int tiles = ceil_div(it.q.rows, kTile), pairs = (tiles + 1) / 2;
+                const int chunks = ceil_div(ceil_div(keys, kTile), a.chunk_tiles);
+                it.a0 = 2 * (rem % pairs);
+                rem /= pairs;
+                it.chunk = rem % chunks;
+                it.kvh = rem / chunks;
+                it.na = min(2, tiles - it.a0);
+                const int last_row = min((it.a0 + it.na) * kTile, it.q.rows) - 1;
+                const int last_key = it.base + (last_row >> a.group_shift);
+                it.b0 = it.chunk * a.chunk_tiles;
+                it.nb = min(a.chunk_tiles, last_key / kTile + 1 - it.b0);
+            } else {
+                const int tiles = ceil_div(keys, kTile), pairs = (tiles + 1) / 2;
+                it.a0 = 2 * (rem % pairs);
+                it.kvh = rem / pairs;
+                it.chunk = 0;
+                it.na = min(2, tiles - it.a0);
+                // rows from the first that sees the item's first key
+                const int first = max(0, it.a0 * kTile - it.base) << a.group_shift;
+                it.b0 = first / kTile;
+                it.nb = ceil_div(it.q.rows, kTile) - it.b0;
+            }
+            if (it.nb > 0) {
+                k += gridDim.x;
+                return true;
+            }
+        }
+    }
+};
+
+// Sum of 2^(x * sl2 + off) over 32 values, into four pairs of accumulators.
+PKV_DEVINL void add_exp(const float (&x)[32], float sl2, float off, float (&acc)[8]) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float a0, a1;
+        ffma2(a0, a1, x[e], x[e + 1], sl2, sl2, off, off);
+        const int u = e & 6;
+        fadd2(acc[u], acc[u + 1], acc[u], acc[u + 1], fast_exp2(a0), fast_exp2(a1));
+    }
+}
+PKV_DEVINL float sum8(const float (&v)[8]) {
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+// The K box of tile `tile`, chunk `lane` (lanes below the tile's chunk count).
+template <int D>
+PKV_DEVINL void copy_k_tile(const PrefillWeightsArgs& a, const void* tm_k, const Item& it, int tile,
+                            uint8_t* dst, uint64_t* bar, int lane) {
+    using GM = Geom<D>;
+    const int chunks = ceil_div(it.q.c + it.q.n, kChunk);
+    const int first = tile * kBoxes;
+    const int nb = min(kBoxes, chunks - first);
+    const int chunk = first + (lane & 7);
+    const int csh = a.block_shift - 4;
+    int phys = 0;
+    if (lane < nb) {
+        phys = __ldg(a.block_tables + static_cast<size_t>(it.r) * a.max_blocks_per_seq +
+                     (chunk >> csh));
+        if (phys < 0 || phys >= a.num_blocks) {
+            raise_status(a.status, PKV_ERR_OOB);
+            phys = 0;   // keeps the byte count; the request's weights are not valid
+        }
+    }
+    __syncwarp();
+    const int row = ((phys * a.num_kv_heads + it.kvh) << a.block_shift) +
+                    (chunk & ((1 << csh) - 1)) * kChunk;
+    mbar_arrive_expect_tx_if(lane == 0, bar, nb * GM::kChunkBytes);
+    __syncwarp();
+    if constexpr (D == 128)
+        tma_load_4d_if(lane < nb, dst + lane * GM::kChunkBytes, tm_k, 0, 0, 0, row / 8, bar);
+    else
+        tma_load_2d_if(lane < nb, dst + lane * GM::kChunkBytes, tm_k, 0, row, bar);
+}
+
+// The Q tile `tile` of the window's rows.
+template <int D>
+PKV_DEVINL void copy_q_tile(const PrefillWeightsArgs& a, const void* tm_q, const Item& it, int tile,
+                            uint8_t* dst, uint64_t* bar, int lane) {
+    using GM = Geom<D>;
+    const int token = it.q.qoff + it.q.n - it.q.m + ((tile * kTile) >> a.group_shift);
+    if (lane == 0) {
+        mbar_arrive_expect_tx(bar, GM::kTileBytes);
+#pragma unroll
+        for (int h = 0; h < GM::kHalves; ++h)
+            tma_load_3d(dst + h * kHalf, tm_q, 64 * h, it.kvh << a.group_shift, token, bar);
+    }
+    __syncwarp();
+}
+
+template <int D, int PASS>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k, const PrefillWeightsArgs a) {
+    using GM = Geom<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GM::kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GM::kOffCtl);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* off = reinterpret_cast<int*>(smem + GM::kOffItems);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == kWarpA) {
+        if (lane == 0) {
+            for (int i = 0; i < GM::kBars; ++i)
+                mbar_init(&bars[i], i >= GM::S_FREE && i < GM::S_FREE + 4 ? 4 : 1);
+            *abort_flag = 0;
+            fence_mbar_init();
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+        }
+    } else if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    } else if (warp == 0) {
+        // Items per request, and their running total, 32 requests at a time.
+        int run = 0;
+        for (int r0 = 0; r0 < a.num_reqs; r0 += 32) {
+            int n = 0;
+            if (r0 + lane < a.num_reqs) {
+                const Request q = request_of(a, r0 + lane, PASS == 1 && blockIdx.x == 0);
+                if (q.rows > 0) {
+                    const int key_tiles = ceil_div(q.c + q.n, kTile);
+                    n = PASS == 1 ? (ceil_div(q.rows, kTile) + 1) / 2 *
+                                        ceil_div(key_tiles, a.chunk_tiles)
+                                  : (key_tiles + 1) / 2;
+                    n *= a.num_kv_heads;
+                }
+            }
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (r0 + lane < a.num_reqs) off[r0 + lane] = run + incl - n;
+            run += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) off[a.num_reqs] = run;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Ctl ctl{bars, abort_flag, a.status};
+    Walk<PASS> walk(a, off);
+    Item it;
+
+    if (warp == kWarpA) {
+        // ------------------------------------------------------------ A tiles
+        int i = 0, issued = 0;
+        for (; walk.next(it); ++i) {
+            const int s = i & 1;
+            if (i >= 2 && !wait_bar(ctl, GM::A_EMPTY + s, ((i >> 1) - 1) & 1)) break;
+            uint8_t* dst = smem + GM::kOffA + s * 2 * GM::kTileBytes;
+            uint64_t* bar = &bars[GM::A_FULL + s];
+            if (PASS == 1) {
+                const int token = it.q.qoff + it.q.n - it.q.m + ((it.a0 * kTile) >> a.group_shift);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, it.na * GM::kTileBytes);
+                    for (int t = 0; t < it.na; ++t)
+#pragma unroll
+                        for (int h = 0; h < GM::kHalves; ++h)
+                            tma_load_3d(dst + t * GM::kTileBytes + h * kHalf, &tm_q, 64 * h,
+                                        it.kvh << a.group_shift,
+                                        token + t * (kTile >> a.group_shift), bar);
+                }
+                __syncwarp();
+            } else {
+                // both tiles' chunks, one lane each
+                const int chunks = ceil_div(it.q.c + it.q.n, kChunk);
+                const int first = it.a0 * kBoxes;
+                const int n = min(2 * kBoxes, chunks - first);
+                const int csh = a.block_shift - 4;
+                int phys = 0;
+                if (lane < n) {
+                    phys = __ldg(a.block_tables +
+                                 static_cast<size_t>(it.r) * a.max_blocks_per_seq +
+                                 ((first + lane) >> csh));
+                    if (phys < 0 || phys >= a.num_blocks) {
+                        raise_status(a.status, PKV_ERR_OOB);
+                        phys = 0;
+                    }
+                }
+                __syncwarp();
+                const int row = ((phys * a.num_kv_heads + it.kvh) << a.block_shift) +
+                                ((first + lane) & ((1 << csh) - 1)) * kChunk;
+                mbar_arrive_expect_tx_if(lane == 0, bar, n * GM::kChunkBytes);
+                __syncwarp();
+                if constexpr (D == 128)
+                    tma_load_4d_if(lane < n, dst + lane * GM::kChunkBytes, &tm_k, 0, 0, 0, row / 8,
+                                   bar);
+                else
+                    tma_load_2d_if(lane < n, dst + lane * GM::kChunkBytes, &tm_k, 0, row, bar);
+            }
+            ++issued;
+        }
+        // every copy has landed before the CTA goes
+        for (int s = 0; s < 2; ++s)
+            if (issued > s)
+                mbar_wait_warp(&bars[GM::A_FULL + s], ((issued - 1 - s) >> 1) & 1, a.status);
+    } else if (warp == kWarpB) {
+        // ------------------------------------------------------------ B tiles
+        int g = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            for (int j = 0; j < it.nb; ++j) {
+                const int s = g % GM::kStagesB;
+                if (g >= GM::kStagesB &&
+                    !wait_bar(ctl, GM::B_EMPTY + s, (g / GM::kStagesB - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* dst = smem + GM::kOffB + s * GM::kTileBytes;
+                if (PASS == 1)
+                    copy_k_tile<D>(a, &tm_k, it, it.b0 + j, dst, &bars[GM::B_FULL + s], lane);
+                else
+                    copy_q_tile<D>(a, &tm_q, it, it.b0 + j, dst, &bars[GM::B_FULL + s], lane);
+                ++g;
+            }
+        }
+        for (int s = 0; s < GM::kStagesB; ++s)
+            if (g > s)
+                mbar_wait_warp(&bars[GM::B_FULL + s], ((g - 1 - s) / GM::kStagesB) & 1, a.status);
+    } else if (warp == kWarpMma) {
+        // ------------------------------------------------------------ MMA issuer
+        // Q tiles: 8-row atoms 1 KB apart, column halves 16 KB apart; K tiles: 8-row
+        // groups every 8 D * 2 bytes, column halves 1 KB apart.
+        constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile, false, false);
+        constexpr uint32_t hi_q = smem_desc_sw128_hi(1024);
+        constexpr uint32_t hi_k = smem_desc_sw128_hi(GM::kGroupBytes);
+        constexpr uint32_t step_q = kHalf >> 4, step_k = 1024 >> 4;
+        constexpr uint32_t hi_a = PASS == 1 ? hi_q : hi_k, hi_b = PASS == 1 ? hi_k : hi_q;
+        constexpr uint32_t step_a = PASS == 1 ? step_q : step_k;
+        constexpr uint32_t step_b = PASS == 1 ? step_k : step_q;
+        const uint32_t lo_a = smem_desc_sw128_lo(smem_u32(smem + GM::kOffA), 16);
+        const uint32_t lo_b = smem_desc_sw128_lo(smem_u32(smem + GM::kOffB), 16);
+        const bool leader = elect_one();
+        int i = 0, g = 0, used[2] = {0, 0};   // items, B tiles, tiles given to warpgroup w
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            const int sa = i & 1;
+            ok = wait_bar(ctl, GM::A_FULL + sa, (i >> 1) & 1);
+            for (int j = 0; ok && j < it.nb; ++j, ++g) {
+                const int sb = g % GM::kStagesB;
+                ok = wait_bar(ctl, GM::B_FULL + sb, (g / GM::kStagesB) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (w >= it.na) continue;
+                    const int buf = w + 2 * (used[w] & 1);
+                    if (used[w] >= 2 &&
+                        !wait_bar(ctl, GM::S_FREE + buf, ((used[w] >> 1) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t la = lo_a + (((sa * 2 + w) * GM::kTileBytes) >> 4);
+                    const uint32_t lb = lo_b + ((sb * GM::kTileBytes) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t kc = ((ks & 3) * 32) >> 4;
+                        umma_bf16_if(leader, tmem + buf * 128,
+                                     desc_join(la + (ks >> 2) * step_a + kc, hi_a),
+                                     desc_join(lb + (ks >> 2) * step_b + kc, hi_b), idesc, ks > 0);
+                    }
+                    umma_commit_if(leader, &bars[GM::S_FULL + buf]);
+                    ++used[w];
+                }
+                umma_commit_if(leader, &bars[GM::B_EMPTY + sb]);
+            }
+            umma_commit_if(leader, &bars[GM::A_EMPTY + sa]);
+            ++i;
+        }
+        // every product has completed before the TMEM goes
+        umma_commit_if(leader, &bars[GM::DRAIN]);
+        mbar_wait_warp(&bars[GM::DRAIN], 0, a.status);
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ consumers
+        const int wg = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;   // TMEM lane: query row or key of the tile
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float sl2 = a.scale_log2;
+        int used = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            if (wg >= it.na) continue;
+            const int tile = it.a0 + wg;
+            const size_t head = static_cast<size_t>(it.r) * a.num_kv_heads + it.kvh;
+            float acc[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) acc[u] = 0.f;
+            if (PASS == 1) {
+                const int rho = tile * kTile + row;
+                const int lim = it.base + (rho >> a.group_shift);        // last key seen
+                const int least = it.base + ((tile * kTile) >> a.group_shift);
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < it.nb; ++j, ++used) {
+                    const int buf = wg + 2 * (used & 1);
+                    if (!wait_bar(ctl, GM::S_FULL + buf, (used >> 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t tS = tmem + lanes + buf * 128;
+                    const int key0 = (it.b0 + j) * kTile;
+                    const int seen = lim - key0 + 1;   // the tile's keys that the row sees
+                    const bool whole = key0 + kTile - 1 <= least;
+                    auto load = [&](int q, float (&x)[32]) {
+                        tmem_ld32(tS + q * 32, x);
+                        tmem_wait_ld();
+                        if (!whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = q * 32 + e < seen ? x[e] : -INFINITY;
+                        }
+                    };
+                    auto tile_max = [&]() {
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            float x[32];
+                            load(q, x);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], x[e], x[e + 1]);
+                        }
+                        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    };
+                    auto tile_sum = [&](float ref) {
+                        float t[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) t[u] = 0.f;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float x[32];
+                            load(q, x);
+                            add_exp(x, sl2, -ref, t);
+                        }
+                        return sum8(t);
+                    };
+                    if (j == 0) {   // a tile of which the row sees nothing leaves any reference
+                        m = tile_max();
+                        if (m == -INFINITY) m = 0.f;
+                    }
+                    const float t = tile_sum(m);
+                    if (__any_sync(0xffffffffu, l + t > kSumLimit)) {
+                        // far above the reference: take the tile again from its own maximum
+                        const float mt = fmaxf(m, tile_max());
+                        if (mt > m) {
+                            l *= fast_exp2(m - mt);
+                            m = mt;
+                        }
+                        l += tile_sum(m);
+                    } else {
+                        l += t;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_if(lane == 0, &bars[GM::S_FREE + buf]);
+                }
+                if (ok && rho < it.q.rows)
+                    a.stats[(head * a.splits + it.chunk) * a.rows_pad + rho] = make_float2(m, l);
+            } else {
+                const int key = tile * kTile + row;
+                const int last = tile * kTile + kTile - 1;
+                // rows that see the key: rho >= from
+                const int from = max(0, key - it.base) << a.group_shift;
+                const int from_last = max(0, last - it.base) << a.group_shift;
+                const float* lse = a.neg_lse + head * a.rows_pad;
+                const bool there = key < it.q.c + it.q.n;
+                float* w = a.weights + (static_cast<size_t>(it.q.wrow) * a.num_kv_heads + it.kvh) *
+                                           static_cast<size_t>(a.weights_stride) + key;
+                const float before = there && a.decay != 0.f ? *w : 0.f;
+                for (int j = 0; j < it.nb; ++j, ++used) {
+                    const int buf = wg + 2 * (used & 1);
+                    if (!wait_bar(ctl, GM::S_FULL + buf, (used >> 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t tS = tmem + lanes + buf * 128;
+                    const int row0 = (it.b0 + j) * kTile;
+                    const bool whole = row0 >= from_last && row0 + kTile <= it.q.rows;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float x[32];
+                        float4 n[8];   // the rows' -lse, the same address in every lane
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            n[e] = __ldg(reinterpret_cast<const float4*>(lse + row0 + q * 32) + e);
+                        tmem_ld32(tS + q * 32, x);
+                        tmem_wait_ld();
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float a0, a1, a2, a3;
+                                ffma2(a0, a1, x[4 * e], x[4 * e + 1], sl2, sl2, n[e].x, n[e].y);
+                                ffma2(a2, a3, x[4 * e + 2], x[4 * e + 3], sl2, sl2, n[e].z, n[e].w);
+                                const int u = 4 * (e & 1);
+                                fadd2(acc[u], acc[u + 1], acc[u], acc[u + 1], fast_exp2(a0),
+                                      fast_exp2(a1));
+                                fadd2(acc[u + 2], acc[u + 3], acc[u + 2], acc[u + 3],
+                                      fast_exp2(a2), fast_exp2(a3));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float nn[4] = {n[e].x, n[e].y, n[e].z, n[e].w};
+#pragma unroll
+                                for (int f = 0; f < 4; ++f) {
+                                    const int rho = row0 + q * 32 + 4 * e + f;
+                                    const bool on = rho >= from && rho < it.q.rows;
+                                    acc[f] += on ? fast_exp2(fmaf(x[4 * e + f], sl2, nn[f])) : 0.f;
+                                }
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_if(lane == 0, &bars[GM::S_FREE + buf]);
+                }
+                if (ok && there) {
+                    const float t = sum8(acc);
+                    *w = a.decay != 0.f ? fmaf(a.decay, before, t) : t;
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// -log2 of a row's sum over its chunks, and -inf for the rows that pad the last tile.
+// Grid (row blocks, kv head, request).
+__global__ void __launch_bounds__(128)
+merge_stats_kernel(const PrefillWeightsArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rho = blockIdx.x * 128 + threadIdx.x;
+    const Request q = request_of(a, blockIdx.z, false);
+    if (q.rows == 0 || blockIdx.x * 128 >= q.rows) return;
+    const size_t head = static_cast<size_t>(blockIdx.z) * a.num_kv_heads + blockIdx.y;
+    float neg = -INFINITY;
+    if (rho < q.rows) {
+        // the chunks of the row's tile pair: those up to the last key that the pair sees
+        const int pair_last = min((rho / 256 + 1) * 256, q.rows) - 1;
+        const int last_key = q.c + q.n - q.m + (pair_last >> a.group_shift);
+        const int chunks = last_key / kTile / a.chunk_tiles + 1;
+        const float2* st = a.stats + head * a.splits * a.rows_pad + rho;
+        float M = -INFINITY;
+        for (int z = 0; z < chunks; ++z) {
+            const float2 f = st[static_cast<size_t>(z) * a.rows_pad];
+            if (f.y != 0.f) M = fmaxf(M, f.x);   // 0: a chunk the row sees nothing of
+        }
+        float l = 0.f;
+        for (int z = 0; z < chunks; ++z) {
+            const float2 f = st[static_cast<size_t>(z) * a.rows_pad];
+            if (f.y != 0.f) l += f.y * fast_exp2(f.x - M);
+        }
+        neg = -(M + log2f(l));
+    }
+    a.neg_lse[head * a.rows_pad + rho] = neg;
+}
+
+// Streaming multiprocessors of the current device.
+int sm_count() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    int v = cached[dev].load(std::memory_order_relaxed);
+    if (v <= 0) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+            return 1;
+        cached[dev].store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
+
+template <int D>
+cudaError_t launch_d(PrefillWeightsArgs a, int group, cudaStream_t stream) {
+    using GM = Geom<D>;
+    a.group_shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
+    CUtensorMap mq, mk;
+    const int64_t rows = (a.num_blocks * a.num_kv_heads) << a.block_shift;
+    const bool ok = D == 128 ? make_pool_block_map(&mk, a.k_pool, rows)
+                             : make_pool_map(&mk, a.k_pool, rows, D);
+    if (!ok || !make_q_group_map(&mq, a.q, a.total_new, a.num_q_heads, D, group, kTile / group))
+        return cudaErrorInvalidValue;
+    auto pass1 = prefill_weights_kernel<D, 1>;
+    auto pass2 = prefill_weights_kernel<D, 2>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(pass1), GM::kBytes);
+    if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void*>(pass2), GM::kBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t row_tiles = (static_cast<int64_t>(a.max_rows) * group + kTile - 1) / kTile;
+    const int64_t key_pairs = (static_cast<int64_t>(a.max_context) + 2 * kTile - 1) / (2 * kTile);
+    // Up to kMaxReqs requests per round of launches (their item offsets sit in shared memory).
+    const int total = a.num_reqs;
+    for (int r0 = 0; r0 < total; r0 += kMaxReqs) {
+        PrefillWeightsArgs g = a;
+        g.num_reqs = total - r0 < kMaxReqs ? total - r0 : kMaxReqs;
+        g.block_tables += static_cast<size_t>(r0) * a.max_blocks_per_seq;
+        g.cached_lens += r0;
+        g.new_lens += r0;
+        g.q_offsets += r0;
+        if (a.row_ids) {
+            g.row_ids += r0;
+        } else {
+            g.weights += static_cast<size_t>(r0) * a.num_kv_heads * a.weights_stride;
+            g.num_rows -= r0;
+        }
+        const int64_t heads = static_cast<int64_t>(g.num_reqs) * a.num_kv_heads;
+        const int64_t items1 = heads * ((row_tiles + 1) / 2) * a.splits;
+        const int64_t items2 = heads * key_pairs;
+        if (items1 > INT32_MAX || items2 > INT32_MAX) return cudaErrorNotSupported;
+        const int sms = sm_count();
+        e = launch_pdl(pass1, dim3(static_cast<unsigned>(items1 < sms ? items1 : sms)),
+                       dim3(kThreads), GM::kBytes, stream, mq, mk, g);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(merge_stats_kernel,
+                       dim3(static_cast<unsigned>(row_tiles), a.num_kv_heads, g.num_reqs),
+                       dim3(128), 0, stream, g);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(pass2, dim3(static_cast<unsigned>(items2 < sms ? items2 : sms)),
+                       dim3(kThreads), GM::kBytes, stream, mq, mk, g);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, int head_dim, int group,
+                                      cudaStream_t stream) {
+    return head_dim == 128 ? launch_d<128>(a, group, stream) : launch_d<64>(a, group, stream);
+}
+
+}  // namespace pkv
