@@ -224,7 +224,8 @@ struct PrefillWeightsArgs {
     const int32_t* q_offsets;
     const int32_t* row_ids;   // weight row of each request (null: its index)
     float* weights;           // [num_rows][Hkv][weights_stride]
-    float2* stats;            // workspace: (reference, sum) [R][Hkv][splits][rows_pad]
+    float2* stats;            // workspace: (reference, sum) [R][Hkv][splits][rows_pad];
+                              // tensor cores: two of them, [..][splits][2][rows_pad]
     float* neg_lse;           // workspace (tensor cores): -log2(sum 2^s) [R][Hkv][rows_pad]
     int* status;
     int64_t num_blocks;

@@ -1158,15 +1158,17 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
                          (num_q_heads / pool->num_kv_heads);
     if (rows > INT32_MAX - 128) return false;
     p->rows_pad = static_cast<int>((rows + 127) / 128 * 128);
-    // Enough parts that about eight items per SM exist where there are few query tiles (the
-    // lengths are not known here, only their bound); a part has at least 8 tiles of 128 keys.
+    // Items of at most 16 tiles of 128 keys, so that CTAs that walk a dozen of them end
+    // together; smaller ones, down to 8 tiles, while there are fewer than 16 items per SM (the
+    // lengths are not known here, only their bound); larger ones past 256 parts.
     const int64_t heads = static_cast<int64_t>(num_reqs) * pool->num_kv_heads;
     const int64_t items = heads * ((p->rows_pad / 128 + 1) / 2);
     const int tiles = ceil_div(max_context, 128);
-    const int64_t want = std::min<int64_t>((8 * 152 + items - 1) / items, 64);
-    p->chunk_tiles = std::max(8, ceil_div(tiles, want));
+    const int64_t want = (16 * 152 + items - 1) / items;
+    p->chunk_tiles = std::min(16, std::max(8, ceil_div(tiles, want)));
+    p->chunk_tiles = std::max(p->chunk_tiles, ceil_div(tiles, 256));
     p->splits = ceil_div(tiles, p->chunk_tiles);
-    p->stats_bytes = static_cast<size_t>(heads) * p->splits * p->rows_pad * sizeof(float2);
+    p->stats_bytes = static_cast<size_t>(heads) * p->splits * 2 * p->rows_pad * sizeof(float2);
     p->bytes = p->stats_bytes + static_cast<size_t>(heads) * p->rows_pad * sizeof(float);
     return true;
 }

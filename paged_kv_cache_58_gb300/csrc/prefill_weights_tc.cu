@@ -9,8 +9,10 @@
 // TMEM lanes: a thread owns a query row (pass 1) or a key (pass 2) and reduces over its
 // own registers, with no exchange between threads in either pass.  An item holds up to
 // two A tiles (256 rows or keys) and streams B tiles past them; every B tile staged
-// serves both, which halves the copies per product.  Warpgroup a of the two consumer
-// warpgroups takes A tile a, in two TMEM buffers of 128 columns each (all 512 columns).
+// serves both, which halves the copies per product.  Each A tile has two TMEM buffers of
+// 128 columns (all 512 columns) and two consumer warpgroups, one per half of the columns:
+// with 16 consumer warps a scheduler has four to switch between while loads from TMEM,
+// exponentials and barriers are under way (8 warps took 1.4 times as long).
 //
 // Pass 1 keeps the maximum of a row's first tile of the item as its reference and adds
 // 2^(s - m) from there on without looking for a larger one: there is no accumulator to
@@ -23,7 +25,8 @@
 //
 // Persistent CTAs, one per SM, each walking every gridDim.x-th item: producers run ahead
 // into the next item's tiles while the consumers finish the current one.  Roles: warps
-// 0-3 and 4-7 consumers, warp 8 A tiles, warp 9 B tiles, warp 10 MMA and TMEM.
+// 0-3 and 4-7 consumers, warp 8 A tiles, warp 9 B tiles, warp 10 MMA and TMEM, warp 11 the
+// B rows' -lse (pass 2).
 #include <atomic>
 
 #include <cuda.h>
@@ -41,9 +44,11 @@ constexpr int kTile = 128;
 constexpr int kChunk = 16;          // tokens per TMA box of K
 constexpr int kBoxes = kTile / kChunk;
 constexpr int kHalf = kTile * 128;  // a 64-column half of a Q tile: 16 KB
-constexpr int kThreads = 384;
-constexpr int kWarpA = 8, kWarpB = 9, kWarpMma = 10;
-constexpr int kMaxReqs = 384;       // requests per launch (the item offsets in shared memory)
+constexpr int kThreads = 640;
+constexpr int kConsumers = 16;      // warps
+constexpr int kWarpA = 16, kWarpB = 17, kWarpMma = 18, kWarpL = 19;
+constexpr int kMaxReqs = 256;       // requests per launch (the item offsets in shared memory)
+constexpr int kStagesL = 3;         // tiles of -lse staged (pass 2), 512 B each
 constexpr float kSumLimit = 7.9e28f;   // 2^96
 
 template <int D>
@@ -56,14 +61,19 @@ struct Geom {
     static constexpr int kOffA = 0;                   // two pairs of tiles
     static constexpr int kOffB = 4 * kTileBytes;
     static constexpr int kOffBar = kOffB + kStagesB * kTileBytes;
-    static constexpr int kBars = 2 + 2 + 2 * kStagesB + 4 + 4 + 1;
-    static constexpr int kOffCtl = kOffBar + kBars * 8;          // TMEM address, abort flag
-    static constexpr int kOffItems = kOffCtl + 16;
-    static constexpr int kBytes = kOffItems + (kMaxReqs + 1) * 4 + 1024;   // + align slack
     // barriers
     static constexpr int A_FULL = 0, A_EMPTY = 2, B_FULL = 4, B_EMPTY = 4 + kStagesB,
-                         S_FULL = 4 + 2 * kStagesB, S_FREE = S_FULL + 4, DRAIN = S_FREE + 4;
+                         S_FULL = 4 + 2 * kStagesB, S_FREE = S_FULL + 4, L_FULL = S_FREE + 4,
+                         L_EMPTY = L_FULL + kStagesL, X_FULL = L_EMPTY + kStagesL,
+                         DRAIN = X_FULL + 16;
+    static constexpr int kBars = DRAIN + 1;
+    static constexpr int kOffL = kOffBar + (kBars * 8 + 15) / 16 * 16;
+    static constexpr int kOffCtl = kOffL + kStagesL * kTile * 4;   // TMEM address, abort flag
+    static constexpr int kOffItems = kOffCtl + 16;
+    static constexpr int kBytes = kOffItems + (kMaxReqs + 1) * 4;
 };
+// One CTA fills an SM; there is no room for slack to align by, so the kernel relies on the
+// dynamic shared memory starting on a 1 KB boundary (there is no static) and checks it.
 static_assert(Geom<128>::kBytes <= 232448, "shared memory of one SM");
 
 struct Ctl {
@@ -235,9 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const PrefillWeightsArgs a) {
     using GM = Geom<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GM::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GM::kOffCtl);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -247,10 +255,17 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
 
     griddep_wait();
     griddep_launch_dependents();
+    if (smem_u32(smem) & 1023u) {   // the swizzled tiles would not lie as their copies assume
+        if (threadIdx.x == 0) raise_status(a.status, PKV_ERR_UNSUPPORTED);
+        return;
+    }
     if (warp == kWarpA) {
         if (lane == 0) {
-            for (int i = 0; i < GM::kBars; ++i)
-                mbar_init(&bars[i], i >= GM::S_FREE && i < GM::S_FREE + 4 ? 4 : 1);
+            for (int i = 0; i < GM::kBars; ++i)   // arrivals: an A tile's consumers, all of them, 1
+                mbar_init(&bars[i],
+                          i >= GM::S_FREE && i < GM::S_FREE + 4 ? kConsumers / 2
+                          : i >= GM::L_EMPTY && i < GM::L_EMPTY + kStagesL ? kConsumers
+                                                                           : 1);
             *abort_flag = 0;
             fence_mbar_init();
             prefetch_tmap(&tm_q);
@@ -422,37 +437,66 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
         // every product has completed before the TMEM goes
         umma_commit_if(leader, &bars[GM::DRAIN]);
         mbar_wait_warp(&bars[GM::DRAIN], 0, a.status);
-    } else if (warp < 8) {
+    } else if (warp == kWarpL) {
+        // ------------------------------------------------------------ -lse of the B rows
+        if (PASS == 2) {
+            int g = 0;
+            bool ok = true;
+            while (ok && walk.next(it)) {
+                const float* lse = a.neg_lse +
+                                   (static_cast<size_t>(it.r) * a.num_kv_heads + it.kvh) *
+                                       a.rows_pad;
+                for (int j = 0; j < it.nb; ++j) {
+                    const int s = g % kStagesL;
+                    if (g >= kStagesL && !wait_bar(ctl, GM::L_EMPTY + s, (g / kStagesL - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars[GM::L_FULL + s], kTile * 4);
+                        bulk_g2s(smem + GM::kOffL + s * kTile * 4, lse + (it.b0 + j) * kTile,
+                                 kTile * 4, &bars[GM::L_FULL + s]);
+                    }
+                    __syncwarp();
+                    ++g;
+                }
+            }
+            for (int s = 0; s < kStagesL; ++s)
+                if (g > s)
+                    mbar_wait_warp(&bars[GM::L_FULL + s], ((g - 1 - s) / kStagesL) & 1, a.status);
+        }
+    } else if (warp < kConsumers) {
         // ------------------------------------------------------------ consumers
-        const int wg = warp >> 2;
-        const int row = (warp & 3) * 32 + lane;   // TMEM lane: query row or key of the tile
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int wg = (warp >> 2) & 1;           // A tile of the item
+        const int half = warp >> 3;               // columns 64 half .. 64 half + 63
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;      // TMEM lane: query row or key of the tile
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const float sl2 = a.scale_log2;
-        int used = 0;
+        int used = 0, gl = 0;   // tiles of this A tile's consumers; tiles of -lse
+        uint32_t met_phase[2] = {0, 0};
         bool ok = true;
         while (ok && walk.next(it)) {
-            if (wg >= it.na) continue;
             const int tile = it.a0 + wg;
+            const bool mine = wg < it.na;
             const size_t head = static_cast<size_t>(it.r) * a.num_kv_heads + it.kvh;
-            float acc[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) acc[u] = 0.f;
             if (PASS == 1) {
+                if (!mine) continue;
                 const int rho = tile * kTile + row;
                 const int lim = it.base + (rho >> a.group_shift);        // last key seen
                 const int least = it.base + ((tile * kTile) >> a.group_shift);
-                float m = -INFINITY, l = 0.f;
+                float m = 0.f, l = 0.f;
                 for (int j = 0; j < it.nb; ++j, ++used) {
                     const int buf = wg + 2 * (used & 1);
                     if (!wait_bar(ctl, GM::S_FULL + buf, (used >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t tS = tmem + lanes + buf * 128;
-                    const int key0 = (it.b0 + j) * kTile;
-                    const int seen = lim - key0 + 1;   // the tile's keys that the row sees
-                    const bool whole = key0 + kTile - 1 <= least;
+                    const uint32_t tS = tmem + lanes + buf * 128 + 64 * half;
+                    const int key0 = (it.b0 + j) * kTile + 64 * half;
+                    const int seen = lim - key0 + 1;   // the columns that the row sees
+                    const bool whole = key0 + 63 <= least;
                     auto load = [&](int q, float (&x)[32]) {
                         tmem_ld32(tS + q * 32, x);
-                        tmem_wait_ld();
+                        tmem_wait_ld32(x);
                         if (!whole) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
@@ -462,7 +506,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                     auto tile_max = [&]() {
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             float x[32];
                             load(q, x);
 #pragma unroll
@@ -476,7 +520,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
                         for (int u = 0; u < 8; ++u) t[u] = 0.f;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             float x[32];
                             load(q, x);
                             add_exp(x, sl2, -ref, t);
@@ -504,67 +548,100 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                     mbar_arrive_if(lane == 0, &bars[GM::S_FREE + buf]);
                 }
                 if (ok && rho < it.q.rows)
-                    a.stats[(head * a.splits + it.chunk) * a.rows_pad + rho] = make_float2(m, l);
+                    a.stats[((head * a.splits + it.chunk) * 2 + half) * a.rows_pad + rho] =
+                        make_float2(m, l);
             } else {
                 const int key = tile * kTile + row;
                 const int last = tile * kTile + kTile - 1;
                 // rows that see the key: rho >= from
                 const int from = max(0, key - it.base) << a.group_shift;
                 const int from_last = max(0, last - it.base) << a.group_shift;
-                const float* lse = a.neg_lse + head * a.rows_pad;
-                const bool there = key < it.q.c + it.q.n;
+                const bool there = mine && half == 0 && key < it.q.c + it.q.n;
                 float* w = a.weights + (static_cast<size_t>(it.q.wrow) * a.num_kv_heads + it.kvh) *
                                            static_cast<size_t>(a.weights_stride) + key;
                 const float before = there && a.decay != 0.f ? *w : 0.f;
-                for (int j = 0; j < it.nb; ++j, ++used) {
-                    const int buf = wg + 2 * (used & 1);
-                    if (!wait_bar(ctl, GM::S_FULL + buf, (used >> 1) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t tS = tmem + lanes + buf * 128;
-                    const int row0 = (it.b0 + j) * kTile;
-                    const bool whole = row0 >= from_last && row0 + kTile <= it.q.rows;
+                float acc[8], total = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float x[32];
-                        float4 n[8];   // the rows' -lse, the same address in every lane
+                for (int u = 0; u < 8; ++u) acc[u] = 0.f;
+                for (int j = 0; j < it.nb; ++j, ++gl) {
+                    const int sl = gl % kStagesL;
+                    if (!wait_bar(ctl, GM::L_FULL + sl, (gl / kStagesL) & 1)) { ok = false; break; }
+                    if (mine) {
+                        const int buf = wg + 2 * (used & 1);
+                        const uint32_t phase = (used >> 1) & 1;
+                        if (!wait_bar(ctl, GM::S_FULL + buf, phase)) { ok = false; break; }
+                        ++used;
+                        tc_fence_after();
+                        const uint32_t tS = tmem + lanes + buf * 128;
+                        const int row0 = (it.b0 + j) * kTile + 64 * half;
+                        const bool whole = row0 >= from_last && row0 + 64 <= it.q.rows;
+                        // the rows' -lse, the same address in every lane
+                        const float4* n4 = reinterpret_cast<const float4*>(
+                            smem + GM::kOffL + sl * kTile * 4 + 256 * half);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            n[e] = __ldg(reinterpret_cast<const float4*>(lse + row0 + q * 32) + e);
-                        tmem_ld32(tS + q * 32, x);
-                        tmem_wait_ld();
-                        if (whole) {
+                        for (int q = 0; q < 2; ++q) {
+                            float x[32];
+                            tmem_ld32(tS + 64 * half + q * 32, x);
+                            tmem_wait_ld32(x);
+                            if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float a0, a1, a2, a3;
-                                ffma2(a0, a1, x[4 * e], x[4 * e + 1], sl2, sl2, n[e].x, n[e].y);
-                                ffma2(a2, a3, x[4 * e + 2], x[4 * e + 3], sl2, sl2, n[e].z, n[e].w);
-                                const int u = 4 * (e & 1);
-                                fadd2(acc[u], acc[u + 1], acc[u], acc[u + 1], fast_exp2(a0),
-                                      fast_exp2(a1));
-                                fadd2(acc[u + 2], acc[u + 3], acc[u + 2], acc[u + 3],
-                                      fast_exp2(a2), fast_exp2(a3));
-                            }
-                        } else {
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 n = n4[q * 8 + e];
+                                    float a0, a1, a2, a3;
+                                    ffma2(a0, a1, x[4 * e], x[4 * e + 1], sl2, sl2, n.x, n.y);
+                                    ffma2(a2, a3, x[4 * e + 2], x[4 * e + 3], sl2, sl2, n.z, n.w);
+                                    const int u = 4 * (e & 1);
+                                    fadd2(acc[u], acc[u + 1], acc[u], acc[u + 1], fast_exp2(a0),
+                                          fast_exp2(a1));
+                                    fadd2(acc[u + 2], acc[u + 3], acc[u + 2], acc[u + 3],
+                                          fast_exp2(a2), fast_exp2(a3));
+                                }
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float nn[4] = {n[e].x, n[e].y, n[e].z, n[e].w};
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 n = n4[q * 8 + e];
+                                    const float nn[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
-                                for (int f = 0; f < 4; ++f) {
-                                    const int rho = row0 + q * 32 + 4 * e + f;
-                                    const bool on = rho >= from && rho < it.q.rows;
-                                    acc[f] += on ? fast_exp2(fmaf(x[4 * e + f], sl2, nn[f])) : 0.f;
+                                    for (int f = 0; f < 4; ++f) {
+                                        const int rho = row0 + q * 32 + 4 * e + f;
+                                        const bool on = rho >= from && rho < it.q.rows;
+                                        acc[f] +=
+                                            on ? fast_exp2(fmaf(x[4 * e + f], sl2, nn[f])) : 0.f;
+                                    }
                                 }
                             }
                         }
+                        if (j + 1 == it.nb) {
+                            // The two halves' sums of a key meet: half 1 leaves its own in a
+                            // column of the tile's buffer that it has read, half 0 takes it
+                            // from there before the buffer is given back.
+                            uint64_t* met = &bars[GM::X_FULL + buf * 4 + quarter];
+                            total = sum8(acc);
+                            if (half == 1) {
+                                tmem_st1(tS + 127, total);
+                                tmem_wait_st();
+                                tc_fence_before();
+                                __syncwarp();
+                                mbar_arrive_if(lane == 0, met);
+                            } else {
+                                if (!wait_bar(ctl, GM::X_FULL + buf * 4 + quarter,
+                                              met_phase[(buf >> 1)])) {
+                                    ok = false;
+                                    break;
+                                }
+                                met_phase[(buf >> 1)] ^= 1;
+                                tc_fence_after();
+                                total += tmem_ld1(tS + 127);
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        mbar_arrive_if(lane == 0, &bars[GM::S_FREE + buf]);
                     }
-                    tc_fence_before();
                     __syncwarp();
-                    mbar_arrive_if(lane == 0, &bars[GM::S_FREE + buf]);
+                    mbar_arrive_if(lane == 0, &bars[GM::L_EMPTY + sl]);
                 }
-                if (ok && there) {
-                    const float t = sum8(acc);
-                    *w = a.decay != 0.f ? fmaf(a.decay, before, t) : t;
-                }
+                if (ok && there) *w = a.decay != 0.f ? fmaf(a.decay, before, total) : total;
             }
         }
     }
@@ -593,8 +670,8 @@ merge_stats_kernel(const PrefillWeightsArgs a) {
         // the chunks of the row's tile pair: those up to the last key that the pair sees
         const int pair_last = min((rho / 256 + 1) * 256, q.rows) - 1;
         const int last_key = q.c + q.n - q.m + (pair_last >> a.group_shift);
-        const int chunks = last_key / kTile / a.chunk_tiles + 1;
-        const float2* st = a.stats + head * a.splits * a.rows_pad + rho;
+        const int chunks = 2 * (last_key / kTile / a.chunk_tiles + 1);   // two halves each
+        const float2* st = a.stats + head * a.splits * 2 * a.rows_pad + rho;
         float M = -INFINITY;
         for (int z = 0; z < chunks; ++z) {
             const float2 f = st[static_cast<size_t>(z) * a.rows_pad];

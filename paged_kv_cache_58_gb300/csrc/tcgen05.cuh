@@ -148,6 +148,35 @@ PKV_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&u)[16]) {
         : "memory");
 }
 
+// One column of this thread's lane.
+PKV_DEVINL void tmem_st1(uint32_t taddr, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
+                 "r"(__float_as_uint(v))
+                 : "memory");
+}
+PKV_DEVINL float tmem_ld1(uint32_t taddr) {   // complete when it returns
+    uint32_t u;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(u)
+        : "r"(taddr)
+        : "memory");
+    return __uint_as_float(u);
+}
+
+// Wait for this thread's TMEM loads, tied to the registers of one of them: whatever uses
+// them comes after the wait (for loads issued ahead of other work).
+PKV_DEVINL void tmem_wait_ld32(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                   "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                   "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]),
+                   "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                   "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                   "+f"(r[30]), "+f"(r[31])
+                 :
+                 : "memory");
+}
 PKV_DEVINL void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 PKV_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
