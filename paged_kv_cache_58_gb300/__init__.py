@@ -556,49 +556,62 @@ def paged_prefill(q, k_pool, v_pool, block_tables, cached_lens, new_lens, q_offs
     return out
 
 
-def _arg(t: torch.Tensor, name: str, dev, dtype, shape) -> int:
-    """Address of a contiguous tensor that must be of this device, dtype and shape."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}, the pools' and current device")
-    if t.dtype != dtype:
+# The raw handle of the current stream of a device, and the current device, without the
+# Python objects around them: a decode step's calls are a few microseconds each.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _wrong(t, name, dev, dtype, shape):
+    """The error for a tensor that `_arg` refuses."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}, the current device")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name: str, dev, dtype, shape):
+def _arg(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
+    """Address of a contiguous tensor that must be of this device, dtype and shape."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _wrong(t, name, dev, dtype, shape)
+
+
+def _opt(t, name: str, dev: int, dtype, shape):
     return None if t is None else _arg(t, name, dev, dtype, shape)
 
 
-def _rows_arg(t: torch.Tensor, name: str, dev, dtype, shape):
+def _rows_arg(t: torch.Tensor, name: str, dev: int, dtype, shape):
     """(address, token stride) of [tokens, heads, head_dim] rows whose tokens may be apart
     (a slice of a fused projection)."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}, the current device")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _wrong(t, name, dev, dtype, shape)
     tokens, heads, dim = shape
-    st = t.stride()
     if tokens == 0 or heads == 0:
         return t.data_ptr(), heads * dim
-    if st[2] != 1 or (heads > 1 and st[1] != dim):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (st[0] if tokens > 1 else heads * dim)
+    return t.data_ptr(), (s0 if tokens > 1 else heads * dim)
 
 
-def _device(t: torch.Tensor, name: str):
+def _device(t: torch.Tensor, name: str) -> int:
     """The CUDA device of the call: `t`'s, which must be the current one (the library's
     streams and status word are the current device's)."""
-    dev = t.device
-    if dev.type != "cuda":
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, not on the current device")
+    if dev != _cur_device():
+        raise ValueError(f"{name} is on cuda:{dev}, not on the current device")
     return dev
 
 
@@ -606,29 +619,28 @@ def _fresh(shape, dtype, dev, stream):
     """A tensor the call writes, allocated on the stream that will use it, so that its memory
     is not handed on while that stream still works in it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device="cuda")
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device="cuda")
 
 
 def _workspace_arg(ws, need, dev, stream):
     """(tensor, address, bytes) of the given workspace, or of one made here."""
     if ws is None:
         ws = _fresh((max(need(), 16),), torch.uint8, dev, stream)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _pools(k_pool, v_pool):
     """(descriptor, device, K address, V address) of a pair of pools."""
-    if k_pool.dim() != 4:
+    dev, dt, shape = _device(k_pool, "k_pool"), k_pool.dtype, k_pool.shape
+    if len(shape) != 4:
         raise ValueError("k_pool must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    dev = _device(k_pool, "k_pool")
-    shape = k_pool.shape
-    return (pool_desc(k_pool), dev, _arg(k_pool, "k_pool", dev, k_pool.dtype, shape),
-            _arg(v_pool, "v_pool", dev, k_pool.dtype, shape))
+    return (pool_desc(k_pool), dev, _arg(k_pool, "k_pool", dev, dt, shape),
+            _arg(v_pool, "v_pool", dev, dt, shape))
 
 
 def _weights_arg(weights, dev, dtype, hkv, name="weights"):
@@ -682,7 +694,7 @@ def rope(x, positions, inv_freq, *, interleaved=False, inverse=False, attn_scale
     st = _load().pkv_rope(_dtype_code(x), op, os_, xp, xs,
                           _arg(positions, "positions", dev, torch.int32, (T,)),
                           _arg(inv_freq, "inv_freq", dev, torch.float64, (half,)), 2 * half,
-                          bool(interleaved), bool(inverse), attn_scale, T, H, D, _stream(stream))
+                          bool(interleaved), bool(inverse), attn_scale, T, H, D, _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_rope", st)
     return out
@@ -710,7 +722,7 @@ def rope_append(q, k, v, k_pool, v_pool, slot_mapping, positions, inv_freq, *, i
                                  os_, qp, qs, kr, ks, vr, vs,
                                  _arg(positions, "positions", dev, torch.int32, (T,)),
                                  _arg(inv_freq, "inv_freq", dev, torch.float64, (half,)),
-                                 2 * half, bool(interleaved), attn_scale, T, Hq, _stream(stream))
+                                 2 * half, bool(interleaved), attn_scale, T, Hq, _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_rope_append", st)
     return q_out
@@ -749,7 +761,7 @@ def paged_decode_weights(q, k_pool, v_pool, block_tables, context_lens, scale, w
         _arg(block_tables, "block_tables", dev, torch.int32, (S, block_tables.shape[1])),
         block_tables.shape[1], _arg(context_lens, "context_lens", dev, torch.int32, (S,)),
         max_context, S, Hq, scale, partition_blocks, wp, stride,
-        _opt(row_ids, "row_ids", dev, torch.int32, (S,)), rows, decay, ws, wsb, _stream(stream))
+        _opt(row_ids, "row_ids", dev, torch.int32, (S,)), rows, decay, ws, wsb, _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_paged_decode_weights", st)
     return out
@@ -788,7 +800,7 @@ def paged_prefill_weights(q, k_pool, block_tables, cached_lens, new_lens, q_offs
         _arg(new_lens, "new_lens", dev, torch.int32, (R,)),
         _arg(q_offsets, "q_offsets", dev, torch.int32, (R + 1,)), R, N, max_new, max_context, Hq,
         scale, window, wp, stride, _opt(row_ids, "row_ids", dev, torch.int32, (R,)), rows, decay,
-        ws, wsb, _stream(stream))
+        ws, wsb, _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_paged_prefill_weights", st)
     return weights
@@ -833,7 +845,7 @@ def evict(k_pool, v_pool, block_tables, context_lens, budgets, weights, position
         _opt(seen_lens, "seen_lens", dev, i32, one),
         _opt(tracked_lens, "tracked_lens", dev, i32, one), wp, wo, pp, po, stride,
         _opt(row_ids, "row_ids", dev, i32, one), rows, _arg(new_lens, "new_lens", dev, i32, one),
-        ws, wsb, _stream(stream))
+        ws, wsb, _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_evict", st)
     return new_lens

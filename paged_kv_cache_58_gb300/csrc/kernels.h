@@ -270,7 +270,7 @@ struct EvictArgs {
     const int32_t* positions;
     int32_t* positions_out;
     int32_t* new_lens;
-    int32_t* moves;   // workspace: [S][Hkv][max_context]
+    int32_t* moves;   // workspace: [S][Hkv][4][max_context / 2]
     int* status;
     int64_t num_blocks;
     int64_t weights_stride;
@@ -280,7 +280,7 @@ struct EvictArgs {
     int max_context;
     int num_seqs;
     int num_kv_heads;
-    int row_bytes;
+    int row_shift;   // log2 of a row's 16-byte chunks
     int sinks;
     int recent;
 };

@@ -1270,7 +1270,8 @@ bool same_or_apart(const void* a, const void* b, uint64_t bytes) {
 
 size_t pkv_evict_workspace_bytes(const pkv_pool_desc* pool, int num_seqs, int max_context) {
     if (check_pool(pool) != PKV_OK || num_seqs <= 0 || max_context <= 0) return 0;
-    return static_cast<size_t>(num_seqs) * pool->num_kv_heads * max_context * sizeof(int32_t);
+    return static_cast<size_t>(num_seqs) * pool->num_kv_heads * 4 *
+           static_cast<size_t>(std::max(max_context / 2, 1)) * sizeof(int32_t);
 }
 
 pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
@@ -1333,7 +1334,8 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
     a.max_context = max_context;
     a.num_seqs = num_seqs;
     a.num_kv_heads = pool->num_kv_heads;
-    a.row_bytes = pool->head_dim * elem_bytes(pool->dtype);
+    const int chunks = pool->head_dim * elem_bytes(pool->dtype) / 16;   // 8, 16 or 32
+    a.row_shift = chunks == 8 ? 3 : chunks == 16 ? 4 : 5;
     a.sinks = sinks;
     a.recent = recent;
     return from_cuda(pkv::launch_evict(a, static_cast<cudaStream_t>(stream)));
