@@ -475,6 +475,7 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
  * ones, in any order.  Afterwards the blocks past ceil(new_lens[s] / B) are free to return
  * (pkv_alloc_truncate), and new tokens append at index new_lens[s].
  *   context_lens  device int32 [num_seqs], cached tokens L (<= max_context); 0: nothing to do.
+ *   max_context   host upper bound of context_lens, at most 2^20 (PKV_ERR_UNSUPPORTED).
  *   budgets       device int32 [num_seqs]; negative: no limit.
  *   positions     device int32 [num_rows][num_kv_heads][weights_stride]: original positions of
  *                 the entries [0, tracked_lens[s]).  Entries from there on are the newest in

@@ -10,20 +10,25 @@
 // and sources (past the budget) and destinations (below it) never overlap.
 //
 // A row (sequence, kv head) is one cluster of C CTAs, each with a slice of its entries:
-//   1. weights -> 32-bit keys whose unsigned order is theirs, into shared memory, with a
-//      bit per entry for its class; the protected are counted.  Either all of them are
-//      kept and the others compete for what is left of the budget, or they alone do.
-//   2. radix select of the threshold among the competing class, 11 + 11 + 10 bits: a
-//      histogram of the entries that match the digits found so far, equal digits of a
-//      warp added at once (weights crowd into few exponents: one atomic per entry spent
-//      most of a pass waiting on the same counter); it ends early when a bin is kept whole.
-//   3. places: freed ones below the budget and kept ones past it are numbered by scans
-//      over the threads' contiguous segments and written to two lists, a mover with its
-//      weight and position, so that its old entry can be cleared at once.
+//   1. one scan over the weights: a bit per entry for its class, the protected counted, and
+//      a histogram of the others' first digit.  Weights become 32-bit keys whose unsigned
+//      order is theirs; a radix select narrows the threshold by 11 + 11 + 10 bits.  Either
+//      all protected entries are kept and the others compete for what is left of the
+//      budget, or (rarely: then the histogram is made again) the protected alone do.
+//   2. a second scan decides every entry outside the threshold's first bin, and lists the
+//      few inside it; the other digits and the rest of the decisions come from that list.
+//      (Where it overflows, as with many equal weights, from scans of the slice.)  The
+//      select ends early when a bin is kept whole.
+//   3. freed places below the budget and kept entries past it are counted and numbered 32 at
+//      a time, a thread per word of the bits, and written to two lists, a mover with its
+//      weight and position, so that its old entry is cleared in the same scan.
 //   4. after one cluster barrier all threads copy the listed rows, 16 bytes of K and of V
-//      per lane, four rows in flight per lane.
-// With C = 1 there are no cluster barriers.  Entries past the shared-memory capacity of a
-// slice are looked at in global memory again in each step.
+//      per lane, four rows in flight per lane and the places of the next four looked up
+//      meanwhile.
+// With C = 1 there are no cluster barriers.  The scans read the weights where they are, in
+// L2 after the first: keys kept in shared memory left two CTAs on an SM and a row's
+// latencies uncovered, where without them six fit.  Weights crowd into few exponents (and
+// many may be zero): the lanes that share the first lane's digit count at once.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -36,9 +41,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+constexpr int NT = 256;              // threads
+constexpr int kWarps = NT / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kCapEntries = 32768;   // entries of a slice held in shared memory, at most
+constexpr int kList = 1024;          // entries of the threshold's bin listed per CTA
 
 // Unsigned order of the result = order of the weights; -0 equals +0, NaN ranks last.
 PKV_DEVINL uint32_t order_key(float w) {
@@ -47,51 +54,71 @@ PKV_DEVINL uint32_t order_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One spare word in 32, so that threads walking contiguous segments of 2^n entries do not
-// meet in one bank.
-PKV_DEVINL int padded(int i) { return i + (i >> 5); }
+// One spare word in 8: a thread walks 8 neighbouring bins, and the threads of a warp should
+// not meet in one bank.
+PKV_DEVINL int spread(int bin) { return bin + (bin >> 3); }
+constexpr int kHist = kBins + kBins / 8;
 
-struct Shared {                       // after it: keys, class bits, cluster histograms
-    int hist[kBins];
-    unsigned long long warp_sums[32];
-    unsigned long long cluster_sums[2][kMaxCluster];
+struct Shared {   // after it: bits and numbers per 32 entries
+    int hist[kHist];
+    int cluster_hist[kHist];          // the cluster's, in its first CTA
+    uint32_t list_key[kList];
+    int list_at[kList];
+    unsigned long long warp_sums[kWarps];
+    unsigned long long cluster_sums[3][kMaxCluster];
     int pick[3];                      // bin, entries above it, entries in it
+    int listed;
 };
 
 // Exclusive prefix of v over the CTA's threads; `total` gets the sum.
-template <int NT>
-PKV_DEVINL unsigned long long block_scan(unsigned long long v, unsigned long long* warp_sums,
-                                         unsigned long long& total) {
-    constexpr int W = NT / 32;
+template <typename V>
+PKV_DEVINL V block_scan(V v, unsigned long long* warp_sums, V& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long incl = v;
+    V incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const V y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    if (lane == 31) warp_sums[warp] = incl;
+    if (lane == 31) warp_sums[warp] = static_cast<unsigned long long>(incl);
     __syncthreads();
-    unsigned long long s = lane < W ? warp_sums[lane] : 0, t = s;
+    V before = 0;
+    total = 0;
 #pragma unroll
-    for (int o = 1; o < W; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, t, o);
-        if (lane >= o) t += y;
+    for (int i = 0; i < kWarps; ++i) {
+        const V s = static_cast<V>(warp_sums[i]);
+        if (i < warp) before += s;
+        total += s;
     }
-    total = __shfl_sync(0xffffffffu, t, W - 1);
-    const unsigned long long before = __shfl_sync(0xffffffffu, t - s, warp);
     __syncthreads();   // warp_sums may be written again
     return before + incl - v;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(NT)
-evict_kernel(const EvictArgs a, const int C, const int cap) {
+// Adds `digit` of the lanes with `on` to the histogram (all lanes of the warp call).
+PKV_DEVINL void count_digit(int* hist, bool on, uint32_t digit) {
+    const uint32_t active = __ballot_sync(0xffffffffu, on);
+    if (active == 0) return;
+    const int lead = __ffs(active) - 1;
+    const uint32_t lead_digit = __shfl_sync(0xffffffffu, digit, lead);
+    const bool like = on && digit == lead_digit;
+    const uint32_t same = __ballot_sync(0xffffffffu, like);
+    if (static_cast<int>(threadIdx.x & 31) == lead)
+        atomicAdd(&hist[spread(digit)], __popc(same));
+    else if (on && !like)
+        atomicAdd(&hist[spread(digit)], 1);
+}
+
+// F: entries in flight per thread in a scan.
+template <int F>
+__global__ void __launch_bounds__(NT, 4)
+evict_kernel(const EvictArgs a, const int C, const int words) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sm = *reinterpret_cast<Shared*>(raw);
-    uint32_t* keys = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));   // [padded(cap)]
-    uint32_t* bits = keys + padded(cap) + 1;                               // [cap / 32 + 1]
-    int* ghist = reinterpret_cast<int*>(bits + cap / 32 + 1);              // [3][kBins], C > 1
+    uint32_t* safe_bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));   // protected
+    uint32_t* keep_bits = safe_bits + words;
+    uint32_t* tie_bits = keep_bits + words;      // equal to the threshold
+    uint32_t* hole_no = tie_bits + words;        // freed places before these 32 entries
+    uint32_t* mover_no = hole_no + words;        // movers before them
     griddep_wait();
     griddep_launch_dependents();
     const int kvh = blockIdx.x / C, rank = blockIdx.x % C, seq = blockIdx.y;
@@ -130,49 +157,55 @@ evict_kernel(const EvictArgs a, const int C, const int cap) {
     const int tracked = min(max(tracked_in, 0), L);
     auto position = [&](int j) { return j < tracked ? pos[j] : seen - L + j; };
 
-    // this CTA's slice [i0, i0 + n)
+    // this CTA's slice [i0, i0 + n): whole words but for the row's end
     const int per = ((L + C - 1) / C + 31) & ~31;
     const int i0 = min(rank * per, L);
     const int n = min(per, L - i0);
-    // What stays where it is, entry by entry (freed places are filled in step 4).
-    auto copy_through = [&](int end) {
-        const int m = min(n, end - i0);
-        const bool ws = w != wo, ps = pos != po;
-        for (int i = tid; i < m; i += NT) {
-            const int j = i0 + i;
-            if (ws) wo[j] = w[j];
-            if (ps || j >= tracked) po[j] = position(j);
-        }
-    };
+    const bool move_w = w != wo, move_p = pos != po;
     if (!shrinks) {
-        copy_through(L);
+        for (int i = tid; i < n; i += NT) {
+            const int j = i0 + i;
+            if (move_w) wo[j] = w[j];
+            if (move_p || j >= tracked) po[j] = position(j);
+        }
         return;
     }
-
-    // ---------------------------------------------------------------- 1. keys and classes
-    const int recent_from = seen - a.recent;
-    auto is_safe = [&](int j) {
-        const int p = position(j);
-        return p < a.sinks || p >= recent_from;
-    };
-    for (int i = tid; i < kBins; i += NT) sm.hist[i] = 0;
-    if (C > 1)
-        for (int i = tid; i < 3 * kBins; i += NT) ghist[i] = 0;
-    int mine = 0;
-    for (int i = tid; i - lane < n; i += NT) {   // whole warps
-        bool s = false;
-        if (i < n) {
-            s = is_safe(i0 + i);
-            if (i < cap) keys[padded(i)] = order_key(w[i0 + i]);
-        }
-        const uint32_t ball = __ballot_sync(0xffffffffu, s);
-        if (lane == 0 && i < cap) bits[i >> 5] = ball;
-        mine += s;
-    }
-    unsigned long long total;
-    block_scan<NT>(static_cast<unsigned long long>(mine), sm.warp_sums, total);
     cg::cluster_group cluster = cg::this_cluster();
-    // Totals of the CTAs before this one, and of all, in `slot` of the exchange array.
+
+    // ---------------------------------------------------------------- 1. classes, first digit
+    for (int i = tid; i < kHist; i += NT) sm.hist[i] = sm.cluster_hist[i] = 0;
+    if (tid == 0) sm.listed = 0;
+    __syncthreads();
+    const int recent_from = seen - a.recent;
+    int mine = 0;
+    for (int ib = tid; ib - lane < n; ib += F * NT) {   // whole warps
+        float x[F];
+        int p[F];
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            const int i = ib + u * NT;
+            if (i < n) {
+                x[u] = w[i0 + i];
+                p[u] = position(i0 + i);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            const int i = ib + u * NT;
+            if (i - lane >= n) break;
+            const bool in = i < n;
+            const bool s = in && (p[u] < a.sinks || p[u] >= recent_from);
+            const uint32_t ball = __ballot_sync(0xffffffffu, s);
+            if (lane == 0) {
+                safe_bits[i >> 5] = ball;
+                mine += __popc(ball);
+            }
+            count_digit(sm.hist, in && !s, in ? order_key(x[u]) >> 21 : 0u);
+        }
+    }
+    int cta_safe;
+    block_scan(mine, sm.warp_sums, cta_safe);
+    // Totals of the CTAs before this one, and of all, through `slot` of the exchange array.
     auto gather = [&](unsigned long long v, int slot, unsigned long long& before,
                       unsigned long long& all) {
         before = 0;
@@ -186,62 +219,60 @@ evict_kernel(const EvictArgs a, const int C, const int cap) {
             all += sm.cluster_sums[slot][r];
         }
     };
-    unsigned long long before, all;
-    gather(total, 0, before, all);
+    unsigned long long before, all, total;
+    gather(static_cast<unsigned long long>(cta_safe), 0, before, all);
     const int nsafe = static_cast<int>(all);
     const bool among_safe = nsafe >= b;
     int need = among_safe ? b : b - nsafe;   // entries to pick among the competing class
-
-    // Key and class of entry i of the slice.
-    auto entry = [&](int i, uint32_t& key) {
-        if (i < cap) {
-            key = keys[padded(i)];
-            return ((bits[i >> 5] >> (i & 31)) & 1u) != 0;
-        }
-        key = order_key(w[i0 + i]);
-        return is_safe(i0 + i);
+    // Entry i's class bit: 1 where it competes.
+    const uint32_t flip = among_safe ? 0u : 0xffffffffu;
+    auto competes = [&](int i) {
+        return (((safe_bits[i >> 5] ^ flip) >> (i & 31)) & 1u) != 0;
     };
+    // f(i, in, weight) for the slice's entries, whole warps at a time, one by one: for the
+    // rare cases (a batch of entries unrolled in every one of them would be mostly code, which
+    // a CTA that runs each line once has to fetch).
+    auto scan = [&](auto f) {
+#pragma unroll 1
+        for (int i = tid; i - lane < n; i += NT) f(i, i < n, i < n ? w[i0 + i] : 0.f);
+    };
+    if (among_safe) {   // the counted class does not compete after all
+        for (int i = tid; i < kHist; i += NT) sm.hist[i] = 0;
+        __syncthreads();
+        scan([&](int i, bool in, float x) {
+            count_digit(sm.hist, in && competes(i), order_key(x) >> 21);
+        });
+        __syncthreads();
+    }
 
     // ---------------------------------------------------------------- 2. threshold
     uint32_t prefix = 0, mask = 0;   // digits of the threshold found so far
-    int in_bin = need > 0 ? 0 : -1;
-    for (int pass = 0; need > 0 && pass < 3 && in_bin != need; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
-        if (pass > 0) {
-            for (int i = tid; i < kBins; i += NT) sm.hist[i] = 0;
-            __syncthreads();
-        }
-        for (int i = tid; i - lane < n; i += NT) {
-            uint32_t key = 0;
-            const bool on = i < n && entry(i, key) == among_safe && (key & mask) == prefix;
-            const uint32_t active = __ballot_sync(0xffffffffu, on);
-            if (on) {
-                const uint32_t digit = (key >> shift) & digit_mask;
-                const uint32_t same = __match_any_sync(active, digit);
-                if (lane == __ffs(same) - 1) atomicAdd(&sm.hist[digit], __popc(same));
-            }
-        }
-        __syncthreads();
+    int in_bin = -1;
+    // The histogram's bin at which the count from above reaches `need`; leaves hist zeroed.
+    auto narrow = [&](int shift, uint32_t digit_mask) {
         int* g = sm.hist;
         if (C > 1) {   // the cluster's histogram, in its first CTA
-            g = ghist + pass * kBins;
+            g = sm.cluster_hist;
             int* first = cluster.map_shared_rank(g, 0);
-            for (int i = tid; i < kBins; i += NT)
-                if (sm.hist[i]) atomicAdd(first + i, sm.hist[i]);
+            for (int i = tid; i < kHist; i += NT)
+                if (sm.hist[i]) {
+                    atomicAdd(first + i, sm.hist[i]);
+                    sm.hist[i] = 0;
+                }
             cluster.sync();
         }
-        if (rank == 0) {   // the bin at which the count from above reaches `need`
+        if (rank == 0) {
             constexpr int PER = kBins / NT;
             int cnt[PER], sum = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                cnt[i] = g[kBins - 1 - (tid * PER + i)];
+                int& bin = g[spread(kBins - 1 - (tid * PER + i))];
+                cnt[i] = bin;
+                bin = 0;
                 sum += cnt[i];
             }
-            unsigned long long t;
-            int above = static_cast<int>(
-                block_scan<NT>(static_cast<unsigned long long>(sum), sm.warp_sums, t));
+            int t;
+            int above = block_scan(sum, sm.warp_sums, t);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 if (above < need && above + cnt[i] >= need)
@@ -262,71 +293,202 @@ evict_kernel(const EvictArgs a, const int C, const int cap) {
         mask |= digit_mask << shift;
         need -= sm.pick[1];
         in_bin = sm.pick[2];
+    };
+    if (need > 0) narrow(21, 2047u);
+    // Second scan: kept for sure above the bin (the whole bin, if it is kept whole); what is
+    // in it is listed and its next digit counted.
+    const bool open = need > 0 && in_bin != need;
+    for (int ib = tid; ib - lane < n; ib += F * NT) {
+        float x[F];
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            const int i = ib + u * NT;
+            x[u] = i < n ? w[i0 + i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            const int i = ib + u * NT;
+            if (i - lane >= n) break;
+            const bool rival = i < n && competes(i);
+            const uint32_t key = order_key(x[u]), k = key & mask;
+            const bool keep = i < n && (rival ? need > 0 && (k > prefix || (!open && k == prefix))
+                                              : !among_safe);
+            const bool inside = rival && open && k == prefix;
+            const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+            const uint32_t found = __ballot_sync(0xffffffffu, inside);
+            if (lane == 0) {
+                keep_bits[i >> 5] = kept;
+                tie_bits[i >> 5] = 0;
+            }
+            if (inside) {
+                const int slot = atomicAdd(&sm.listed, 1);
+                if (slot < kList) {
+                    sm.list_key[slot] = key;
+                    sm.list_at[slot] = i;
+                }
+            }
+            if (found) count_digit(sm.hist, inside, (key >> 10) & 2047u);
+        }
     }
-    // Kept of the competing class: (key & mask) above `prefix`, and the first `need` equal
-    // to it (all of them where the bin was kept whole).
+    __syncthreads();
+    const int listed = open ? sm.listed : 0;
+    // A short list of one CTA is ranked outright, each entry against all.
+    const bool ranked = open && C == 1 && listed <= NT;
+    if (ranked && tid < listed) {
+        const uint32_t key = sm.list_key[tid];
+        const int i = sm.list_at[tid];
+        int better = 0;
+        for (int q = 0; q < listed; ++q) {
+            const uint32_t k = sm.list_key[q];
+            better += k > key || (k == key && sm.list_at[q] < i);
+        }
+        if (better < need) atomicOr(&keep_bits[i >> 5], 1u << (i & 31));
+    }
+    if (ranked) __syncthreads();
+    if (open && !ranked) {
+        const bool by_list = listed <= kList;
+        // f(i, on, key) for the entries in the first bin, whole warps at a time
+        const uint32_t bin_mask = mask, bin = prefix;
+        auto candidates = [&](auto f) {
+            if (by_list) {
+                for (int q = tid; q - lane < listed; q += NT) {
+                    const bool on = q < listed;
+                    f(on ? sm.list_at[q] : 0, on, on ? sm.list_key[q] : 0u);
+                }
+            } else {
+                scan([&](int i, bool in, float x) {
+                    const uint32_t key = order_key(x);
+                    f(i, in && competes(i) && (key & bin_mask) == bin, key);
+                });
+            }
+        };
+        narrow(10, 2047u);
+        if (in_bin != need) {   // the last ten bits
+            candidates([&](int, bool on, uint32_t key) {
+                count_digit(sm.hist, on && (key & mask) == prefix, key & 1023u);
+            });
+            __syncthreads();
+            narrow(0, 1023u);
+        }
+        const bool whole = in_bin == need;
+        candidates([&](int i, bool on, uint32_t key) {
+            const uint32_t k = key & mask;
+            if (on && (k > prefix || (whole && k == prefix)))
+                atomicOr(&keep_bits[i >> 5], 1u << (i & 31));
+            else if (on && k == prefix)
+                atomicOr(&tie_bits[i >> 5], 1u << (i & 31));
+        });
+        __syncthreads();
+    }
 
     // ---------------------------------------------------------------- 3. places
-    const int E = (n + NT - 1) / NT;
-    const int s0 = min(tid * E, n), s1 = min(s0 + E, n);   // this thread's segment
-    // -1: not kept, 0: in the threshold's bin, 1: kept
-    auto verdict = [&](int i) {
-        uint32_t key;
-        const bool s = entry(i, key);
-        if (s != among_safe) return s ? 1 : -1;
-        if (need <= 0) return -1;   // nothing of the competing class is kept
-        const uint32_t k = key & mask;
-        return k > prefix ? 1 : k == prefix ? 0 : -1;
-    };
-    int ties = 0;
-    for (int i = s0; i < s1; ++i) ties += verdict(i) == 0;
-    int tie_rank = static_cast<int>(
-        block_scan<NT>(static_cast<unsigned long long>(ties), sm.warp_sums, total));
-    gather(total, 1, before, all);
-    tie_rank += static_cast<int>(before);
-
-    unsigned long long moved = 0;   // freed places, and kept entries past the budget << 32
-    int t = tie_rank;
-    for (int i = s0; i < s1; ++i) {
-        const int v = verdict(i);
-        const bool keep = v > 0 || (v == 0 && t < need);
-        t += v == 0;
-        if (i0 + i < b)
-            moved += keep ? 0ull : 1ull;
-        else
-            moved += keep ? 1ull << 32 : 0ull;
+    const int nw = (n + 31) >> 5;
+    const int E = (nw + NT - 1) / NT;
+    const int w0 = min(tid * E, nw), w1 = min(w0 + E, nw);   // this thread's words
+    if (open && !ranked && in_bin != need) {   // equal weights: the first `need` of them, by index
+        int ties = 0, cta_ties;
+        for (int x = w0; x < w1; ++x) ties += __popc(tie_bits[x]);
+        int no = block_scan(ties, sm.warp_sums, cta_ties);
+        gather(static_cast<unsigned long long>(cta_ties), 1, before, all);
+        no += static_cast<int>(before);
+        for (int x = w0; x < w1; ++x) {
+            uint32_t tied = tie_bits[x];
+            const int cnt = __popc(tied);
+            for (int drop = no + cnt - need; drop > 0 && tied; --drop)   // the last ones go
+                tied &= ~(0x80000000u >> __clz(tied));
+            keep_bits[x] |= tied;
+            no += cnt;
+        }
     }
-    unsigned long long first = block_scan<NT>(moved, sm.warp_sums, total);
-    gather(total, 0, before, all);
+    // Entries of word x that are freed places, and that move.
+    auto hole_mask = [&](int x) {
+        const int left = b - i0 - 32 * x;   // entries below the budget
+        return left <= 0 ? 0u : ~keep_bits[x] & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
+    };
+    auto mover_mask = [&](int x) {
+        const int left = b - i0 - 32 * x;
+        return left >= 32 ? 0u : keep_bits[x] & (left <= 0 ? 0xffffffffu : ~((1u << left) - 1u));
+    };
+    unsigned long long moved = 0;   // freed places, and movers << 32
+    for (int x = w0; x < w1; ++x)
+        moved += static_cast<unsigned long long>(__popc(hole_mask(x))) |
+                 static_cast<unsigned long long>(__popc(mover_mask(x))) << 32;
+    unsigned long long first = block_scan(moved, sm.warp_sums, total);
+    gather(total, 2, before, all);
     first += before;
     const int nmoves = static_cast<int>(all >> 32);
+    for (int x = w0; x < w1; ++x) {
+        hole_no[x] = static_cast<uint32_t>(first);
+        mover_no[x] = static_cast<uint32_t>(first >> 32);
+        first += static_cast<unsigned long long>(__popc(hole_mask(x))) |
+                 static_cast<unsigned long long>(__popc(mover_mask(x))) << 32;
+    }
+    __syncthreads();
     // lists of at most min(b, L - b) <= max_context / 2 moves
     const int most = a.max_context >> 1;
     int32_t* holes = a.moves + (static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
-                                   (4 * static_cast<size_t>(most));
-    int32_t* movers = holes + most;
-    float* mover_w = reinterpret_cast<float*>(movers + most);
-    int32_t* mover_pos = movers + 2 * static_cast<size_t>(most);
-    int h = static_cast<int>(first & 0xffffffffu), m = static_cast<int>(first >> 32);
-    t = tie_rank;
-    if (moved)
-        for (int i = s0; i < s1; ++i) {
-            const int v = verdict(i);
-            const bool keep = v > 0 || (v == 0 && t < need);
-            t += v == 0;
-            const int j = i0 + i;
+                                   (5 * static_cast<size_t>(most));
+    uint32_t* hole_slot = reinterpret_cast<uint32_t*>(holes + most);
+    uint32_t* mover_slot = hole_slot + most;
+    float* mover_w = reinterpret_cast<float*>(mover_slot + most);
+    int32_t* mover_pos = holes + 4 * static_cast<size_t>(most);
+    // Pool slots fit 32 bits: 2^32 rows of the least 128 bytes are more than this GPU holds.
+    const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.max_blocks_per_seq;
+    const uint32_t low = (1u << a.block_shift) - 1u;
+    constexpr uint32_t kNoSlot = 0xffffffffu;
+    auto slot_of = [&](int j) {
+        const int phys = __ldg(bt + (j >> a.block_shift));
+        if (phys < 0 || phys >= a.num_blocks) {
+            raise_status(a.status, PKV_ERR_OOB);
+            return kNoSlot;
+        }
+        return (static_cast<uint32_t>(phys) << a.block_shift) + (static_cast<uint32_t>(j) & low);
+    };
+    const uint32_t lower = (1u << lane) - 1u;
+    // Several entries per thread at a time, loads before stores: in place the compiler cannot
+    // tell that a store does not change what the next entry loads.
+    constexpr int U3 = F;
+    for (int ib = tid; ib < n; ib += U3 * NT) {
+        float x[U3];
+        int p[U3], to[U3];   // to: the entry's number in its list, or -1
+        uint32_t slot[U3];
+#pragma unroll
+        for (int u = 0; u < U3; ++u) {
+            const int i = ib + u * NT, j = i0 + i;
+            to[u] = -1;
+            if (i >= n) continue;
+            const int word = i >> 5;
+            const bool under = j < b;
+            const uint32_t listed = under ? hole_mask(word) : mover_mask(word);
+            if (listed >> lane & 1u)
+                to[u] = static_cast<int>((under ? hole_no : mover_no)[word] +
+                                         __popc(listed & lower));
+            if (to[u] >= 0) slot[u] = slot_of(j);
+            if (under ? to[u] < 0 && move_w : to[u] >= 0) x[u] = w[j];
+            if (under ? to[u] < 0 && (move_p || j >= tracked) : to[u] >= 0) p[u] = position(j);
+        }
+#pragma unroll
+        for (int u = 0; u < U3; ++u) {
+            const int i = ib + u * NT, j = i0 + i;
+            if (i >= n) continue;
             if (j < b) {
-                if (!keep) holes[h++] = j;
-            } else if (keep) {
-                movers[m] = j;
-                mover_w[m] = w[j];
-                mover_pos[m] = position(j);
-                ++m;
+                if (to[u] >= 0) {
+                    holes[to[u]] = j;
+                    hole_slot[to[u]] = slot[u];
+                } else {
+                    if (move_w) wo[j] = x[u];
+                    if (move_p || j >= tracked) po[j] = p[u];
+                }
+            } else {
+                if (to[u] >= 0) {
+                    mover_slot[to[u]] = slot[u];
+                    mover_w[to[u]] = x[u];
+                    mover_pos[to[u]] = p[u];
+                }
+                wo[j] = 0.f;   // a free place starts at zero
             }
         }
-    __syncthreads();
-    copy_through(b);
-    for (int i = max(0, b - i0) + tid; i < n; i += NT) wo[i0 + i] = 0.f;   // free places
+    }
     if (C > 1)
         cluster.sync();
     else
@@ -339,61 +501,58 @@ evict_kernel(const EvictArgs a, const int C, const int cap) {
         wo[to] = mover_w[k];
         po[to] = mover_pos[k];
     }
-    const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.max_blocks_per_seq;
     const int csh = a.row_shift;            // log2 of 16-byte chunks per row
     const int ch = worker & ((1 << csh) - 1);
     const int step = workers >> csh;        // rows per sweep
-    const int low = (1 << a.block_shift) - 1;
     uint4* kp = static_cast<uint4*>(a.k_pool);
     uint4* vp = static_cast<uint4*>(a.v_pool);
+    auto chunk = [&](uint32_t slot) {       // 16-byte chunk of the slot's row of this head
+        const size_t blk = slot >> a.block_shift;
+        return ((((blk * a.num_kv_heads + kvh) << a.block_shift) + (slot & low)) << csh) + ch;
+    };
     constexpr int U = 4;
-    for (int k0 = worker >> csh; k0 < nmoves; k0 += U * step) {
-        int from[U], to[U], pf[U], pt[U];
-        bool ok[U];
+    uint32_t from[U], to[U];
+    auto look_up = [&](int k0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u * step;
-            ok[u] = k < nmoves;
-            from[u] = ok[u] ? movers[k] : 0;
-            to[u] = ok[u] ? holes[k] : 0;
+            from[u] = k < nmoves ? mover_slot[k] : kNoSlot;
+            to[u] = k < nmoves ? hole_slot[k] : kNoSlot;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            pf[u] = ok[u] ? __ldg(bt + (from[u] >> a.block_shift)) : 0;
-            pt[u] = ok[u] ? __ldg(bt + (to[u] >> a.block_shift)) : 0;
-        }
+    };
+    int k0 = worker >> csh;
+    look_up(k0);
+    while (k0 < nmoves) {
         uint4 xk[U], xv[U];
+        size_t dst[U];
+        bool on[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!ok[u]) continue;
-            if (pf[u] < 0 || pf[u] >= a.num_blocks || pt[u] < 0 || pt[u] >= a.num_blocks) {
-                raise_status(a.status, PKV_ERR_OOB);
-                ok[u] = false;
-                continue;
-            }
-            const size_t src = (((((static_cast<size_t>(pf[u]) * a.num_kv_heads + kvh)
-                                   << a.block_shift) + (from[u] & low))) << csh) + ch;
+            on[u] = from[u] != kNoSlot && to[u] != kNoSlot;
+            if (!on[u]) continue;
+            const size_t src = chunk(from[u]);
             xk[u] = kp[src];
             xv[u] = vp[src];
+            dst[u] = chunk(to[u]);
         }
+        k0 += U * step;
+        look_up(k0);   // the next rows' places, while these rows are on their way
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!ok[u]) continue;
-            const size_t dst = (((((static_cast<size_t>(pt[u]) * a.num_kv_heads + kvh)
-                                   << a.block_shift) + (to[u] & low))) << csh) + ch;
-            kp[dst] = xk[u];
-            vp[dst] = xv[u];
+            if (!on[u]) continue;
+            kp[dst[u]] = xk[u];
+            vp[dst[u]] = xv[u];
         }
     }
 }
 
-template <int NT>
-cudaError_t launch_nt(const EvictArgs& a, int C, cudaStream_t stream) {
-    const int slice = ((a.max_context + C - 1) / C + 31) & ~31;
-    const int cap = slice < kCapEntries ? slice : kCapEntries;
-    const int words = cap + (cap >> 5) + 1 + cap / 32 + 1 + (C > 1 ? 3 * kBins : 0);
-    const int smem = static_cast<int>(sizeof(Shared)) + 4 * words;
-    auto kern = evict_kernel<NT>;
+template <int F>
+cudaError_t launch_f(const EvictArgs& a, int C, cudaStream_t stream) {
+    auto kern = evict_kernel<F>;
+    const int words = ((a.max_context + C - 1) / C + 31) / 32;
+    const int smem = static_cast<int>(sizeof(Shared)) + 5 * 4 * words;
+    static_assert(sizeof(Shared) + 5 * 4 * (kEvictMaxContext / kMaxCluster / 32) <= 232448,
+                  "the bits of the longest slice fit");
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -409,22 +568,21 @@ cudaError_t launch_nt(const EvictArgs& a, int C, cudaStream_t stream) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a, C, cap);
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, C, words);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-    // CTAs per row: enough that a slice fits in shared memory beside others, and that about
-    // two CTAs per SM exist where there are few rows.
+    // CTAs per row: enough that a slice has at most 16384 entries, and that about two CTAs per
+    // SM exist where there are few rows.
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
     int C = 1;
     while (C < kMaxCluster &&
            (a.max_context > 16384 * C || (rows * C < 304 && a.max_context > 1024 * C)))
         C *= 2;
-    // Short rows: CTAs of 256 threads, so that more of them share an SM.
-    return C == 1 ? launch_nt<256>(a, C, stream) : launch_nt<512>(a, C, stream);
+    return C == 1 ? launch_f<4>(a, C, stream) : launch_f<8>(a, C, stream);
 }
 
 }  // namespace pkv

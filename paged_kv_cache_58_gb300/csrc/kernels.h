@@ -255,7 +255,8 @@ cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int head_dim, in
 cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, int head_dim, int group,
                                       cudaStream_t stream);
 
-// Eviction by accumulated weight.
+// Eviction by accumulated weight.  A row's bits have to fit in the shared memory of a cluster.
+constexpr int kEvictMaxContext = 1 << 20;
 struct EvictArgs {
     void* k_pool;
     void* v_pool;
@@ -270,7 +271,7 @@ struct EvictArgs {
     const int32_t* positions;
     int32_t* positions_out;
     int32_t* new_lens;
-    int32_t* moves;   // workspace: [S][Hkv][4][max_context / 2]
+    int32_t* moves;   // workspace: [S][Hkv][5][max_context / 2]
     int* status;
     int64_t num_blocks;
     int64_t weights_stride;

@@ -1270,7 +1270,7 @@ bool same_or_apart(const void* a, const void* b, uint64_t bytes) {
 
 size_t pkv_evict_workspace_bytes(const pkv_pool_desc* pool, int num_seqs, int max_context) {
     if (check_pool(pool) != PKV_OK || num_seqs <= 0 || max_context <= 0) return 0;
-    return static_cast<size_t>(num_seqs) * pool->num_kv_heads * 4 *
+    return static_cast<size_t>(num_seqs) * pool->num_kv_heads * 5 *
            static_cast<size_t>(std::max(max_context / 2, 1)) * sizeof(int32_t);
 }
 
@@ -1305,7 +1305,7 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
     if (new_lens == context_lens || new_lens == budgets || new_lens == seen_lens ||
         new_lens == tracked_lens || new_lens == row_ids)
         return PKV_ERR_INVALID;
-    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || max_context > pkv::kEvictMaxContext) return PKV_ERR_UNSUPPORTED;
     const size_t need = pkv_evict_workspace_bytes(pool, num_seqs, max_context);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_NOMEM;
     int* status = status_word();
