@@ -526,11 +526,12 @@ decode_combine_kernel(const DecodeArgs a) {
 
 // The finishing launch of a decode with accumulated attention weights.  CTAs [0,
 // combine_ctas) merge partitions as decode_combine_kernel does; each CTA after them takes
-// kWeightTile tokens of one (sequence, kv head): it merges the partitions' (m, l) of the
-// G query heads into their softmax statistics, M and 1 / sum, and adds
+// `run` tiles of kWeightTile tokens of one (sequence, kv head): it merges the partitions'
+// (m, l) of the G query heads into their softmax statistics, M and 1 / sum, and adds
 //   weights[row][kvh][j] = decay * weights + sum_g 2^(s_gj - M_g) / sum_g
-// from the scores the split kernel kept (mostly still in L2).  One thread owns a token,
-// so no two threads add to the same weight and the sum's order is fixed.
+// from the scores the split kernel kept (in L2 still, where they fit).  One thread owns a
+// token, so no two threads add to the same weight and the sum's order is fixed.  It is a
+// streaming kernel: the scores of the next tile are loaded while one is worked on.
 constexpr int kWeightTile = 512;
 
 // The G scores of a token, in the widest loads their alignment (4 G bytes) allows.
@@ -552,7 +553,7 @@ PKV_DEVINL void load_scores(const float* p, float (&s)[G]) {
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCombineWarps * 32)
-decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int tiles) {
+decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs, const int run) {
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5;
@@ -565,15 +566,15 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int tiles
     constexpr int PER = kWeightTile / kThr;
     __shared__ float coef[2][G];
     int idx = static_cast<int>(blockIdx.x) - combine_ctas;
-    const int tile = idx % tiles;
-    idx /= tiles;
+    const int first = idx % runs * run;
+    idx /= runs;
     const int kvh = idx % a.num_kv_heads;
     const int seq = idx / a.num_kv_heads;
+    const int row = a.row_ids ? __ldg(a.row_ids + seq) : seq;
     int L = min(__ldg(a.context_lens + seq), a.score_tokens);
     L = min(L, (a.max_blocks_per_seq << a.chunk_shift) * kBlock);
-    const int row = a.row_ids ? __ldg(a.row_ids + seq) : seq;
-    const int j0 = tile * kWeightTile;
-    if (row < 0 || j0 >= L) return;   // a padding row, or past the sequence
+    int j0 = first * kWeightTile + static_cast<int>(threadIdx.x);
+    if (row < 0 || first * kWeightTile >= L) return;   // a padding row, or past the sequence
     if (row >= a.num_rows || L > a.weights_stride) {
         if (threadIdx.x == 0) raise_status(a.status, PKV_ERR_OOB);
         if (row >= a.num_rows) return;
@@ -583,13 +584,17 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int tiles
                                      a.score_tokens * G;
     float* wp = a.weights + (static_cast<size_t>(row) * a.num_kv_heads + kvh) *
                                 static_cast<size_t>(a.weights_stride);
-    float s[PER][G], w[PER];
+    const int end = min(L, (first + run) * kWeightTile);
+    auto load = [&](int j, float (&s)[PER][G], float (&w)[PER]) {
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {   // loaded beside the statistics
-        const int j = j0 + u * kThr + threadIdx.x;
-        w[u] = (j < L && a.decay != 0.f) ? wp[j] : 0.f;
-        if (j < L) load_scores<G>(sp + static_cast<size_t>(j) * G, s[u]);
-    }
+        for (int u = 0; u < PER; ++u) {
+            const int ju = j + u * kThr;
+            w[u] = (ju < end && a.decay != 0.f) ? wp[ju] : 0.f;
+            if (ju < end) load_scores<G>(sp + static_cast<size_t>(ju) * G, s[u]);
+        }
+    };
+    float s[PER][G], w[PER];
+    load(j0, s, w);   // beside the statistics
     const int total = a.max_parts;
     const int nchunks = (L + kBlock - 1) / kBlock;
     const int np = min(total, (nchunks + a.partition_chunks - 1) / a.partition_chunks);
@@ -611,14 +616,28 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int tiles
         }
     }
     __syncthreads();
+    for (;;) {
+        const int next = j0 + kWeightTile;
+        const bool more = next - static_cast<int>(threadIdx.x) < end;
+        float sn[PER][G], wn[PER];
+        if (more) load(next, sn, wn);
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int j = j0 + u * kThr + threadIdx.x;
-        if (j >= L) continue;
-        float p = 0.f;
+        for (int u = 0; u < PER; ++u) {
+            const int j = j0 + u * kThr;
+            if (j >= end) continue;
+            float p = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) p = fmaf(fast_exp2(s[u][g] - coef[0][g]), coef[1][g], p);
-        wp[j] = a.decay != 0.f ? fmaf(a.decay, w[u], p) : p;
+            for (int g = 0; g < G; ++g) p = fmaf(fast_exp2(s[u][g] - coef[0][g]), coef[1][g], p);
+            wp[j] = a.decay != 0.f ? fmaf(a.decay, w[u], p) : p;
+        }
+        if (!more) break;
+        j0 = next;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            w[u] = wn[u];
+#pragma unroll
+            for (int g = 0; g < G; ++g) s[u][g] = sn[u][g];
+        }
     }
 }
 
@@ -653,11 +672,16 @@ cudaError_t launch_finish_typed(const DecodeArgs& a, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     // one partition: the split kernel has written the output, no merge is left
     const int64_t combine = a.max_parts > 1 ? (rows + kCombineWarps - 1) / kCombineWarps : 0;
+    // Runs of 8 tiles, shorter while there would be fewer than 8 CTAs per SM.
     const int tiles = (a.score_tokens + kWeightTile - 1) / kWeightTile;
-    const int64_t grid = combine + static_cast<int64_t>(tiles) * a.num_kv_heads * a.num_seqs;
+    const int64_t heads = static_cast<int64_t>(a.num_kv_heads) * a.num_seqs;
+    int run = 8;
+    while (run > 1 && (tiles + run - 1) / run * heads < 8 * 152) run /= 2;
+    const int runs = (tiles + run - 1) / run;
+    const int64_t grid = combine + runs * heads;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     return launch_pdl(decode_finish_kernel<T, D, G>, dim3(static_cast<unsigned>(grid)),
-                      dim3(kCombineWarps * 32), 0, stream, a, static_cast<int>(combine), tiles);
+                      dim3(kCombineWarps * 32), 0, stream, a, static_cast<int>(combine), runs, run);
 }
 
 template <typename T, int D>
