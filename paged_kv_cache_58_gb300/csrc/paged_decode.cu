@@ -554,11 +554,11 @@ PKV_DEVINL void load_scores(const float* p, float (&s)[G]) {
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCombineWarps * 32)
 decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs, const int run) {
-    griddep_wait();
-    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (static_cast<int>(blockIdx.x) < combine_ctas) {
+        griddep_wait();
+        griddep_launch_dependents();
         combine_row<T, D>(a, static_cast<size_t>(blockIdx.x) * kCombineWarps + warp, lane);
         return;
     }
@@ -570,31 +570,43 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
     idx /= runs;
     const int kvh = idx % a.num_kv_heads;
     const int seq = idx / a.num_kv_heads;
+    // The lengths, rows and old weights come from before the split kernel.  That kernel lets
+    // this one start only once all its CTAs have seen their own predecessors complete, so
+    // these are read while it still runs; its scores and partials only after the wait.
     const int row = a.row_ids ? __ldg(a.row_ids + seq) : seq;
     int L = min(__ldg(a.context_lens + seq), a.score_tokens);
     L = min(L, (a.max_blocks_per_seq << a.chunk_shift) * kBlock);
     int j0 = first * kWeightTile + static_cast<int>(threadIdx.x);
-    if (row < 0 || first * kWeightTile >= L) return;   // a padding row, or past the sequence
-    if (row >= a.num_rows || L > a.weights_stride) {
-        if (threadIdx.x == 0) raise_status(a.status, PKV_ERR_OOB);
-        if (row >= a.num_rows) return;
-        L = static_cast<int>(min(static_cast<int64_t>(L), a.weights_stride));
-    }
+    const bool idle = row < 0 || first * kWeightTile >= L;   // padding, or past the sequence
+    const bool lost = !idle && row >= a.num_rows;
+    const bool beyond = !idle && L > a.weights_stride;
+    if (beyond) L = static_cast<int>(a.weights_stride);
     const float* sp = a.scores + (static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
                                      a.score_tokens * G;
-    float* wp = a.weights + (static_cast<size_t>(row) * a.num_kv_heads + kvh) *
+    float* wp = a.weights + (static_cast<size_t>(idle || lost ? 0 : row) * a.num_kv_heads + kvh) *
                                 static_cast<size_t>(a.weights_stride);
-    const int end = min(L, (first + run) * kWeightTile);
-    auto load = [&](int j, float (&s)[PER][G], float (&w)[PER]) {
+    const int end = idle || lost ? 0 : min(L, (first + run) * kWeightTile);
+    auto load_weights = [&](int j, float (&w)[PER]) {
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int ju = j + u * kThr;
             w[u] = (ju < end && a.decay != 0.f) ? wp[ju] : 0.f;
+        }
+    };
+    auto load = [&](int j, float (&s)[PER][G]) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int ju = j + u * kThr;
             if (ju < end) load_scores<G>(sp + static_cast<size_t>(ju) * G, s[u]);
         }
     };
     float s[PER][G], w[PER];
-    load(j0, s, w);   // beside the statistics
+    load_weights(j0, w);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (threadIdx.x == 0 && (lost || beyond)) raise_status(a.status, PKV_ERR_OOB);
+    if (end == 0) return;
+    load(j0, s);   // beside the statistics
     const int total = a.max_parts;
     const int nchunks = (L + kBlock - 1) / kBlock;
     const int np = min(total, (nchunks + a.partition_chunks - 1) / a.partition_chunks);
@@ -620,7 +632,10 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
         const int next = j0 + kWeightTile;
         const bool more = next - static_cast<int>(threadIdx.x) < end;
         float sn[PER][G], wn[PER];
-        if (more) load(next, sn, wn);
+        if (more) {
+            load(next, sn);
+            load_weights(next, wn);
+        }
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int j = j0 + u * kThr;
@@ -672,11 +687,11 @@ cudaError_t launch_finish_typed(const DecodeArgs& a, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     // one partition: the split kernel has written the output, no merge is left
     const int64_t combine = a.max_parts > 1 ? (rows + kCombineWarps - 1) / kCombineWarps : 0;
-    // Runs of 8 tiles, shorter while there would be fewer than 8 CTAs per SM.
+    // Runs of 8 tiles, shorter while there would be fewer than 6 CTAs per SM.
     const int tiles = (a.score_tokens + kWeightTile - 1) / kWeightTile;
     const int64_t heads = static_cast<int64_t>(a.num_kv_heads) * a.num_seqs;
     int run = 8;
-    while (run > 1 && (tiles + run - 1) / run * heads < 8 * 152) run /= 2;
+    while (run > 1 && (tiles + run - 1) / run * heads < 6 * 152) run /= 2;
     const int runs = (tiles + run - 1) / run;
     const int64_t grid = combine + runs * heads;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
