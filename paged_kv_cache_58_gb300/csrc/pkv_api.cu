@@ -1158,10 +1158,20 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
                          (num_q_heads / pool->num_kv_heads);
     if (rows > INT32_MAX - 128) return false;
     p->rows_pad = static_cast<int>((rows + 127) / 128 * 128);
-    // Items of at most 16 tiles of 128 keys, so that CTAs that walk a dozen of them end
+    // Tensor cores: items of at most 16 tiles of 128 keys, so that CTAs that walk a dozen of them end
     // together; smaller ones, down to 8 tiles, while there are fewer than 16 items per SM (the
     // lengths are not known here, only their bound); larger ones past 256 parts.
     const int64_t heads = static_cast<int64_t>(num_reqs) * pool->num_kv_heads;
+    if (pool->dtype == PKV_F32) {
+        // CUDA cores: 64-row by 64-key tiles; parts of the keys until there are two CTAs per SM.
+        const int64_t ctas = heads * (p->rows_pad / 64);
+        p->chunk_tiles = 0;
+        p->splits = static_cast<int>(std::min<int64_t>(
+            std::min<int64_t>((2 * 152 + ctas - 1) / ctas, ceil_div(max_context, 64)), 32));
+        p->bytes = p->stats_bytes =
+            static_cast<size_t>(heads) * p->splits * p->rows_pad * sizeof(float2);
+        return true;
+    }
     const int64_t items = heads * ((p->rows_pad / 128 + 1) / 2);
     const int tiles = ceil_div(max_context, 128);
     const int64_t want = (16 * 152 + items - 1) / items;

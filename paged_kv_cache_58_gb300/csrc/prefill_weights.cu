@@ -12,7 +12,9 @@
 //
 // This is the CUDA-core form, for fp32 pools (the tensor cores would round the operands to
 // tf32; bf16 pools have a tensor-core form in prefill_weights_tc.cu): a 64 x 64 tile of
-// scores per step, 256 threads of 4 x 4 scores each, both operand tiles in shared memory.
+// scores per step, 256 threads of 4 x 4 scores each, both operand tiles in shared memory,
+// the next tile on its way into registers meanwhile.  Pass 1 splits a row tile's keys over
+// CTAs where there are few; pass 2 merges the parts' statistics as it reads them.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -56,54 +58,65 @@ struct Smem {
     float red[2][kTile][17];
 };
 
-// Rows (i, g) of the window, token-major: row rho is token n - m + rho / G of the
-// request's new tokens, head kvh * G + rho % G.
+// A tile on its way from global memory: each thread holds its pieces in registers while the
+// tile before it is worked on, then puts them into shared memory.
 template <int D>
-PKV_DEVINL void load_q(float (*dst)[Smem<D>::kStride], const PrefillWeightsArgs& a,
-                       const Request& rq, int group, int kvh, int row0) {
-    constexpr int E = 4;   // floats per 16-byte piece
-    for (int t = threadIdx.x; t < kTile * (D / E); t += kThreads) {
-        const int row = t / (D / E), ch = t % (D / E);
-        const int rho = row0 + row;
-        float* d = &dst[row][ch * E];
-        if (rho < rq.rows) {
-            const int64_t tok = static_cast<int64_t>(rq.qoff) + rq.n - rq.m + rho / group;
-            const float* src = static_cast<const float*>(a.q) +
-                           (tok * a.num_q_heads + kvh * group + rho % group) * D + ch * E;
-            *reinterpret_cast<float4*>(d) = __ldg(reinterpret_cast<const float4*>(src));
-        } else {
-            *reinterpret_cast<float4*>(d) = make_float4(0.f, 0.f, 0.f, 0.f);
+struct Fetch {
+    static constexpr int kPieces = kTile * (D / 4) / kThreads;   // 16-byte pieces per thread
+    float4 v[kPieces];
+    PKV_DEVINL void put(float (*dst)[Smem<D>::kStride]) const {
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const int t = threadIdx.x + u * kThreads;
+            *reinterpret_cast<float4*>(&dst[t / (D / 4)][t % (D / 4) * 4]) = v[u];
         }
     }
-}
-template <int D>
-PKV_DEVINL void load_k(float (*dst)[Smem<D>::kStride], const PrefillWeightsArgs& a, int req,
-                       int kvh, int key0, int keys) {
-    constexpr int E = 4;   // floats per 16-byte piece
-    const int32_t* bt = a.block_tables + static_cast<size_t>(req) * a.max_blocks_per_seq;
-    for (int t = threadIdx.x; t < kTile * (D / E); t += kThreads) {
-        const int row = t / (D / E), ch = t % (D / E);
-        const int key = key0 + row;
-        float* d = &dst[row][ch * E];
-        int phys = -1;
-        if (key < keys) {
-            phys = __ldg(bt + (key >> a.block_shift));
-            if (phys < 0 || phys >= a.num_blocks) {
-                raise_status(a.status, PKV_ERR_OOB);
-                phys = -1;
+    // Rows (i, g) of the window, token-major: row rho is token n - m + rho / G of the
+    // request's new tokens, head kvh * G + rho % G.
+    PKV_DEVINL void rows(const PrefillWeightsArgs& a, const Request& rq, int group, int kvh,
+                         int row0) {
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const int t = threadIdx.x + u * kThreads;
+            const int rho = row0 + t / (D / 4);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (rho < rq.rows) {
+                const int64_t tok = static_cast<int64_t>(rq.qoff) + rq.n - rq.m + rho / group;
+                const float* src = static_cast<const float*>(a.q) +
+                                   (tok * a.num_q_heads + kvh * group + rho % group) * D +
+                                   t % (D / 4) * 4;
+                v[u] = __ldg(reinterpret_cast<const float4*>(src));
             }
         }
-        if (phys >= 0) {
-            const float* src = static_cast<const float*>(a.k_pool) +
-                           (((static_cast<int64_t>(phys) * a.num_kv_heads + kvh)
-                             << a.block_shift) +
-                            (key & ((1 << a.block_shift) - 1))) * D + ch * E;
-            *reinterpret_cast<float4*>(d) = __ldg(reinterpret_cast<const float4*>(src));
-        } else {
-            *reinterpret_cast<float4*>(d) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // Keys key0 .. of the request, those from `keys` on as zeros.
+    PKV_DEVINL void keys(const PrefillWeightsArgs& a, int req, int kvh, int key0, int keys) {
+        const int32_t* bt = a.block_tables + static_cast<size_t>(req) * a.max_blocks_per_seq;
+        int phys[kPieces];
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const int key = key0 + (threadIdx.x + u * kThreads) / (D / 4);
+            phys[u] = key < keys ? __ldg(bt + (key >> a.block_shift)) : -1;
+            if (key < keys && (phys[u] < 0 || phys[u] >= a.num_blocks)) {
+                raise_status(a.status, PKV_ERR_OOB);
+                phys[u] = -1;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const int t = threadIdx.x + u * kThreads;
+            const int key = key0 + t / (D / 4);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (phys[u] >= 0) {
+                const float* src = static_cast<const float*>(a.k_pool) +
+                                   (((static_cast<int64_t>(phys[u]) * a.num_kv_heads + kvh)
+                                     << a.block_shift) +
+                                    (key & ((1 << a.block_shift) - 1))) * D + t % (D / 4) * 4;
+                v[u] = __ldg(reinterpret_cast<const float4*>(src));
+            }
         }
     }
-}
+};
 
 // s[i][j] = q row (ty + 16 i) . k row (tx + 16 j), scaled; 4 x 4 per thread.
 template <int D>
@@ -156,7 +169,10 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
     const int key_tiles = last / kTile + 1;
     const int per = (key_tiles + a.splits - 1) / a.splits;
     const int t0 = split * per, t1 = min(key_tiles, t0 + per);
-    load_q<D>(sm.q, a, rq, group, kvh, row0);
+    Fetch<D> f;
+    f.rows(a, rq, group, kvh, row0);
+    f.put(sm.q);
+    if (t0 < t1) f.keys(a, req, kvh, t0 * kTile, last + 1);
     float m[4], l[4];
     int lim[4];   // last key of each of the thread's rows
 #pragma unroll
@@ -166,8 +182,9 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
         lim[i] = rq.c + rq.n - rq.m + (row0 + ty + 16 * i) / group;
     }
     for (int t = t0; t < t1; ++t) {
-        load_k<D>(sm.k, a, req, kvh, t * kTile, last + 1);
+        f.put(sm.k);
         __syncthreads();
+        if (t + 1 < t1) f.keys(a, req, kvh, (t + 1) * kTile, last + 1);
         float s[4][4];
         scores<D>(sm, a.scale_log2, s);
 #pragma unroll
@@ -221,12 +238,16 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     const int keys = rq.c + rq.n;
     if (rq.rows == 0 || key0 >= keys) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_k<D>(sm.k, a, req, kvh, key0, keys);
+    Fetch<D> f;
+    f.keys(a, req, kvh, key0, keys);
+    f.put(sm.k);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     const int base = rq.c + rq.n - rq.m;   // last key of the window's first token
     const int first = max(0, key0 - base) * group;   // earlier rows see no key of the tile
-    for (int row0 = first / kTile * kTile; row0 < rq.rows; row0 += kTile) {
-        load_q<D>(sm.q, a, rq, group, kvh, row0);
+    const int start = first / kTile * kTile;
+    if (start < rq.rows) f.rows(a, rq, group, kvh, start);
+    for (int row0 = start; row0 < rq.rows; row0 += kTile) {
+        f.put(sm.q);
         if (threadIdx.x < kTile) {   // merge the splits' statistics of the tile's rows
             float M = -INFINITY, l = 0.f;
             if (row0 + static_cast<int>(threadIdx.x) < rq.rows) {
@@ -243,6 +264,7 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
             sm.red[1][threadIdx.x][0] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         }
         __syncthreads();
+        if (row0 + kTile < rq.rows) f.rows(a, rq, group, kvh, row0 + kTile);
         float s[4][4];
         scores<D>(sm, a.scale_log2, s);
 #pragma unroll

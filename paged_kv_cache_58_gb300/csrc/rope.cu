@@ -32,7 +32,8 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 3;   // rows in flight per thread
+constexpr int kBatch = 2;   // rows in flight per thread (8192 tokens of 48 rows: 1, 3 and 6
+                            // took 38.8, 39.1 and 37.7 us, 2 takes 36.9)
 
 // Fraction of a turn per position, in units of 2^-64 turns.
 PKV_DEVINL uint64_t turn_fraction(double inv_freq) {
