@@ -7,12 +7,23 @@
 //
 // The side whose sums are wanted sits on the M side of the product, so it lies along the
 // TMEM lanes: a thread owns a query row (pass 1) or a key (pass 2) and reduces over its
-// own registers, with no exchange between threads in either pass.  An item holds up to
-// two A tiles (256 rows or keys) and streams B tiles past them; every B tile staged
-// serves both, which halves the copies per product.  Each A tile has two TMEM buffers of
-// 128 columns (all 512 columns) and two consumer warpgroups, one per half of the columns:
-// with 16 consumer warps a scheduler has four to switch between while loads from TMEM,
-// exponentials and barriers are under way (8 warps took 1.4 times as long).
+// own registers.  An item holds up to two A tiles (256 rows or keys) and streams B tiles
+// past them; every B tile staged serves both, which halves the copies per product.  Each A
+// tile has two TMEM buffers of 128 columns (all 512 columns) and two consumer warpgroups,
+// one per half of the columns: with 16 consumer warps a scheduler has four to switch
+// between while loads from TMEM, exponentials and barriers are under way (8 warps took 1.2
+// times as long).
+//
+// What bounds it: a product of 128 x 128 x 128 takes the tensor pipe 512 cycles, its 16384
+// exponentials 512 cycles at 32 a cycle, and its operands are read from shared memory at 128
+// bytes a cycle, all there is, so that the copies' writes (32 KB per B tile) and pass 2's
+// reads of -lse slow the products down.  On the 16 x 512-token batch (every new token, 3.2e11
+// flop a pass) the two passes take 284 and 288 us; 482 us together with the exponentials left
+// out and 326 us with one MMA in eight as well.  Measured there and not kept: four A tiles
+// per B tile with one TMEM buffer each (half the copies): 653 us for the call instead of 596;
+// B tiles of 256, whose products read 96 bytes a cycle, with one TMEM buffer per A tile: 638
+// us (425 us without exponentials: a tile's product and its exponentials take turns); equal
+// contiguous stretches of A tiles per CTA instead of every n-th item: 620 us.
 //
 // Pass 1 keeps the maximum of a row's first tile of the item as its reference and adds
 // 2^(s - m) from there on without looking for a larger one: there is no accumulator to
