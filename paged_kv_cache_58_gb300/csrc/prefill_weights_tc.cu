@@ -34,10 +34,10 @@
 // -log2(sum 2^s) per row, which is all that pass 2 needs:
 //   p = 2^(scale_log2 s - lse).
 //
-// Persistent CTAs, one per SM, each walking every gridDim.x-th item: producers run ahead
-// into the next item's tiles while the consumers finish the current one.  Roles: warps
-// 0-3 and 4-7 consumers, warp 8 A tiles, warp 9 B tiles, warp 10 MMA and TMEM, warp 11 the
-// B rows' -lse (pass 2).
+// Persistent CTAs, one per SM, each walking every gridDim.x-th item: producers run ahead into
+// the next item's tiles while the consumers finish the current one.  (Items sorted into large
+// ones first changed nothing: 593 us.)  Roles: warps 0-15 consumers, warp 16 A tiles, warp 17
+// B tiles, warp 18 MMA and TMEM, warp 19 the B rows' -lse (pass 2).
 #include <atomic>
 
 #include <cuda.h>
