@@ -404,8 +404,9 @@ pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int
 /* pkv_rope of a step's q rows into q_out, and pkv_kv_append of its k rows, turned, and v
  * rows, in one launch.  q, k, v: [num_tokens][heads][head_dim] with token strides as above
  * (q has num_q_heads heads, k and v the pool's); q_out may be q itself (same stride).
- * Slots as pkv_kv_append: a negative one skips the token's K and V (its q is turned all the
- * same), one past the pool raises PKV_ERR_OOB in the device status word. */
+ * Slots as pkv_kv_append, no two tokens with the same one: a negative slot skips the token's K
+ * and V (its q is turned all the same), one past the pool raises PKV_ERR_OOB in the device
+ * status word. */
 pkv_status pkv_rope_append(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
                            const int64_t* slot_mapping, void* q_out, int64_t q_out_stride,
                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -486,7 +487,7 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
  *   weights_out, positions_out  where the shrunk rows go: the inputs themselves (in place) or
  *                 buffers that do not overlap them.  Weights from new_lens[s] to L become 0;
  *                 positions_out holds new_lens[s] entries per head, the rest is not written.
- *   new_lens      device int32 [num_seqs], written; must not be one of the input arrays.
+ *   new_lens      device int32 [num_seqs], written; must not overlap an input array.
  *   row_ids       as above; a negative one leaves the sequence as it is (new_lens = L).
  *   sinks, recent >= 0.  weights_stride >= max_context.
  *   workspace     >= pkv_evict_workspace_bytes(...), 16-byte aligned, clobbered.

@@ -416,7 +416,11 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     unsigned long long first = block_scan(moved, sm.warp_sums, total);
     gather(total, 2, before, all);
     first += before;
-    const int nmoves = static_cast<int>(all >> 32);
+    // Equal counts, unless the weights change while they are read (a row used by two sequences
+    // at once): then no more moves than both lists hold.
+    const int most = a.max_context >> 1;
+    const int nmoves = min(min(static_cast<int>(all >> 32), static_cast<int>(all & 0xffffffffu)),
+                           most);
     for (int x = w0; x < w1; ++x) {
         hole_no[x] = static_cast<uint32_t>(first);
         mover_no[x] = static_cast<uint32_t>(first >> 32);
@@ -424,8 +428,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
                  static_cast<unsigned long long>(__popc(mover_mask(x))) << 32;
     }
     __syncthreads();
-    // lists of at most min(b, L - b) <= max_context / 2 moves
-    const int most = a.max_context >> 1;
+    // lists of at most min(b, L - b) <= max_context / 2 = most moves
     int32_t* holes = a.moves + (static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
                                    (5 * static_cast<size_t>(most));
     uint32_t* hole_slot = reinterpret_cast<uint32_t*>(holes + most);
@@ -473,6 +476,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
             if (i >= n) continue;
             if (j < b) {
                 if (to[u] >= 0) {
+                    if (to[u] >= most) continue;
                     holes[to[u]] = j;
                     hole_slot[to[u]] = slot[u];
                 } else {
@@ -480,7 +484,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
                     if (move_p || j >= tracked) po[j] = p[u];
                 }
             } else {
-                if (to[u] >= 0) {
+                if (to[u] >= 0 && to[u] < most) {
                     mover_slot[to[u]] = slot[u];
                     mover_w[to[u]] = x[u];
                     mover_pos[to[u]] = p[u];

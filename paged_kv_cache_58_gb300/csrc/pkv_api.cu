@@ -78,6 +78,8 @@ cudaStream_t copy_stream(int which) {
     return s;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // An NVTX range around each call that enqueues GPU work, named after the call, so that
@@ -282,7 +284,12 @@ struct WeightsOut {
 bool weights_ok(const WeightsOut& w, int num_seqs, int max_context) {
     return w.weights && w.stride >= max_context && w.num_rows > 0 &&
            (w.row_ids || w.num_rows >= num_seqs) && w.decay >= 0.f && w.decay <= 1.f &&
-           (reinterpret_cast<uintptr_t>(w.weights) & 3u) == 0;
+           aligned4(w.weights) && aligned4(w.row_ids);
+}
+
+// The scores are kept for whole partitions: none is longer than the context.
+int weights_partition(int partition_blocks, int max_context, int block_size) {
+    return std::min(partition_blocks, ceil_div(max_context, block_size));
 }
 
 size_t round16(size_t x) { return (x + 15) / 16 * 16; }
@@ -331,8 +338,9 @@ pkv_status decode_impl(const pkv_pool_desc* pool, void* out, const void* q, cons
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
         return PKV_ERR_INVALID;
 
-    const int pb = partition_blocks ? partition_blocks
-                                    : auto_partition(num_seqs, num_q_heads, max_context, B);
+    int pb = partition_blocks ? partition_blocks
+                              : auto_partition(num_seqs, num_q_heads, max_context, B);
+    if (wo) pb = weights_partition(pb, max_context, B);
     const int max_parts = ceil_div(ceil_div(max_context, B), pb);
     if (max_parts > pkv::kMaxParts) return PKV_ERR_UNSUPPORTED;
     size_t need = decode_workspace(num_seqs, num_q_heads, pool->head_dim, max_parts);
@@ -1011,8 +1019,10 @@ size_t pkv_paged_decode_weights_workspace_bytes(const pkv_pool_desc* pool, int n
         partition_blocks < 0)
         return 0;
     const int B = pool->block_size;
-    const int pb = partition_blocks ? partition_blocks
-                                    : auto_partition(num_seqs, num_q_heads, max_context, B);
+    const int pb = weights_partition(partition_blocks
+                                         ? partition_blocks
+                                         : auto_partition(num_seqs, num_q_heads, max_context, B),
+                                     max_context, B);
     WeightsWorkspace w;
     return weights_workspace(num_seqs, num_q_heads, pool->head_dim,
                              ceil_div(ceil_div(max_context, B), pb), pb << chunk_shift(B), &w)
@@ -1060,7 +1070,8 @@ pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int
     if (rotary_dim > head_dim) return PKV_ERR_INVALID;
     if (num_tokens == 0) return PKV_OK;
     if (num_tokens > INT32_MAX || num_heads > 1 << 20) return PKV_ERR_UNSUPPORTED;
-    if (!out || !x || !positions || !inv_freq || !aligned16(out) || !aligned16(x))
+    if (!out || !x || !positions || !inv_freq || !aligned16(out) || !aligned16(x) ||
+        !aligned4(positions) || !aligned8(inv_freq))
         return PKV_ERR_INVALID;
     const int es = elem_bytes(dtype);
     if (!stride_ok(out_stride, static_cast<int64_t>(num_heads) * head_dim, es) ||
@@ -1105,7 +1116,8 @@ pkv_status pkv_rope_append(const pkv_pool_desc* pool, void* k_pool, void* v_pool
     if (!k_pool || !v_pool || !slot_mapping || !q_out || !q || !k || !v || !positions || !inv_freq)
         return PKV_ERR_INVALID;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(q_out) || !aligned16(q) ||
-        !aligned16(k) || !aligned16(v))
+        !aligned16(k) || !aligned16(v) || !aligned8(slot_mapping) || !aligned4(positions) ||
+        !aligned8(inv_freq))
         return PKV_ERR_INVALID;
     const int es = elem_bytes(pool->dtype);
     if (!stride_ok(q_out_stride, static_cast<int64_t>(num_q_heads) * pool->head_dim, es) ||
@@ -1270,10 +1282,13 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
 
 namespace {
 
-// Same array, or no byte in common.
-bool same_or_apart(const void* a, const void* b, uint64_t bytes) {
+// No byte in common (`b` null: not given); or the same array.
+bool apart(const void* a, const void* b, uint64_t bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x == y || x + bytes <= y || y + bytes <= x;
+    return !b || x + bytes <= y || y + bytes <= x;
+}
+bool same_or_apart(const void* a, const void* b, uint64_t bytes) {
+    return a == b || apart(a, b, bytes);
 }
 
 }  // namespace
@@ -1311,9 +1326,16 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
     if (!same_or_apart(weights, weights_out, extent) ||
         !same_or_apart(positions, positions_out, extent))
         return PKV_ERR_INVALID;
-    // the heads of a sequence run at different times: nothing they read may change
-    if (new_lens == context_lens || new_lens == budgets || new_lens == seen_lens ||
-        new_lens == tracked_lens || new_lens == row_ids)
+    // the CTAs of a sequence run at different times: nothing they read may change meanwhile
+    const uint64_t lens = static_cast<uint64_t>(num_seqs) * sizeof(int32_t);
+    if (!apart(new_lens, context_lens, lens) || !apart(new_lens, budgets, lens) ||
+        !apart(new_lens, seen_lens, lens) || !apart(new_lens, tracked_lens, lens) ||
+        !apart(new_lens, row_ids, lens))
+        return PKV_ERR_INVALID;
+    if (!aligned4(context_lens) || !aligned4(budgets) || !aligned4(seen_lens) ||
+        !aligned4(tracked_lens) || !aligned4(row_ids) || !aligned4(new_lens) ||
+        !aligned4(positions) || !aligned4(positions_out) || !aligned4(weights_out) ||
+        !aligned4(block_tables))
         return PKV_ERR_INVALID;
     if (num_seqs > 65535 || max_context > pkv::kEvictMaxContext) return PKV_ERR_UNSUPPORTED;
     const size_t need = pkv_evict_workspace_bytes(pool, num_seqs, max_context);

@@ -170,6 +170,36 @@ def test_decode_weights_padding_and_lengths(pkv):
                                  workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
 
 
+def test_decode_weights_many_sequences(pkv):
+    """Enough sequences that the finishing launch works through several tiles per CTA, and a
+    partition far longer than the context: a few sequences against the 64-bit sums, all of them
+    against one another (each head's weights add up to the group)."""
+    g = gen(44)
+    S, hkv, group, d = 64, 8, 1, 64
+    lens = torch.randint(700, 2049, (S,), generator=torch.Generator().manual_seed(1)).tolist()
+    lens[5] = 2048
+    kp, vp, table = paged(lens, hkv, 16, d, torch.bfloat16, g)
+    q = torch.randn(S, hkv * group, d, generator=g, device="cuda").bfloat16()
+    w = torch.full((S, hkv, 2048), float("nan"), device="cuda")
+    for pb in (0, 1 << 20):
+        out = pkv.paged_decode_weights(q, kp, vp, table, i32(lens), 0.125, w, max_context=2048,
+                                       decay=0.0, partition_blocks=pb)
+        assert pkv.read_device_status() == 0
+        assert torch.equal(out, pkv.paged_decode(q, kp, vp, table, i32(lens), 0.125,
+                                                 max_context=2048,
+                                                 partition_blocks=min(pb, 128)))
+        kc, tc = kp.cpu(), table.cpu()
+        for i in range(S):
+            n = lens[i]
+            got = w[i, :, :n].cpu().double()
+            assert float((got.sum(-1) - group).abs().max()) < 1e-4
+            assert bool(torch.isnan(w[i, :, n:]).all())
+            if i % 16 == 5:
+                k = tokens(kc, tc[i], n)
+                _, p, size = attention(q[i:i + 1].cpu(), k, None, 0.125, first=n - 1)
+                assert bool(((got - p).abs() <= weight_bound(p, p * 0, size, d, n + group)).all())
+
+
 def test_decode_weights_growing_scores(pkv):
     """Scores that grow along the context, so that every partition's maximum differs and early
     tokens' weights underflow: nothing is lost where it counts, nothing is NaN."""
@@ -250,6 +280,96 @@ def test_prefill_weights(pkv, case):
     call(nans, 0.0)
     for i, n in enumerate(total):
         assert bool(torch.isfinite(nans[int(ids[i]), :, :n]).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_prefill_weights_growing_scores(pkv, dtype):
+    """Scores that grow far beyond a row's first tile (2^96 and more above it), then fall: the
+    sums are taken again from a larger reference, and nothing is lost where it counts."""
+    n, d = 900, 64
+    g = gen(19)
+    kp, _, table = paged([n], 1, 16, d, dtype, g)
+    ids = table[0, :57].long()
+    flat = kp[ids].transpose(1, 2).reshape(-1, d).clone()
+    flat[:n] = 0
+    j = torch.arange(n, device="cuda")
+    flat[:n, 0] = torch.where(j < 600, j // 4, 150 - (j - 600) // 4).to(dtype)   # 0 .. 150 .. 75
+    kp[ids] = flat.view(57, 16, 1, d).transpose(1, 2)
+    q = torch.zeros(40, 4, d, device="cuda", dtype=dtype)
+    q[..., 0] = torch.tensor([1.0, -1.0, 0.5, 2.0], device="cuda").to(dtype)
+    w = torch.zeros(1, 1, n, device="cuda")
+    pkv.paged_prefill_weights(q, kp, table, i32([n - 40]), i32([40]), i32([0, 40]), 1.0, w,
+                              max_new=40, max_context=n)
+    assert pkv.read_device_status() == 0
+    k = tokens(kp.cpu(), table.cpu()[0], n)
+    _, p, _ = attention(q.cpu(), k, None, 1.0, first=n - 40)
+    # scores are whole or half numbers up to 300 < 2^9, exact; times log2(e) and less the row's
+    # statistic, up to 2^9 each, they round by 2^-24 of that thrice: below 2^-13 of a weight; the
+    # exponentials and sums of 40 x 4 + 900 terms stay below 2^-13 too
+    err = (w[0].cpu().double() - p).abs()
+    assert bool((err <= p * 2.0 ** -12 + 160 * 2.0 ** -120).all()), (err / p.clamp(min=1e-30)).max()
+
+
+@pytest.mark.parametrize("rows", [False, True])
+def test_prefill_weights_many_requests(pkv, rows):
+    """More requests than one round of launches takes: 300 short ones, odd lengths."""
+    g = gen(23)
+    R, hkv, group, d = 300, 2, 2, 64
+    cached = [(7 * i) % 150 for i in range(R)]
+    new = [1 + (5 * i) % 9 for i in range(R)]
+    new[17] = 0
+    total = [c + n for c, n in zip(cached, new)]
+    kp, _, table = paged(total, hkv, 16, d, torch.bfloat16, g)
+    q = torch.randn(sum(new), hkv * group, d, generator=g, device="cuda").bfloat16()
+    off = [sum(new[:i]) for i in range(R + 1)]
+    ids = torch.randperm(R + 7, generator=g, device="cuda")[:R].to(torch.int32) if rows else None
+    w = torch.zeros(R + 7 if rows else R, hkv, max(total), device="cuda")
+    pkv.paged_prefill_weights(q, kp, table, i32(cached), i32(new), i32(off), 0.125, w, max_new=9,
+                              max_context=max(total), row_ids=ids)
+    assert pkv.read_device_status() == 0
+    kc, tc, qc, wc = kp.cpu(), table.cpu(), q.cpu(), w.cpu().double()
+    for i in range(R):
+        row = int(ids[i]) if rows else i
+        n = total[i]
+        if new[i] == 0:
+            assert bool((wc[row] == 0).all())
+            continue
+        k = tokens(kc, tc[i], n)
+        _, p, size = attention(qc[off[i]:off[i + 1]], k, None, 0.125, first=cached[i])
+        err = (wc[row, :, :n] - p).abs()
+        assert bool((err <= weight_bound(p, p * 0, size, d, n + new[i] * group)).all()), i
+        assert bool((wc[row, :, n:] == 0).all())
+
+
+def test_two_streams_at_once(pkv):
+    """Calls of both forms on two streams at the same time, each with its own workspace."""
+    g = gen(29)
+    lens, hkv, group, d = [900, 300, 1200], 2, 4, 128
+    kp, vp, table = paged(lens, hkv, 16, d, torch.bfloat16, g)
+    qs = torch.randn(2, 3, hkv * group, d, generator=g, device="cuda").bfloat16()
+    qp = torch.randn(2, 90, hkv * group, d, generator=g, device="cuda").bfloat16()
+    off, nl = i32([0, 40, 50, 90]), i32([40, 10, 40])
+    cached, cl = i32([860, 290, 1160]), i32(lens)
+
+    def run(i, w, stream=None):
+        for _ in range(5):
+            pkv.paged_prefill_weights(qp[i], kp, table, cached, nl, off, 0.09, w, max_new=40,
+                                      max_context=1200, stream=stream)
+            pkv.paged_decode_weights(qs[i], kp, vp, table, cl, 0.09, w, max_context=1200,
+                                     stream=stream)
+
+    want = [torch.zeros(3, hkv, 1200, device="cuda") for _ in range(2)]
+    for i in range(2):
+        run(i, want[i])
+    got = [torch.zeros(3, hkv, 1200, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        run(i, got[i], streams[i])
+    torch.cuda.synchronize()
+    assert pkv.read_device_status() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
 
 
 def test_prefill_weights_of_one_token_are_the_decodes(pkv):

@@ -94,6 +94,8 @@ CASES = [  # lens, budgets, hkv, bs, d, dtype, sinks, recent
     ([3000], [2999], 1, 16, 128, torch.bfloat16, 0, 128),
     ([5000, 130], [700, 128], 1, 32, 64, torch.float32, 1, 100),
     ([20000], [1000], 1, 16, 64, torch.bfloat16, 4, 256),
+    ([5000, 3000], [50, 2999], 1, 16, 64, torch.bfloat16, 60, 10),   # protected ones compete
+    ([9000], [0], 1, 16, 64, torch.bfloat16, 4, 4),
 ]
 
 
@@ -140,6 +142,76 @@ def test_evict(pkv, case, in_place, kind):
     other = int(order[S])
     assert torch.equal(bits(wo[other]), bits(w[other])) if in_place else bool(
         (wo[other] == 5).all())
+
+
+@pytest.mark.parametrize("kind", ["spread", "zeros"])
+def test_evict_many_rows(pkv, kind):
+    """Enough rows that each is one CTA's, over more entries than it lists."""
+    lens = [2100 - 37 * i for i in range(40)]
+    budgets = [300 + 40 * (i % 7) for i in range(40)]
+    kp, vp, table, g = setup(lens, 8, 16, 64, torch.bfloat16, 6)
+    w = torch.rand(40, 8, 2100, generator=g, device="cuda")
+    if kind == "zeros":
+        w = torch.where(w < 0.9, torch.zeros_like(w), w)
+    pos = torch.zeros(40, 8, 2100, dtype=torch.int32, device="cuda")
+    want = expect(kp, vp, table, lens, budgets, w, pos, 4, 64, lens, [0] * 40, list(range(40)))
+    left = pkv.evict(kp, vp, table, i32(lens), i32(budgets), w, pos, max_context=2100, sinks=4,
+                     recent=64)
+    assert pkv.read_device_status() == 0 and left.tolist() == want[4]
+    assert torch.equal(w.cpu(), want[2]) and same_positions(pos, want[3], range(40), want[4])
+    assert torch.equal(bits(kp), bits(want[0])) and torch.equal(bits(vp), bits(want[1]))
+
+
+def test_evict_long_row(pkv):
+    """A context past eight slices of 16384 entries, and one of the largest the call takes."""
+    lens = [140001]
+    kp, vp, table, g = setup(lens, 1, 32, 64, torch.bfloat16, 12)
+    w = torch.exp(2 * torch.randn(1, 1, 140001, generator=g, device="cuda"))
+    pos = torch.zeros(1, 1, 140001, dtype=torch.int32, device="cuda")
+    want = expect(kp, vp, table, lens, [9000], w, pos, 4, 1000, lens, [0], [0])
+    left = pkv.evict(kp, vp, table, i32(lens), i32([9000]), w, pos, max_context=140001, sinks=4,
+                     recent=1000)
+    assert pkv.read_device_status() == 0 and left.tolist() == [9000]
+    assert torch.equal(w.cpu(), want[2]) and same_positions(pos, want[3], [0], [9000])
+    assert torch.equal(bits(kp), bits(want[0])) and torch.equal(bits(vp), bits(want[1]))
+
+    n = 1 << 20
+    kp, vp, table, g = setup([n], 1, 32, 64, torch.bfloat16, 13)
+    w = torch.rand(1, 1, n, generator=g, device="cuda")
+    w0, k0 = w.clone(), kp.clone()
+    pos = torch.zeros(1, 1, n, dtype=torch.int32, device="cuda")
+    left = pkv.evict(kp, vp, table, i32([n]), i32([100000]), w, pos, max_context=n)
+    assert pkv.read_device_status() == 0 and left.tolist() == [100000]
+    order = torch.sort(w0[0, 0], descending=True, stable=True).indices[:100000]
+    kept = pos[0, 0, :100000].long()
+    assert torch.equal(kept.sort().values, order.sort().values)
+    assert torch.equal(w[0, 0, :100000], w0[0, 0][kept])
+    assert bool((w[0, 0, 100000:] == 0).all())
+    at = torch.arange(100000, device="cuda")
+    rows = kp[table[0].long()[at // 32], 0, at % 32]
+    src = k0[table[0].long()[kept // 32], 0, kept % 32]
+    assert torch.equal(rows, src)
+
+
+def test_two_evictions_at_once(pkv):
+    """Different sequences of one pool on two streams at the same time."""
+    lens = [700, 800]
+    kp, vp, table, g = setup(lens, 2, 16, 64, torch.bfloat16, 15)
+    w = torch.rand(2, 2, 800, generator=g, device="cuda")
+    pos = torch.zeros(2, 2, 800, dtype=torch.int32, device="cuda")
+    want = expect(kp, vp, table, lens, [200, 300], w, pos, 2, 20, lens, [0, 0], [0, 1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    cl, b = i32(lens), i32([200, 300])
+    ids = i32([0, 1])
+    torch.cuda.synchronize()
+    left = [pkv.evict(kp, vp, table[i:i + 1], cl[i:i + 1], b[i:i + 1], w, pos, max_context=800,
+                      sinks=2, recent=20, row_ids=ids[i:i + 1], stream=streams[i])
+            for i in range(2)]
+    torch.cuda.synchronize()
+    assert pkv.read_device_status() == 0
+    assert [int(x) for x in left] == [200, 300]
+    assert torch.equal(w.cpu(), want[2]) and same_positions(pos, want[3], [0, 1], [200, 300])
+    assert torch.equal(bits(kp), bits(want[0])) and torch.equal(bits(vp), bits(want[1]))
 
 
 def test_defaults_and_padding(pkv):

@@ -182,6 +182,7 @@ def test_rope_checks(pkv):
     assert r(os=1028) == INVALID              # not whole 16-byte chunks
     assert r(xs=1028) == INVALID and r(xs=-1024) == INVALID
     assert r(T=1 << 31) == UNSUPPORTED
+    assert r(pos=0x10002) == INVALID and r(f=0x10004) == INVALID
 
 
 @fake
@@ -230,6 +231,9 @@ def test_decode_weights_checks(pkv):
     # one partition needs a workspace too: the scores go there
     one = lib.pkv_paged_decode_weights_workspace_bytes(ctypes.byref(desc(pkv)), 2, 32, 100, 7)
     assert w(pb=7, wsb=one - 1) == NOMEM
+    # a partition longer than the context needs no more than one of the context
+    assert lib.pkv_paged_decode_weights_workspace_bytes(ctypes.byref(desc(pkv)), 2, 32, 100,
+                                                        1 << 30) == one
     ask = lib.pkv_paged_decode_weights_workspace_bytes
     assert ask(ctypes.byref(desc(pkv)), 0, 32, 100, 0) == 0
     assert ask(ctypes.byref(desc(pkv, d=96)), 2, 32, 100, 0) == 0
@@ -279,6 +283,10 @@ def test_evict_checks(pkv):
     assert e(wo=A + 16) == INVALID and e(poo=A + 4096) == INVALID   # overlap, not the same
     for name in ("cl", "bu", "seen", "tracked", "ids"):
         assert e(**{name: A2}) == INVALID, name                     # new_lens is an input
+        assert e(**{name: A2 + 4}) == INVALID, name                 # overlaps one by a value
+    for name in ("cl", "bu", "seen", "tracked", "ids", "nl", "po", "poo", "wo", "bt"):
+        assert e(**{name: 0x9000002}) == INVALID, name              # not on 4 bytes
+    assert e(max_ctx=(1 << 20) + 1, mbs=1 << 17, stride=1 << 21) == UNSUPPORTED
     need = lib.pkv_evict_workspace_bytes(ctypes.byref(desc(pkv)), 2, 100)
     assert need > 0
     assert e(wsb=need - 1) == NOMEM and e(ws=None) == NOMEM and e(ws=U) == NOMEM
