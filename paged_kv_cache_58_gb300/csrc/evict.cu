@@ -25,10 +25,16 @@
 //   4. after one cluster barrier all threads copy the listed rows, 16 bytes of K and of V
 //      per lane, four rows in flight per lane and the places of the next four looked up
 //      meanwhile.
+// Measured (one call of many, from a graph): 64 x 8 rows of 1040 entries, 16 over budget, 13.9
+// us, the chain of dependent steps (about 1.7 us to start, 2 a scan, 1 a narrowing, 2 to list);
+// 512 to 4096 down to 1024, 68.5 us, 44 of them the moves at 5.7 TB/s; 16 x 8 rows of 16k to
+// 128k down to 8192, 241 us, 133 of them the moves at 7.3 TB/s, the rest three scans of 10.9 M
+// entries at about 90 issue slots per 32.
 // With C = 1 there are no cluster barriers.  The scans read the weights where they are, in
 // L2 after the first: keys kept in shared memory left two CTAs on an SM and a row's
-// latencies uncovered, where without them six fit.  Weights crowd into few exponents (and
-// many may be zero): the lanes that share the first lane's digit count at once.
+// latencies uncovered.  Weights crowd into few exponents (and many may be zero), but counting
+// the lanes that share a digit at once, with votes, was slower than one shared-memory atomic
+// per entry (16 x 128k tokens: 256 against 245 us; with all weights zero 230 against 204).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -59,7 +65,7 @@ PKV_DEVINL uint32_t order_key(float w) {
 PKV_DEVINL int spread(int bin) { return bin + (bin >> 3); }
 constexpr int kHist = kBins + kBins / 8;
 
-struct Shared {   // after it: bits and numbers per 32 entries
+struct Shared {   // after it: three bits per entry
     int hist[kHist];
     int cluster_hist[kHist];          // the cluster's, in its first CTA
     uint32_t list_key[kList];
@@ -94,20 +100,6 @@ PKV_DEVINL V block_scan(V v, unsigned long long* warp_sums, V& total) {
     return before + incl - v;
 }
 
-// Adds `digit` of the lanes with `on` to the histogram (all lanes of the warp call).
-PKV_DEVINL void count_digit(int* hist, bool on, uint32_t digit) {
-    const uint32_t active = __ballot_sync(0xffffffffu, on);
-    if (active == 0) return;
-    const int lead = __ffs(active) - 1;
-    const uint32_t lead_digit = __shfl_sync(0xffffffffu, digit, lead);
-    const bool like = on && digit == lead_digit;
-    const uint32_t same = __ballot_sync(0xffffffffu, like);
-    if (static_cast<int>(threadIdx.x & 31) == lead)
-        atomicAdd(&hist[spread(digit)], __popc(same));
-    else if (on && !like)
-        atomicAdd(&hist[spread(digit)], 1);
-}
-
 // F: entries in flight per thread in a scan.
 template <int F>
 __global__ void __launch_bounds__(NT, 4)
@@ -117,8 +109,6 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     uint32_t* safe_bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));   // protected
     uint32_t* keep_bits = safe_bits + words;
     uint32_t* tie_bits = keep_bits + words;      // equal to the threshold
-    uint32_t* hole_no = tie_bits + words;        // freed places before these 32 entries
-    uint32_t* mover_no = hole_no + words;        // movers before them
     griddep_wait();
     griddep_launch_dependents();
     const int kvh = blockIdx.x / C, rank = blockIdx.x % C, seq = blockIdx.y;
@@ -200,7 +190,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
                 safe_bits[i >> 5] = ball;
                 mine += __popc(ball);
             }
-            count_digit(sm.hist, in && !s, in ? order_key(x[u]) >> 21 : 0u);
+            if (in && !s) atomicAdd(&sm.hist[spread(order_key(x[u]) >> 21)], 1);
         }
     }
     int cta_safe;
@@ -240,7 +230,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         for (int i = tid; i < kHist; i += NT) sm.hist[i] = 0;
         __syncthreads();
         scan([&](int i, bool in, float x) {
-            count_digit(sm.hist, in && competes(i), order_key(x) >> 21);
+            if (in && competes(i)) atomicAdd(&sm.hist[spread(order_key(x) >> 21)], 1);
         });
         __syncthreads();
     }
@@ -315,19 +305,18 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
                                               : !among_safe);
             const bool inside = rival && open && k == prefix;
             const uint32_t kept = __ballot_sync(0xffffffffu, keep);
-            const uint32_t found = __ballot_sync(0xffffffffu, inside);
             if (lane == 0) {
                 keep_bits[i >> 5] = kept;
                 tie_bits[i >> 5] = 0;
             }
             if (inside) {
+                atomicAdd(&sm.hist[spread((key >> 10) & 2047u)], 1);
                 const int slot = atomicAdd(&sm.listed, 1);
                 if (slot < kList) {
                     sm.list_key[slot] = key;
                     sm.list_at[slot] = i;
                 }
             }
-            if (found) count_digit(sm.hist, inside, (key >> 10) & 2047u);
         }
     }
     __syncthreads();
@@ -365,7 +354,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         narrow(10, 2047u);
         if (in_bin != need) {   // the last ten bits
             candidates([&](int, bool on, uint32_t key) {
-                count_digit(sm.hist, on && (key & mask) == prefix, key & 1023u);
+                if (on && (key & mask) == prefix) atomicAdd(&sm.hist[spread(key & 1023u)], 1);
             });
             __syncthreads();
             narrow(0, 1023u);
@@ -421,18 +410,11 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     const int most = a.max_context >> 1;
     const int nmoves = min(min(static_cast<int>(all >> 32), static_cast<int>(all & 0xffffffffu)),
                            most);
-    for (int x = w0; x < w1; ++x) {
-        hole_no[x] = static_cast<uint32_t>(first);
-        mover_no[x] = static_cast<uint32_t>(first >> 32);
-        first += static_cast<unsigned long long>(__popc(hole_mask(x))) |
-                 static_cast<unsigned long long>(__popc(mover_mask(x))) << 32;
-    }
-    __syncthreads();
     // lists of at most min(b, L - b) <= max_context / 2 = most moves
     int32_t* holes = a.moves + (static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
                                    (5 * static_cast<size_t>(most));
-    uint32_t* hole_slot = reinterpret_cast<uint32_t*>(holes + most);
-    uint32_t* mover_slot = hole_slot + most;
+    int32_t* movers = holes + most;
+    uint32_t* mover_slot = reinterpret_cast<uint32_t*>(movers + most);
     float* mover_w = reinterpret_cast<float*>(mover_slot + most);
     int32_t* mover_pos = holes + 4 * static_cast<size_t>(most);
     // Pool slots fit 32 bits: 2^32 rows of the least 128 bytes are more than this GPU holds.
@@ -447,52 +429,67 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         }
         return (static_cast<uint32_t>(phys) << a.block_shift) + (static_cast<uint32_t>(j) & low);
     };
-    const uint32_t lower = (1u << lane) - 1u;
-    // Several entries per thread at a time, loads before stores: in place the compiler cannot
-    // tell that a store does not change what the next entry loads.
-    constexpr int U3 = F;
-    for (int ib = tid; ib < n; ib += U3 * NT) {
-        float x[U3];
-        int p[U3], to[U3];   // to: the entry's number in its list, or -1
-        uint32_t slot[U3];
+    // The listed entries' indices, word by word, then what goes with them, entry by entry with
+    // every lane at work (one entry in ten is listed where 128k tokens shrink to 8k).
+    int h = static_cast<int>(first & 0xffffffffu), m = static_cast<int>(first >> 32);
+    for (int x = w0; x < w1; ++x) {
+        for (uint32_t bits = hole_mask(x); bits; bits &= bits - 1, ++h)
+            if (h < most) holes[h] = i0 + 32 * x + __ffs(bits) - 1;
+        for (uint32_t bits = mover_mask(x); bits; bits &= bits - 1, ++m)
+            if (m < most) movers[m] = i0 + 32 * x + __ffs(bits) - 1;
+    }
+    __syncthreads();
+    const int m0 = static_cast<int>(before >> 32);
+    const int m1 = min(m0 + static_cast<int>(total >> 32), most);
+    for (int kb = m0 + tid; kb < m1; kb += F * NT) {
+        int j[F], p[F];
+        uint32_t slot[F];
+        float x[F];
 #pragma unroll
-        for (int u = 0; u < U3; ++u) {
-            const int i = ib + u * NT, j = i0 + i;
-            to[u] = -1;
-            if (i >= n) continue;
-            const int word = i >> 5;
-            const bool under = j < b;
-            const uint32_t listed = under ? hole_mask(word) : mover_mask(word);
-            if (listed >> lane & 1u)
-                to[u] = static_cast<int>((under ? hole_no : mover_no)[word] +
-                                         __popc(listed & lower));
-            if (to[u] >= 0) slot[u] = slot_of(j);
-            if (under ? to[u] < 0 && move_w : to[u] >= 0) x[u] = w[j];
-            if (under ? to[u] < 0 && (move_p || j >= tracked) : to[u] >= 0) p[u] = position(j);
+        for (int u = 0; u < F; ++u) {
+            const int k = kb + u * NT;
+            j[u] = k < m1 ? movers[k] : -1;
         }
 #pragma unroll
-        for (int u = 0; u < U3; ++u) {
-            const int i = ib + u * NT, j = i0 + i;
-            if (i >= n) continue;
-            if (j < b) {
-                if (to[u] >= 0) {
-                    if (to[u] >= most) continue;
-                    holes[to[u]] = j;
-                    hole_slot[to[u]] = slot[u];
-                } else {
-                    if (move_w) wo[j] = x[u];
-                    if (move_p || j >= tracked) po[j] = p[u];
-                }
-            } else {
-                if (to[u] >= 0 && to[u] < most) {
-                    mover_slot[to[u]] = slot[u];
-                    mover_w[to[u]] = x[u];
-                    mover_pos[to[u]] = p[u];
-                }
-                wo[j] = 0.f;   // a free place starts at zero
-            }
+        for (int u = 0; u < F; ++u) {
+            if (j[u] < 0) continue;
+            slot[u] = slot_of(j[u]);
+            x[u] = w[j[u]];
+            p[u] = position(j[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            const int k = kb + u * NT;
+            if (j[u] < 0) continue;
+            mover_slot[k] = slot[u];
+            mover_w[k] = x[u];
+            mover_pos[k] = p[u];
         }
     }
+    __syncthreads();
+    // What stays keeps its place (the freed places are filled in step 4), and the places past
+    // the budget start at zero.
+    const int under = min(max(b - i0, 0), n);   // entries of the slice below the budget
+    if (move_w || move_p || i0 + under > tracked)
+        for (int ib = tid; ib < under; ib += F * NT) {
+            float x[F];
+            int p[F];
+#pragma unroll
+            for (int u = 0; u < F; ++u) {
+                const int i = ib + u * NT;
+                if (i >= under) continue;
+                if (move_w) x[u] = w[i0 + i];
+                if (move_p || i0 + i >= tracked) p[u] = position(i0 + i);
+            }
+#pragma unroll
+            for (int u = 0; u < F; ++u) {
+                const int i = ib + u * NT;
+                if (i >= under) continue;
+                if (move_w) wo[i0 + i] = x[u];
+                if (move_p || i0 + i >= tracked) po[i0 + i] = p[u];
+            }
+        }
+    for (int i = under + tid; i < n; i += NT) wo[i0 + i] = 0.f;
     if (C > 1)
         cluster.sync();
     else
@@ -521,8 +518,11 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u * step;
             from[u] = k < nmoves ? mover_slot[k] : kNoSlot;
-            to[u] = k < nmoves ? hole_slot[k] : kNoSlot;
+            to[u] = k < nmoves ? static_cast<uint32_t>(holes[k]) : kNoSlot;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (to[u] != kNoSlot) to[u] = slot_of(static_cast<int>(to[u]));
     };
     int k0 = worker >> csh;
     look_up(k0);
@@ -554,8 +554,8 @@ template <int F>
 cudaError_t launch_f(const EvictArgs& a, int C, cudaStream_t stream) {
     auto kern = evict_kernel<F>;
     const int words = ((a.max_context + C - 1) / C + 31) / 32;
-    const int smem = static_cast<int>(sizeof(Shared)) + 5 * 4 * words;
-    static_assert(sizeof(Shared) + 5 * 4 * (kEvictMaxContext / kMaxCluster / 32) <= 232448,
+    const int smem = static_cast<int>(sizeof(Shared)) + 3 * 4 * words;
+    static_assert(sizeof(Shared) + 3 * 4 * (kEvictMaxContext / kMaxCluster / 32) <= 232448,
                   "the bits of the longest slice fit");
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
