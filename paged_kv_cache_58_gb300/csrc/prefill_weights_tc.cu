@@ -206,26 +206,12 @@ PKV_DEVINL float sum8(const float (&v)[8]) {
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
-// The K box of tile `tile`, chunk `lane` (lanes below the tile's chunk count).
+// The K boxes of one tile: lane b < nb copies 16-token chunk `chunk`, in block `phys`.
 template <int D>
-PKV_DEVINL void copy_k_tile(const PrefillWeightsArgs& a, const void* tm_k, const Item& it, int tile,
-                            uint8_t* dst, uint64_t* bar, int lane) {
+PKV_DEVINL void copy_k_boxes(const PrefillWeightsArgs& a, const void* tm_k, const Item& it,
+                             int chunk, int phys, int nb, uint8_t* dst, uint64_t* bar, int lane) {
     using GM = Geom<D>;
-    const int chunks = ceil_div(it.q.c + it.q.n, kChunk);
-    const int first = tile * kBoxes;
-    const int nb = min(kBoxes, chunks - first);
-    const int chunk = first + (lane & 7);
     const int csh = a.block_shift - 4;
-    int phys = 0;
-    if (lane < nb) {
-        phys = __ldg(a.block_tables + static_cast<size_t>(it.r) * a.max_blocks_per_seq +
-                     (chunk >> csh));
-        if (phys < 0 || phys >= a.num_blocks) {
-            raise_status(a.status, PKV_ERR_OOB);
-            phys = 0;   // keeps the byte count; the request's weights are not valid
-        }
-    }
-    __syncwarp();
     const int row = ((phys * a.num_kv_heads + it.kvh) << a.block_shift) +
                     (chunk & ((1 << csh) - 1)) * kChunk;
     mbar_arrive_expect_tx_if(lane == 0, bar, nb * GM::kChunkBytes);
@@ -234,6 +220,22 @@ PKV_DEVINL void copy_k_tile(const PrefillWeightsArgs& a, const void* tm_k, const
         tma_load_4d_if(lane < nb, dst + lane * GM::kChunkBytes, tm_k, 0, 0, 0, row / 8, bar);
     else
         tma_load_2d_if(lane < nb, dst + lane * GM::kChunkBytes, tm_k, 0, row, bar);
+}
+
+// The block of the request's 16-token chunk `chunk`, or 0 past its end; a bad id is reported
+// and replaced by 0, which keeps the byte counts (the request's weights are then not valid).
+PKV_DEVINL int block_of(const PrefillWeightsArgs& a, const Item& it, int chunk, int chunks) {
+    int phys = 0;
+    if (chunk < chunks) {
+        phys = __ldg(a.block_tables + static_cast<size_t>(it.r) * a.max_blocks_per_seq +
+                     (chunk >> (a.block_shift - 4)));
+        if (phys < 0 || phys >= a.num_blocks) {
+            raise_status(a.status, PKV_ERR_OOB);
+            phys = 0;
+        }
+    }
+    __syncwarp();
+    return phys;
 }
 
 // The Q tile `tile` of the window's rows.
@@ -344,27 +346,8 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                 const int chunks = ceil_div(it.q.c + it.q.n, kChunk);
                 const int first = it.a0 * kBoxes;
                 const int n = min(2 * kBoxes, chunks - first);
-                const int csh = a.block_shift - 4;
-                int phys = 0;
-                if (lane < n) {
-                    phys = __ldg(a.block_tables +
-                                 static_cast<size_t>(it.r) * a.max_blocks_per_seq +
-                                 ((first + lane) >> csh));
-                    if (phys < 0 || phys >= a.num_blocks) {
-                        raise_status(a.status, PKV_ERR_OOB);
-                        phys = 0;
-                    }
-                }
-                __syncwarp();
-                const int row = ((phys * a.num_kv_heads + it.kvh) << a.block_shift) +
-                                ((first + lane) & ((1 << csh) - 1)) * kChunk;
-                mbar_arrive_expect_tx_if(lane == 0, bar, n * GM::kChunkBytes);
-                __syncwarp();
-                if constexpr (D == 128)
-                    tma_load_4d_if(lane < n, dst + lane * GM::kChunkBytes, &tm_k, 0, 0, 0, row / 8,
-                                   bar);
-                else
-                    tma_load_2d_if(lane < n, dst + lane * GM::kChunkBytes, &tm_k, 0, row, bar);
+                const int phys = block_of(a, it, lane < n ? first + lane : chunks, chunks);
+                copy_k_boxes<D>(a, &tm_k, it, first + lane, phys, n, dst, bar, lane);
             }
             ++issued;
         }
@@ -377,7 +360,11 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
         int g = 0;
         bool ok = true;
         while (ok && walk.next(it)) {
+            const int chunks = ceil_div(it.q.c + it.q.n, kChunk);
+            int ids = 0;   // pass 1: the blocks of the next four tiles' chunks, one per lane
             for (int j = 0; j < it.nb; ++j) {
+                if (PASS == 1 && (j & 3) == 0)
+                    ids = block_of(a, it, (it.b0 + j) * kBoxes + lane, chunks);
                 const int s = g % GM::kStagesB;
                 if (g >= GM::kStagesB &&
                     !wait_bar(ctl, GM::B_EMPTY + s, (g / GM::kStagesB - 1) & 1)) {
@@ -385,10 +372,15 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                     break;
                 }
                 uint8_t* dst = smem + GM::kOffB + s * GM::kTileBytes;
-                if (PASS == 1)
-                    copy_k_tile<D>(a, &tm_k, it, it.b0 + j, dst, &bars[GM::B_FULL + s], lane);
-                else
-                    copy_q_tile<D>(a, &tm_q, it, it.b0 + j, dst, &bars[GM::B_FULL + s], lane);
+                uint64_t* bar = &bars[GM::B_FULL + s];
+                if (PASS == 1) {
+                    const int first = (it.b0 + j) * kBoxes;
+                    const int id = __shfl_sync(0xffffffffu, ids, (j & 3) * kBoxes + (lane & 7));
+                    copy_k_boxes<D>(a, &tm_k, it, first + (lane & 7), id,
+                                    min(kBoxes, chunks - first), dst, bar, lane);
+                } else {
+                    copy_q_tile<D>(a, &tm_q, it, it.b0 + j, dst, bar, lane);
+                }
                 ++g;
             }
         }
