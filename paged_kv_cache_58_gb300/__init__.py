@@ -239,7 +239,7 @@ _POOL_DESCS: dict = {}
 def pool_desc(k_pool: torch.Tensor) -> PoolDesc:
     """The pool descriptor of a [num_blocks, Hkv, B, D] pool (cached per shape and dtype:
     it holds sizes only)."""
-    key = (tuple(k_pool.shape), k_pool.dtype)
+    key = (k_pool.shape, k_pool.dtype)
     d = _POOL_DESCS.get(key)
     if d is None:
         nb, hkv, bs, dim = key[0]
@@ -636,11 +636,17 @@ def _workspace_arg(ws, need, dev, stream):
 
 def _pools(k_pool, v_pool):
     """(descriptor, device, K address, V address) of a pair of pools."""
-    dev, dt, shape = _device(k_pool, "k_pool"), k_pool.dtype, k_pool.shape
-    if len(shape) != 4:
-        raise ValueError("k_pool must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    return (pool_desc(k_pool), dev, _arg(k_pool, "k_pool", dev, dt, shape),
-            _arg(v_pool, "v_pool", dev, dt, shape))
+    dev, dt, shape = k_pool.get_device(), k_pool.dtype, k_pool.shape
+    if dev < 0 or dev != _cur_device():
+        _device(k_pool, "k_pool")
+    d = _POOL_DESCS.get((shape, dt))
+    if d is None:
+        if len(shape) != 4:
+            raise ValueError("k_pool must be [num_blocks, num_kv_heads, block_size, head_dim]")
+        d = pool_desc(k_pool)
+    if not k_pool.is_contiguous():
+        raise ValueError("k_pool must be contiguous")
+    return d, dev, k_pool.data_ptr(), _arg(v_pool, "v_pool", dev, dt, shape)
 
 
 def _weights_arg(weights, dev, dtype, hkv, name="weights"):

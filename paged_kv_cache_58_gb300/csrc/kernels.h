@@ -244,13 +244,23 @@ struct PrefillWeightsArgs {
     int splits;        // parts the keys of a query tile are split into in pass 1
     int chunk_tiles;   // tensor cores: 128-key tiles per split
     int rows_pad;      // rows of one (request, kv head, split) in `stats`: a multiple of 128
-    int group_shift;   // tensor cores: log2(G)
+    int group_shift;   // log2(G)
+    // Pass 2 splits a key tile's rows into row_parts of rows_per_part (a multiple of 128) where
+    // there are few key tiles; with more than one, each part's sums go to `parts`
+    // ([R][Hkv][row_parts][max_context], workspace) and a last launch adds them up.
+    int row_parts;
+    int rows_per_part;
+    float* parts;
     float scale_log2;
     float decay;
 };
 // fp32 pools, on the CUDA cores.
 cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int head_dim, int group,
                                    cudaStream_t stream);
+// The last launch of either where row_parts > 1: weights = decay * weights + the parts' sums.
+// key_unit, row_unit: keys per pass-2 item and rows per tile, which say what parts a key has.
+cudaError_t launch_add_parts(const PrefillWeightsArgs& a, int key_unit, int row_unit,
+                             cudaStream_t stream);
 // bf16 pools, on the tensor cores.
 cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, int head_dim, int group,
                                       cudaStream_t stream);

@@ -1161,8 +1161,8 @@ int window_rows(int max_new, int window) {
 
 // How pass 1 cuts the keys of a query tile, and the workspace that gives.
 struct PrefillWeightsPlan {
-    int rows_pad, splits, chunk_tiles;
-    size_t stats_bytes, bytes;
+    int rows_pad, splits, chunk_tiles, row_parts, rows_per_part;
+    size_t stats_bytes, lse_bytes, bytes;
 };
 bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_heads, int max_new,
                           int max_context, int window, PrefillWeightsPlan* p) {
@@ -1171,28 +1171,39 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
     if (rows > INT32_MAX - 128) return false;
     p->rows_pad = static_cast<int>((rows + 127) / 128 * 128);
     const int64_t heads = static_cast<int64_t>(num_reqs) * pool->num_kv_heads;
-    if (pool->dtype == PKV_F32) {
+    const bool f32 = pool->dtype == PKV_F32;
+    const int tiles = ceil_div(max_context, 128);
+    const int row_tiles = p->rows_pad / 128;
+    if (f32) {
         // CUDA cores: 64-row by 64-key tiles; parts of the keys until there are two CTAs per SM.
         const int64_t ctas = heads * (p->rows_pad / 64);
         p->chunk_tiles = 0;
         p->splits = static_cast<int>(std::min<int64_t>(
             std::min<int64_t>((2 * 152 + ctas - 1) / ctas, ceil_div(max_context, 64)), 32));
-        p->bytes = p->stats_bytes =
-            static_cast<size_t>(heads) * p->splits * p->rows_pad * sizeof(float2);
-        return true;
+    } else {
+        // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 582 us for the
+        // call, 594 with 16, 609 with 8, where the parts' own first tiles and statistics
+        // count), shorter where there would be fewer than two items per SM, and at most 32 of
+        // them.  The lengths are not known here, only their bound.
+        const int64_t items = heads * ((row_tiles + 1) / 2);
+        p->chunk_tiles = static_cast<int>(
+            std::max<int64_t>(2, std::min<int64_t>(24, (items * tiles + 303) / 304)));
+        p->chunk_tiles = std::max(p->chunk_tiles, ceil_div(tiles, 32));
+        p->splits = ceil_div(tiles, p->chunk_tiles);
     }
-    // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 582 us for the
-    // call, 594 with 16, 609 with 8, where the parts' own first tiles and statistics count),
-    // shorter where there would be fewer than two items per SM, and at most 32 of them.  The
-    // lengths are not known here, only their bound.
-    const int64_t items = heads * ((p->rows_pad / 128 + 1) / 2);
-    const int tiles = ceil_div(max_context, 128);
-    p->chunk_tiles = static_cast<int>(
-        std::max<int64_t>(2, std::min<int64_t>(24, (items * tiles + 303) / 304)));
-    p->chunk_tiles = std::max(p->chunk_tiles, ceil_div(tiles, 32));
-    p->splits = ceil_div(tiles, p->chunk_tiles);
-    p->stats_bytes = static_cast<size_t>(heads) * p->splits * 2 * p->rows_pad * sizeof(float2);
-    p->bytes = p->stats_bytes + static_cast<size_t>(heads) * p->rows_pad * sizeof(float);
+    // Pass 2: parts of the rows, of two tiles of 128 at least, until there are two items per SM.
+    const int64_t items2 = heads * (f32 ? ceil_div(max_context, 64) : (tiles + 1) / 2);
+    const int most = std::min(16, std::max(1, row_tiles / 2));
+    p->row_parts = static_cast<int>(std::min<int64_t>((303 + items2) / items2, most));
+    p->rows_per_part = ceil_div(row_tiles, p->row_parts) * 128;
+    p->row_parts = ceil_div(p->rows_pad, p->rows_per_part);
+    p->stats_bytes = static_cast<size_t>(heads) * p->splits * (f32 ? 1 : 2) * p->rows_pad *
+                     sizeof(float2);
+    p->lse_bytes = f32 ? 0 : static_cast<size_t>(heads) * p->rows_pad * sizeof(float);
+    p->bytes = p->stats_bytes + p->lse_bytes +
+               (p->row_parts > 1 ? static_cast<size_t>(heads) * p->row_parts *
+                                       static_cast<size_t>(max_context) * sizeof(float)
+                                 : 0);
     return true;
 }
 
@@ -1254,6 +1265,11 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     a.weights = weights;
     a.stats = static_cast<float2*>(workspace);
     a.neg_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes +
+                                       plan.lse_bytes);
+    a.row_parts = plan.row_parts;
+    a.rows_per_part = plan.rows_per_part;
+    a.group_shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
     a.status = status;
     a.num_blocks = pool->num_blocks;
     a.weights_stride = weights_stride;

@@ -8,7 +8,10 @@
 //   pass 1  per 64-row query tile, online (max, sum) of each row over its keys,
 //   pass 2  per 64-key tile, the column sums over all the query tiles that see it.
 // Each pass reads only Q and K.  A key tile of a request and kv head belongs to one CTA,
-// which walks its query tiles in order: no atomics, and the same bits every time.
+// which walks its query tiles in order; where there are too few key tiles for the SMs, to one
+// CTA per part of its rows, and a last launch adds the parts in order (one fp32 request with
+// 8 heads on 1 kv head, 1 to 2k keys and 0.5k tokens: 219 us without the parts).  No atomics,
+// and the same bits every time.
 //
 // This is the CUDA-core form, for fp32 pools (the tensor cores would round the operands to
 // tf32; bf16 pools have a tensor-core form in prefill_weights_tc.cu): a 64 x 64 tile of
@@ -224,7 +227,7 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
     }
 }
 
-// Pass 2.  Grid (key tile, kv head, request).
+// Pass 2.  Grid (key tile x row parts, kv head, request).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 column_sums_kernel(const PrefillWeightsArgs a, const int group) {
@@ -234,7 +237,8 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     griddep_launch_dependents();
     const int kvh = blockIdx.y, req = blockIdx.z;
     const Request rq = request_of(a, req, group, false);
-    const int key0 = blockIdx.x * kTile;
+    const int part = blockIdx.x % a.row_parts;
+    const int key0 = blockIdx.x / a.row_parts * kTile;
     const int keys = rq.c + rq.n;
     if (rq.rows == 0 || key0 >= keys) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -244,9 +248,11 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     const int base = rq.c + rq.n - rq.m;   // last key of the window's first token
     const int first = max(0, key0 - base) * group;   // earlier rows see no key of the tile
-    const int start = first / kTile * kTile;
-    if (start < rq.rows) f.rows(a, rq, group, kvh, start);
-    for (int row0 = start; row0 < rq.rows; row0 += kTile) {
+    const int start = max(first / kTile * kTile, part * a.rows_per_part);
+    const int stop = min(rq.rows, (part + 1) * a.rows_per_part);
+    if (start >= stop) return;   // nothing of the part sees the tile
+    f.rows(a, rq, group, kvh, start);
+    for (int row0 = start; row0 < stop; row0 += kTile) {
         f.put(sm.q);
         if (threadIdx.x < kTile) {   // merge the splits' statistics of the tile's rows
             float M = -INFINITY, l = 0.f;
@@ -264,7 +270,7 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
             sm.red[1][threadIdx.x][0] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         }
         __syncthreads();
-        if (row0 + kTile < rq.rows) f.rows(a, rq, group, kvh, row0 + kTile);
+        if (row0 + kTile < stop) f.rows(a, rq, group, kvh, row0 + kTile);
         float s[4][4];
         scores<D>(sm, a.scale_log2, s);
 #pragma unroll
@@ -287,11 +293,39 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
         if (key < keys) {
             float t = 0.f;
             for (int y = 0; y < 16; ++y) t += sm.red[0][threadIdx.x][y];
-            float* w = a.weights + (static_cast<size_t>(rq.wrow) * a.num_kv_heads + kvh) *
-                                       static_cast<size_t>(a.weights_stride) + key;
-            *w = a.decay != 0.f ? fmaf(a.decay, *w, t) : t;
+            if (a.row_parts > 1) {
+                a.parts[((static_cast<size_t>(req) * a.num_kv_heads + kvh) * a.row_parts + part) *
+                            a.max_context + key] = t;
+            } else {
+                float* w = a.weights + (static_cast<size_t>(rq.wrow) * a.num_kv_heads + kvh) *
+                                           static_cast<size_t>(a.weights_stride) + key;
+                *w = a.decay != 0.f ? fmaf(a.decay, *w, t) : t;
+            }
         }
     }
+}
+
+// Grid (256 keys, kv head, request).
+__global__ void __launch_bounds__(256)
+add_parts_kernel(const PrefillWeightsArgs a, const int key_unit, const int row_unit) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int req = blockIdx.z, kvh = blockIdx.y;
+    const Request rq = request_of(a, req, 1 << a.group_shift, false);
+    const int key = blockIdx.x * 256 + threadIdx.x;
+    if (rq.rows == 0 || key >= rq.c + rq.n) return;
+    // first row of the key's pass-2 item
+    const int base = rq.c + rq.n - rq.m;
+    const int first = (max(0, key / key_unit * key_unit - base) << a.group_shift) / row_unit *
+                      row_unit;
+    const float* s = a.parts + (static_cast<size_t>(req) * a.num_kv_heads + kvh) * a.row_parts *
+                                   a.max_context + key;
+    float t = 0.f;
+    for (int p = 0; p < a.row_parts && p * a.rows_per_part < rq.rows; ++p)
+        if ((p + 1) * a.rows_per_part > first) t += s[static_cast<size_t>(p) * a.max_context];
+    float* w = a.weights + (static_cast<size_t>(rq.wrow) * a.num_kv_heads + kvh) *
+                               static_cast<size_t>(a.weights_stride) + key;
+    *w = a.decay != 0.f ? fmaf(a.decay, *w, t) : t;
 }
 
 template <int D>
@@ -308,11 +342,22 @@ cudaError_t launch_typed(const PrefillWeightsArgs& a, int group, cudaStream_t st
                    dim3(static_cast<unsigned>(row_tiles * a.splits), a.num_kv_heads, a.num_reqs),
                    dim3(kThreads), smem, stream, a, group);
     if (e != cudaSuccess) return e;
-    return launch_pdl(column_sums_kernel<D>, dim3(key_tiles, a.num_kv_heads, a.num_reqs),
-                      dim3(kThreads), smem, stream, a, group);
+    if (static_cast<int64_t>(key_tiles) * a.row_parts > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_pdl(column_sums_kernel<D>,
+                   dim3(key_tiles * a.row_parts, a.num_kv_heads, a.num_reqs), dim3(kThreads), smem,
+                   stream, a, group);
+    if (e != cudaSuccess || a.row_parts == 1) return e;
+    return launch_add_parts(a, kTile, kTile, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_add_parts(const PrefillWeightsArgs& a, int key_unit, int row_unit,
+                             cudaStream_t stream) {
+    return launch_pdl(add_parts_kernel,
+                      dim3((a.max_context + 255) / 256, a.num_kv_heads, a.num_reqs), dim3(256), 0,
+                      stream, a, key_unit, row_unit);
+}
 
 cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int head_dim, int group,
                                    cudaStream_t stream) {

@@ -137,7 +137,8 @@ PKV_DEVINL Request request_of(const PrefillWeightsArgs& a, int r, bool report) {
 
 PKV_DEVINL int ceil_div(int x, int y) { return (x + y - 1) / y; }
 
-// One item: A tiles a0, a0 + 1 (na of them) against B tiles [b0, b0 + nb).
+// One item: A tiles a0, a0 + 1 (na of them) against B tiles [b0, b0 + nb), which are those of
+// one chunk of keys (pass 1) or of one part of the rows (pass 2).
 struct Item {
     int r, kvh, chunk, a0, na, b0, nb;
     int base;   // last key that the window's first token sees
@@ -176,13 +177,15 @@ struct Walk {
             } else {
                 const int tiles = ceil_div(keys, kTile), pairs = (tiles + 1) / 2;
                 it.a0 = 2 * (rem % pairs);
-                it.kvh = rem / pairs;
-                it.chunk = 0;
+                rem /= pairs;
+                it.chunk = rem % a.row_parts;
+                it.kvh = rem / a.row_parts;
                 it.na = min(2, tiles - it.a0);
-                // rows from the first that sees the item's first key
+                // rows from the first that sees the item's first key, of the item's part
                 const int first = max(0, it.a0 * kTile - it.base) << a.group_shift;
-                it.b0 = first / kTile;
-                it.nb = ceil_div(it.q.rows, kTile) - it.b0;
+                const int part = a.rows_per_part / kTile;
+                it.b0 = max(first / kTile, it.chunk * part);
+                it.nb = min(ceil_div(it.q.rows, kTile), (it.chunk + 1) * part) - it.b0;
             }
             if (it.nb > 0) {
                 k += gridDim.x;
@@ -298,7 +301,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const int key_tiles = ceil_div(q.c + q.n, kTile);
                     n = PASS == 1 ? (ceil_div(q.rows, kTile) + 1) / 2 *
                                         ceil_div(key_tiles, a.chunk_tiles)
-                                  : (key_tiles + 1) / 2;
+                                  : (key_tiles + 1) / 2 * a.row_parts;
                     n *= a.num_kv_heads;
                 }
             }
@@ -560,9 +563,14 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                 const int from = max(0, key - it.base) << a.group_shift;
                 const int from_last = max(0, last - it.base) << a.group_shift;
                 const bool there = mine && half == 0 && key < it.q.c + it.q.n;
-                float* w = a.weights + (static_cast<size_t>(it.q.wrow) * a.num_kv_heads + it.kvh) *
-                                           static_cast<size_t>(a.weights_stride) + key;
-                const float before = there && a.decay != 0.f ? *w : 0.f;
+                // added to the weights, or kept for the launch that adds the parts up
+                const bool whole_sum = a.row_parts == 1;
+                float* w = whole_sum
+                               ? a.weights + (static_cast<size_t>(it.q.wrow) * a.num_kv_heads +
+                                              it.kvh) * static_cast<size_t>(a.weights_stride) + key
+                               : a.parts + (head * a.row_parts + it.chunk) * a.max_context + key;
+                const float decay = whole_sum ? a.decay : 0.f;
+                const float before = there && decay != 0.f ? *w : 0.f;
                 float acc[8], total = 0.f;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) acc[u] = 0.f;
@@ -644,7 +652,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                     __syncwarp();
                     mbar_arrive_if(lane == 0, &bars[GM::L_EMPTY + sl]);
                 }
-                if (ok && there) *w = a.decay != 0.f ? fmaf(a.decay, before, total) : total;
+                if (ok && there) *w = decay != 0.f ? fmaf(decay, before, total) : total;
             }
         }
     }
@@ -705,9 +713,8 @@ int sm_count() {
 }
 
 template <int D>
-cudaError_t launch_d(PrefillWeightsArgs a, int group, cudaStream_t stream) {
+cudaError_t launch_d(const PrefillWeightsArgs& a, int group, cudaStream_t stream) {
     using GM = Geom<D>;
-    a.group_shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
     CUtensorMap mq, mk;
     const int64_t rows = (a.num_blocks * a.num_kv_heads) << a.block_shift;
     const bool ok = D == 128 ? make_pool_block_map(&mk, a.k_pool, rows)
@@ -738,7 +745,7 @@ cudaError_t launch_d(PrefillWeightsArgs a, int group, cudaStream_t stream) {
         }
         const int64_t heads = static_cast<int64_t>(g.num_reqs) * a.num_kv_heads;
         const int64_t items1 = heads * ((row_tiles + 1) / 2) * a.splits;
-        const int64_t items2 = heads * key_pairs;
+        const int64_t items2 = heads * key_pairs * a.row_parts;
         if (items1 > INT32_MAX || items2 > INT32_MAX) return cudaErrorNotSupported;
         const int sms = sm_count();
         e = launch_pdl(pass1, dim3(static_cast<unsigned>(items1 < sms ? items1 : sms)),
@@ -751,6 +758,10 @@ cudaError_t launch_d(PrefillWeightsArgs a, int group, cudaStream_t stream) {
         e = launch_pdl(pass2, dim3(static_cast<unsigned>(items2 < sms ? items2 : sms)),
                        dim3(kThreads), GM::kBytes, stream, mq, mk, g);
         if (e != cudaSuccess) return e;
+        if (a.row_parts > 1) {
+            e = launch_add_parts(g, 2 * kTile, kTile, stream);
+            if (e != cudaSuccess) return e;
+        }
     }
     return cudaSuccess;
 }

@@ -62,7 +62,7 @@ def attention(q, k, v, scale, first=0):
     x.masked_fill_(future[None, None], -math.inf)
     p = torch.softmax(x, -1)
     out = None if v is None else torch.einsum("hgmn,nhd->mhgd", p, v).reshape(m, hq, d)
-    size = torch.einsum("mhgd,nhd->hgmn", qg.abs(), k.abs()).max() * scale if n else 0.0
+    size = torch.einsum("mhgd,nhd->hgmn", qg.abs(), k.abs()).max() * scale if n and m else 0.0
     return out, p.sum((1, 2)), float(size)
 
 
