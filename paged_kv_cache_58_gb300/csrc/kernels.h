@@ -85,9 +85,9 @@ struct DecodeArgs {
     const void* v_new;
     // Accumulated attention weights (pkv_paged_decode_weights): non-null `scores` makes
     // the split kernels keep every score, scale * log2(e) * q.k, in
-    // scores[S][Hkv][score_tokens][G] and every partition's m / l (also where there is
-    // one partition), from which the finishing launch adds each cached token's weight to
-    // weights[row][kvh][token].
+    // scores[S][Hkv][score_tokens][G].  From them and the partitions' m / l the finishing
+    // launch adds each cached token's weight to weights[row][kvh][token]; where there is one
+    // partition, its CTA does so itself and no second launch follows.
     float* scores;
     int score_tokens;         // tokens per (sequence, kv head) in `scores`
     float* weights;

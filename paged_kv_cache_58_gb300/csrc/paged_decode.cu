@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "decode_weights.cuh"
 #include "kernels.h"
 
 namespace pkv {
@@ -412,10 +413,6 @@ decode_split_kernel(const DecodeArgs a) {
         const size_t row = qrow * hq + h;
         if (nparts == 1) {
             store_elem<T>(static_cast<T*>(a.out) + row * D + d, o / l);
-            if (W && d == 0) {
-                a.m_part[row] = M;
-                a.l_part[row] = l;
-            }
         } else {
             const size_t pr = row * nparts + a.extra_parts + part;
             a.o_part[pr * D + d] = o / l;
@@ -423,6 +420,21 @@ decode_split_kernel(const DecodeArgs a) {
                 a.m_part[pr] = M;
                 a.l_part[pr] = l;
             }
+        }
+    }
+    if constexpr (W) {
+        if (nparts == 1) {   // every score of the (sequence, kv head) is this CTA's
+            float(*coef)[G] = reinterpret_cast<float(*)[G]>(smem);   // the ring is idle
+            if (threadIdx.x < G) {
+                float M = -INFINITY, l = 0.f;
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * G + threadIdx.x]);
+                for (int w = 0; w < kWarps; ++w)
+                    l = fmaf(fast_exp2(mm[w * G + threadIdx.x] - M), ml[w * G + threadIdx.x], l);
+                coef[0][threadIdx.x] = M;
+                coef[1][threadIdx.x] = 1.f / l;
+            }
+            __syncthreads();
+            add_own_weights<G>(a, seq, kvh, L, coef);
         }
     }
 }
@@ -534,23 +546,6 @@ decode_combine_kernel(const DecodeArgs a) {
 // streaming kernel: the scores of the next tile are loaded while one is worked on.
 constexpr int kWeightTile = 512;
 
-// The G scores of a token, in the widest loads their alignment (4 G bytes) allows.
-template <int G>
-PKV_DEVINL void load_scores(const float* p, float (&s)[G]) {
-    if constexpr (G == 1) {
-        s[0] = *p;
-    } else if constexpr (G == 2) {
-        const float2 f = *reinterpret_cast<const float2*>(p);
-        s[0] = f.x; s[1] = f.y;
-    } else {
-#pragma unroll
-        for (int g = 0; g < G; g += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(p + g);
-            s[g] = f.x; s[g + 1] = f.y; s[g + 2] = f.z; s[g + 3] = f.w;
-        }
-    }
-}
-
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCombineWarps * 32)
 decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs, const int run) {
@@ -640,9 +635,7 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
         for (int u = 0; u < PER; ++u) {
             const int j = j0 + u * kThr;
             if (j >= end) continue;
-            float p = 0.f;
-#pragma unroll
-            for (int g = 0; g < G; ++g) p = fmaf(fast_exp2(s[u][g] - coef[0][g]), coef[1][g], p);
+            const float p = step_weight<G>(s[u], coef);
             wp[j] = a.decay != 0.f ? fmaf(a.decay, w[u], p) : p;
         }
         if (!more) break;
@@ -667,7 +660,7 @@ cudaError_t launch_typed(const DecodeArgs& a, cudaStream_t stream) {
         e = launch_maybe_pdl(!a.no_pdl, kern, grid, dim3(kThreads), SM::kTotal, stream, a);
         if (e != cudaSuccess) return e;
     }
-    if constexpr (W)
+    if (W && a.max_parts > 1)
         return launch_decode_finish(a, sizeof(T) == 2 ? PKV_BF16 : PKV_F32, D, G, stream);
     if (a.extra_parts == 0 && a.max_parts == 1) return e;  // output written directly
     if (a.defer_combine) return e;
@@ -685,8 +678,7 @@ cudaError_t launch_combine_typed(const DecodeArgs& a, cudaStream_t stream) {
 template <typename T, int D, int G>
 cudaError_t launch_finish_typed(const DecodeArgs& a, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
-    // one partition: the split kernel has written the output, no merge is left
-    const int64_t combine = a.max_parts > 1 ? (rows + kCombineWarps - 1) / kCombineWarps : 0;
+    const int64_t combine = (rows + kCombineWarps - 1) / kCombineWarps;
     // Runs of 8 tiles, shorter while there would be fewer than 6 CTAs per SM.
     const int tiles = (a.score_tokens + kWeightTile - 1) / kWeightTile;
     const int64_t heads = static_cast<int64_t>(a.num_kv_heads) * a.num_seqs;

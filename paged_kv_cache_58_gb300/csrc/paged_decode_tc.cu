@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "decode_weights.cuh"
 #include "kernels.h"
 
 namespace pkv {
@@ -90,15 +91,18 @@ struct TcSmem {
     static constexpr int kStageBytes = 2 * kSlab;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     // merge scratch reuses the ring once every warp is done
-    static constexpr int kMerge = kWarps * G * D * 4 + 2 * kWarps * G * 4;
+    static constexpr int kMerge = kWarps * G * D * 4 + (2 * kWarps + 2) * G * 4;
     static_assert(kMerge <= kRing, "merge scratch must fit in the ring");
     static constexpr int kBars = kWarps * kStages * 8;
     static constexpr int kTotal = kRing + kBars + 1024;   // + alignment slack
 };
 
-// W: keep the scores and the partitions' m / l for the accumulated attention weights.
+// W: keep the scores and the partitions' m / l for the accumulated attention weights.  As many
+// CTAs share an SM as their stages leave room for, three at head_dim 128 and six at 64; said
+// so, the compiler gives the W form the registers that the other takes by itself (64
+// sequences, 512 to 4096 tokens, head_dim 128: 109.5 -> 107.5 us).
 template <int D, int G, bool W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, W ? (D == 128 ? 3 : 6) : 0)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const DecodeArgs a) {
     using SM = TcSmem<D, G>;
@@ -431,10 +435,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (nparts == 1) {
             static_cast<uint16_t*>(a.out)[row * D + d] =
                 static_cast<uint16_t>(pack_bf16x2(o / l, 0.f) & 0xffffu);
-            if (W && d == 0) {
-                a.m_part[row] = M;
-                a.l_part[row] = l;
-            }
         } else {
             const size_t pr = row * nparts + a.extra_parts + part;
             a.o_part[pr * D + d] = o / l;
@@ -442,6 +442,21 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 a.m_part[pr] = M;
                 a.l_part[pr] = l;
             }
+        }
+    }
+    if constexpr (W) {
+        if (nparts == 1) {   // every score of the (sequence, kv head) is this CTA's
+            float(*coef)[G] = reinterpret_cast<float(*)[G]>(ml + kWarps * G);
+            if (threadIdx.x < G) {
+                float M = -INFINITY, l = 0.f;
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * G + threadIdx.x]);
+                for (int w = 0; w < kWarps; ++w)
+                    l = fmaf(fast_exp2(mm[w * G + threadIdx.x] - M), ml[w * G + threadIdx.x], l);
+                coef[0][threadIdx.x] = M;
+                coef[1][threadIdx.x] = 1.f / l;
+            }
+            __syncthreads();
+            add_own_weights<G>(a, seq, kvh, L, coef);
         }
     }
 }
@@ -466,7 +481,7 @@ cudaError_t launch_tc(const DecodeArgs& a, cudaStream_t stream) {
                              a);
         if (e != cudaSuccess) return e;
     }
-    if constexpr (W) return launch_decode_finish(a, PKV_BF16, D, G, stream);
+    if (W && a.max_parts > 1) return launch_decode_finish(a, PKV_BF16, D, G, stream);
     if (a.extra_parts == 0 && a.max_parts == 1) return e;  // output written directly
     if (a.defer_combine) return e;
     return launch_decode_combine(a, PKV_BF16, D, stream);

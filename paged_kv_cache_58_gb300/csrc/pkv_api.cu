@@ -294,8 +294,8 @@ int weights_partition(int partition_blocks, int max_context, int block_size) {
 
 size_t round16(size_t x) { return (x + 15) / 16 * 16; }
 
-// Workspace of a decode with accumulated weights: the partials' outputs (none for one
-// partition), their m and l, and every score of the partitions' span.
+// Workspace of a decode with accumulated weights: the partials' outputs, m and l (none for
+// one partition), and every score of the partitions' span.
 struct WeightsWorkspace {
     size_t ml_at, scores_at, bytes;
     int score_tokens;
@@ -307,7 +307,7 @@ bool weights_workspace(int num_seqs, int num_q_heads, int head_dim, int max_part
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
     w->score_tokens = static_cast<int>(span);
     w->ml_at = max_parts > 1 ? rows * max_parts * head_dim * sizeof(float) : 0;
-    w->scores_at = w->ml_at + 2 * round16(rows * max_parts * sizeof(float));
+    w->scores_at = w->ml_at + (max_parts > 1 ? 2 * round16(rows * max_parts * sizeof(float)) : 0);
     w->bytes = w->scores_at + rows * static_cast<size_t>(span) * sizeof(float);
     return true;
 }
@@ -1175,11 +1175,12 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
     const int tiles = ceil_div(max_context, 128);
     const int row_tiles = p->rows_pad / 128;
     if (f32) {
-        // CUDA cores: 64-row by 64-key tiles; parts of the keys until there are two CTAs per SM.
+        // CUDA cores: 64-row by 64-key tiles; parts of the keys up to two CTAs per SM, which is
+        // what fits (a few more would be a second wave).
         const int64_t ctas = heads * (p->rows_pad / 64);
         p->chunk_tiles = 0;
         p->splits = static_cast<int>(std::min<int64_t>(
-            std::min<int64_t>((2 * 152 + ctas - 1) / ctas, ceil_div(max_context, 64)), 32));
+            std::min<int64_t>(std::max<int64_t>(304 / ctas, 1), ceil_div(max_context, 64)), 32));
     } else {
         // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 582 us for the
         // call, 594 with 16, 609 with 8, where the parts' own first tiles and statistics
@@ -1191,10 +1192,10 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
         p->chunk_tiles = std::max(p->chunk_tiles, ceil_div(tiles, 32));
         p->splits = ceil_div(tiles, p->chunk_tiles);
     }
-    // Pass 2: parts of the rows, of two tiles of 128 at least, until there are two items per SM.
+    // Pass 2: parts of the rows, of two tiles of 128 at least, up to two items per SM.
     const int64_t items2 = heads * (f32 ? ceil_div(max_context, 64) : (tiles + 1) / 2);
     const int most = std::min(16, std::max(1, row_tiles / 2));
-    p->row_parts = static_cast<int>(std::min<int64_t>((303 + items2) / items2, most));
+    p->row_parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>(304 / items2, 1), most));
     p->rows_per_part = ceil_div(row_tiles, p->row_parts) * 128;
     p->row_parts = ceil_div(p->rows_pad, p->rows_per_part);
     p->stats_bytes = static_cast<size_t>(heads) * p->splits * (f32 ? 1 : 2) * p->rows_pad *

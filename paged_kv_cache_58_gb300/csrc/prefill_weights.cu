@@ -121,10 +121,15 @@ struct Fetch {
     }
 };
 
+// The thread's place in the 16 x 16 grid: a warp covers 4 rows by 8 keys, so that each of its
+// 16-byte shared-memory reads is one pass (2 by 16 took two for the keys).
+PKV_DEVINL int thread_x() { return (threadIdx.x & 7) + ((threadIdx.x >> 5) & 1) * 8; }
+PKV_DEVINL int thread_y() { return ((threadIdx.x >> 3) & 3) + (threadIdx.x >> 6) * 4; }
+
 // s[i][j] = q row (ty + 16 i) . k row (tx + 16 j), scaled; 4 x 4 per thread.
 template <int D>
 PKV_DEVINL void scores(const Smem<D>& sm, float scale, float (&s)[4][4]) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = thread_x(), ty = thread_y();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -166,7 +171,7 @@ row_stats_kernel(const PrefillWeightsArgs a, const int group) {
     const Request rq = request_of(a, req, group, threadIdx.x == 0 && blockIdx.x == 0);
     const int row0 = tile * kTile;
     if (row0 >= rq.rows) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = thread_x(), ty = thread_y();
     // keys any row of the tile sees
     const int last = rq.c + rq.n - rq.m + (min(row0 + kTile, rq.rows) - 1) / group;
     const int key_tiles = last / kTile + 1;
@@ -241,7 +246,7 @@ column_sums_kernel(const PrefillWeightsArgs a, const int group) {
     const int key0 = blockIdx.x / a.row_parts * kTile;
     const int keys = rq.c + rq.n;
     if (rq.rows == 0 || key0 >= keys) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = thread_x(), ty = thread_y();
     Fetch<D> f;
     f.keys(a, req, kvh, key0, keys);
     f.put(sm.k);
