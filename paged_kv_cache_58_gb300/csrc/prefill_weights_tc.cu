@@ -25,7 +25,8 @@
 // us (425 us without exponentials: a tile's product and its exponentials take turns); equal
 // contiguous stretches of A tiles per CTA instead of every n-th item: 620 us.
 //
-// Pass 1 keeps the maximum of a row's first tile of the item as its reference and adds
+// Pass 1 keeps the maximum of a row's first tile of the item (the first with a score above
+// -inf) as its reference and adds
 // 2^(s - m) from there on without looking for a larger one: there is no accumulator to
 // keep in range, only a sum in fp32, whose relative precision does not depend on the
 // reference.  Only a sum past 2^96 (later scores beyond the first tile's maximum by that
@@ -533,9 +534,11 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                         }
                         return sum8(t);
                     };
-                    if (j == 0) {   // a tile of which the row sees nothing leaves any reference
-                        m = tile_max();
-                        if (m == -INFINITY) m = 0.f;
+                    if (j == 0 || __any_sync(0xffffffffu, l == 0.f)) {
+                        // no reference yet; a tile of which the row sees nothing, or -inf
+                        // scores alone, leaves any
+                        const float mt = tile_max();
+                        if (l == 0.f) m = mt == -INFINITY ? 0.f : mt;
                     }
                     const float t = tile_sum(m);
                     if (__any_sync(0xffffffffu, l + t > kSumLimit)) {

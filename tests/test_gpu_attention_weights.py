@@ -319,6 +319,39 @@ def test_prefill_weights_growing_scores(pkv, dtype):
     assert bool((err <= p * 2.0 ** -12 + 160 * 2.0 ** -120).all()), (err / p.clamp(min=1e-30)).max()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_prefill_weights_infinite_keys(pkv, dtype):
+    """Keys whose score is -inf, more of them than a row's first tiles hold, before keys whose
+    scores are far below zero: a softmax over the latter alone."""
+    n, d = 700, 64
+    g = gen(37)
+    kp, _, table = paged([n], 1, 16, d, dtype, g)
+    ids = table[0, :44].long()
+    flat = kp[ids].transpose(1, 2).reshape(-1, d).clone()
+    flat[:n] = 0
+    j = torch.arange(n, device="cuda")
+    flat[:n, 0] = torch.where(j < 300, float("-inf"), -500.0 - (j % 4)).to(dtype)
+    kp[ids] = flat.view(44, 16, 1, d).transpose(1, 2)
+    q = torch.zeros(40, 2, d, device="cuda", dtype=dtype)
+    q[..., 0] = torch.tensor([1.0, 0.5], device="cuda").to(dtype)
+    q[..., 1] = 1.0
+    w = torch.zeros(1, 1, n, device="cuda")
+    pkv.paged_prefill_weights(q, kp, table, i32([n - 40]), i32([40]), i32([0, 40]), 1.0, w,
+                              max_new=40, max_context=n)
+    assert pkv.read_device_status() == 0
+    x = kp.cpu()[ids.cpu()].transpose(1, 2).reshape(-1, d)[:n, 0].double()
+    want = torch.zeros(n, dtype=torch.float64)
+    for i in range(40):
+        for f in (1.0, 0.5):
+            want[:n - 39 + i] += torch.softmax(x[:n - 39 + i] * f, 0)
+    got = w[0, 0].cpu().double()
+    assert bool((got[:300] == 0).all())
+    # scores are whole or half numbers below 2^9, exact; times log2(e) and less the row's statistic
+    # they round by 2^-24 of 2^10 thrice at most: below 2^-12 of a weight; the exponentials and sums
+    # of 80 + 700 terms stay below 2^-13
+    assert bool(((got - want).abs() <= want * 2.0 ** -11).all()), ((got - want).abs() / want).max()
+
+
 @pytest.mark.parametrize("rows", [False, True])
 def test_prefill_weights_many_requests(pkv, rows):
     """More requests than one round of launches takes: 300 short ones, odd lengths."""
