@@ -921,7 +921,7 @@ class BlockAllocator:
     def privatize(self, seq_id: int, num_tokens: int):
         """Private copies of the blocks of the first num_tokens tokens that others reference;
         returns the (old, new) pairs for copy_blocks."""
-        most = max(-(-num_tokens // self.block_size), 0)
+        most = min(max(-(-num_tokens // self.block_size), 0), self.num_blocks)
         pairs = (ctypes.c_int32 * max(2 * most, 1))()
         n = ctypes.c_int(0)
         _check("pkv_alloc_privatize", self._lib.pkv_alloc_privatize(self._h, seq_id, num_tokens,

@@ -139,6 +139,20 @@ def test_privatize_and_truncate_refusals(pkv):
     assert torch.equal(a.block_table([1, 2], 4), before) and a.num_free == 2
 
 
+def test_privatize_of_absurd_lengths(pkv):
+    """Lengths no sequence has are refused without room being made for their pairs."""
+    a = pkv.BlockAllocator(6, 16)
+    a.add_seq(1, 64)
+    for n in (2 ** 40, 2 ** 62):
+        with pytest.raises(pkv.PkvError) as e:
+            a.privatize(1, n)
+        assert e.value.status == INVALID
+    a.fork(1, 2)
+    a.truncate(1, 16)
+    assert len(a.privatize(2, 64)) == 1   # what the other still holds
+    assert a.num_free == 1
+
+
 def test_truncate_and_privatize_respect_the_prefix_cache(pkv):
     """Blocks that a prefix cache holds are shared: an eviction copies them first, and a
     truncation leaves them cached."""
