@@ -555,9 +555,11 @@ cudaError_t launch_f(const EvictArgs& a, int C, cudaStream_t stream) {
     auto kern = evict_kernel<F>;
     const int words = ((a.max_context + C - 1) / C + 31) / 32;
     const int smem = static_cast<int>(sizeof(Shared)) + 3 * 4 * words;
-    static_assert(sizeof(Shared) + 3 * 4 * (kEvictMaxContext / kMaxCluster / 32) <= 232448,
-                  "the bits of the longest slice fit");
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
+    // allowed for the longest slice at once: host threads that raised the limit to what each
+    // needs could lower it for one another
+    constexpr int kMost = sizeof(Shared) + 3 * 4 * (kEvictMaxContext / kMaxCluster / 32);
+    static_assert(kMost <= 232448, "the bits of the longest slice fit");
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), kMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_kv_heads * C, a.num_seqs);
@@ -579,8 +581,13 @@ cudaError_t launch_f(const EvictArgs& a, int C, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-    // CTAs per row: enough that a slice has at most 16384 entries, and that about two CTAs per
-    // SM exist where there are few rows.
+    // CTAs per row: enough that a slice has at most 16384 entries (128 rows of 16k to 128k: 256
+    // us, 269 with slices of 32768, before the scans counted as they do now), and that about two CTAs per SM exist where there are few
+    // rows.  More where rows fill the SMs only adds cluster barriers (512 rows with two each: a
+    // block of 64 took 39 us against 15.6, 512 to 4096 entries 76 against 72).
+    // Entries in flight per thread: four in a CTA that has its row alone (eight: 16.3 and 73.2 us
+    // against 15.6 and 72.3), eight where clusters scan long rows (four 243.5 us, sixteen 258,
+    // against 241).
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
     int C = 1;
     while (C < kMaxCluster &&
