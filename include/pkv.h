@@ -485,7 +485,8 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
  *   tracked_lens  device int32 [num_seqs], new_lens of the sequence's last pkv_evict, 0 before
  *                 the first; NULL: zeros.
  *   weights_out, positions_out  where the shrunk rows go: the inputs themselves (in place) or
- *                 buffers that do not overlap them.  Weights from new_lens[s] to L become 0;
+ *                 buffers that do not overlap them.  Weights from new_lens[s] to L become 0
+ *                 and those from L on are not written (a separate buffer starts zeroed);
  *                 positions_out holds new_lens[s] entries per head, the rest is not written.
  *   new_lens      device int32 [num_seqs], written; must not overlap an input array.
  *   row_ids       as above; a negative one leaves the sequence as it is (new_lens = L).

@@ -122,7 +122,7 @@ struct Fetch {
 };
 
 // The thread's place in the 16 x 16 grid: a warp covers 4 rows by 8 keys, so that each of its
-// 16-byte shared-memory reads is one pass (2 by 16 took two for the keys).
+// 16-byte shared-memory reads is one pass (2 by 16 needs two for the keys; the times were alike).
 PKV_DEVINL int thread_x() { return (threadIdx.x & 7) + ((threadIdx.x >> 5) & 1) * 8; }
 PKV_DEVINL int thread_y() { return ((threadIdx.x >> 3) & 3) + (threadIdx.x >> 6) * 4; }
 

@@ -237,8 +237,10 @@ cudaError_t launch_tt(const RopeArgs& a, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_d(const RopeArgs& a, cudaStream_t stream) {
-    // Few tokens: one per CTA, so that as many SMs as there are tokens work; many: four,
-    // so that each angle serves as many rows and the angles of a CTA fill its threads.
+    // Few tokens: one per CTA, so that as many SMs as there are tokens work; many: four, so
+    // that the angles of a CTA fill its threads and a thread has more rows to walk.  At 64 tokens
+    // of 48 rows one takes 2.4 us; at 8192 of them (three rows in flight) one took 42.8 us, two
+    // 37.6 and four 39.1; at 4097 fp32 tokens of 16 rows 12.3, 8.4 and 7.35 us.
     return a.num_tokens >= 2048 ? launch_tt<T, D, 4>(a, stream) : launch_tt<T, D, 1>(a, stream);
 }
 
