@@ -453,7 +453,10 @@ pkv_status pkv_paged_decode_weights(const pkv_pool_desc* pool, void* out, const 
  * [0, total_new)) raises PKV_ERR_OOB in the device status word and is skipped, as is a block
  * id outside the pool (that request's weights are then not valid).
  *   max_context  host upper bound of cached + new, at most max_blocks_per_seq * block_size.
- *   workspace    16-byte aligned, clobbered.  Other arguments as pkv_paged_prefill. */
+ *   workspace    16-byte aligned, clobbered.  (fp32 pools: it holds scores, up to 256 MB of
+ *                them, or one (request, kv head)'s up to 1 GB; they go by the bounds max_new,
+ *                window and max_context, not by the lengths.)  Other arguments as
+ *                pkv_paged_prefill. */
 size_t pkv_paged_prefill_weights_workspace_bytes(const pkv_pool_desc* pool, int num_reqs,
                                                  int num_q_heads, int max_new, int max_context,
                                                  int window);

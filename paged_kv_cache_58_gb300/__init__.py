@@ -775,7 +775,8 @@ def paged_decode_weights(q, k_pool, v_pool, block_tables, context_lens, scale, w
 
 def prefill_weights_workspace_bytes(k_pool, num_reqs, num_q_heads, max_new, max_context,
                                     window=0) -> int:
-    """Workspace of paged_prefill_weights (the query rows' softmax statistics)."""
+    """Workspace of paged_prefill_weights (the query rows' softmax statistics; for fp32 pools
+    also scores, up to 256 MB, or 1 GB where one kv head of a request alone has that many)."""
     return int(_load().pkv_paged_prefill_weights_workspace_bytes(
         ctypes.byref(pool_desc(k_pool)), num_reqs, num_q_heads, max_new, max_context, window))
 

@@ -251,6 +251,11 @@ struct PrefillWeightsArgs {
     int row_parts;
     int rows_per_part;
     float* parts;
+    // fp32: a launch takes heads_per_launch (request, kv head) pairs; pass 1 keeps their scores,
+    // [heads_per_launch][rows_pad][key_pad], for pass 2, or, null, pass 2 computes them again.
+    float* scores;
+    int64_t key_pad;
+    int heads_per_launch;
     float scale_log2;
     float decay;
 };

@@ -1161,9 +1161,13 @@ int window_rows(int max_new, int window) {
 
 // How pass 1 cuts the keys of a query tile, and the workspace that gives.
 struct PrefillWeightsPlan {
-    int rows_pad, splits, chunk_tiles, row_parts, rows_per_part;
-    size_t stats_bytes, lse_bytes, bytes;
+    int rows_pad, splits, chunk_tiles, row_parts, rows_per_part, heads_per_launch;
+    int64_t key_pad;
+    size_t stats_bytes, lse_bytes, score_bytes, bytes;
 };
+// What the kept scores of one launch may take (fp32): as many (request, kv head) pairs as fit
+// kScoreBytes, or one alone that fits kScoreMost.  A larger one has its scores computed twice.
+constexpr int64_t kScoreBytes = int64_t{256} << 20, kScoreMost = int64_t{1} << 30;
 bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_heads, int max_new,
                           int max_context, int window, PrefillWeightsPlan* p) {
     const int64_t rows = static_cast<int64_t>(window_rows(max_new, window)) *
@@ -1171,14 +1175,26 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
     if (rows > INT32_MAX - 128) return false;
     p->rows_pad = static_cast<int>((rows + 127) / 128 * 128);
     const int64_t heads = static_cast<int64_t>(num_reqs) * pool->num_kv_heads;
+    if (heads > INT32_MAX) return false;
+    p->heads_per_launch = static_cast<int>(heads);
+    p->key_pad = 0;
+    p->score_bytes = 0;
     const bool f32 = pool->dtype == PKV_F32;
     const int tiles = ceil_div(max_context, 128);
     const int row_tiles = p->rows_pad / 128;
     if (f32) {
         // CUDA cores: 64-row by 64-key tiles; parts of the keys up to two CTAs per SM, which is
         // what fits (a few more would be a second wave).
-        const int64_t ctas = heads * (p->rows_pad / 64);
+        const int64_t ctas = static_cast<int64_t>(p->heads_per_launch) * (p->rows_pad / 64);
         p->chunk_tiles = 0;
+        p->key_pad = (static_cast<int64_t>(max_context) + 63) / 64 * 64;
+        int64_t fit = 65535;   // a grid's second dimension
+        if (p->key_pad <= kScoreMost / 4 / p->rows_pad) {
+            const int64_t one = p->rows_pad * p->key_pad * 4;
+            fit = std::max<int64_t>(std::min(fit, kScoreBytes / one), 1);
+            p->score_bytes = static_cast<size_t>(std::min(fit, heads) * one);
+        }
+        p->heads_per_launch = static_cast<int>(std::min(fit, heads));
         p->splits = static_cast<int>(std::min<int64_t>(
             std::min<int64_t>(std::max<int64_t>(304 / ctas, 1), ceil_div(max_context, 64)), 32));
     } else {
@@ -1193,7 +1209,8 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
         p->splits = ceil_div(tiles, p->chunk_tiles);
     }
     // Pass 2: parts of the rows, of two tiles of 128 at least, up to two items per SM.
-    const int64_t items2 = heads * (f32 ? ceil_div(max_context, 64) : (tiles + 1) / 2);
+    const int64_t items2 = static_cast<int64_t>(p->heads_per_launch) *
+                           (f32 ? ceil_div(max_context, 64) : (tiles + 1) / 2);
     const int most = std::min(16, std::max(1, row_tiles / 2));
     p->row_parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>(304 / items2, 1), most));
     p->rows_per_part = ceil_div(row_tiles, p->row_parts) * 128;
@@ -1201,7 +1218,7 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
     p->stats_bytes = static_cast<size_t>(heads) * p->splits * (f32 ? 1 : 2) * p->rows_pad *
                      sizeof(float2);
     p->lse_bytes = f32 ? 0 : static_cast<size_t>(heads) * p->rows_pad * sizeof(float);
-    p->bytes = p->stats_bytes + p->lse_bytes +
+    p->bytes = p->stats_bytes + p->lse_bytes + p->score_bytes +
                (p->row_parts > 1 ? static_cast<size_t>(heads) * p->row_parts *
                                        static_cast<size_t>(max_context) * sizeof(float)
                                  : 0);
@@ -1266,8 +1283,11 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     a.weights = weights;
     a.stats = static_cast<float2*>(workspace);
     a.neg_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes);
-    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes +
-                                       plan.lse_bytes);
+    char* after = static_cast<char*>(workspace) + plan.stats_bytes + plan.lse_bytes;
+    a.scores = plan.score_bytes ? reinterpret_cast<float*>(after) : nullptr;
+    a.parts = reinterpret_cast<float*>(after + plan.score_bytes);
+    a.key_pad = plan.key_pad;
+    a.heads_per_launch = plan.heads_per_launch;
     a.row_parts = plan.row_parts;
     a.rows_per_part = plan.rows_per_part;
     a.group_shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;

@@ -319,6 +319,41 @@ def test_prefill_weights_growing_scores(pkv, dtype):
     assert bool((err <= p * 2.0 ** -12 + 160 * 2.0 ** -120).all()), (err / p.clamp(min=1e-30)).max()
 
 
+@pytest.mark.parametrize("max_new,max_context", [(1024, 4096),     # a launch per kv head
+                                                 (16384, 4096)])   # scores computed twice
+@pytest.mark.parametrize("window", [0, 50])
+def test_prefill_weights_wide_bounds(pkv, max_new, max_context, window):
+    """Bounds far above the lengths: what the call keeps goes by the bounds (fp32)."""
+    hkv, group, d, bs = 2, 8, 64, 16
+    cached, new = [70, 0, 300], [130, 9, 40]
+    total = [c + n for c, n in zip(cached, new)]
+    g = gen(43)
+    kp, _, table = paged(total, hkv, bs, d, torch.float32, g)
+    wide = torch.full((3, max_context // bs), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = torch.randn(sum(new), hkv * group, d, generator=g, device="cuda")
+    off = [0, 130, 139, 179]
+    if window:   # the window counts for the bound on rows, unless it is above it
+        max_new = 2 * max_new
+    w0 = torch.rand(3, hkv, max_context, generator=g, device="cuda")
+    w = w0.clone()
+    need = pkv.prefill_weights_workspace_bytes(kp, 3, hkv * group, max_new, max_context, window)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ws.view(torch.float32).fill_(float("nan"))   # whatever was there does not count
+    pkv.paged_prefill_weights(q, kp, wide, i32(cached), i32(new), i32(off), 0.125, w,
+                              max_new=max_new, max_context=max_context, window=window,
+                              decay=0.5, workspace=ws)
+    assert pkv.read_device_status() == 0
+    for i, n in enumerate(total):
+        m = min(new[i], window) if window else new[i]
+        k = tokens(kp.cpu(), table.cpu()[i], n)
+        _, p, size = attention(q.cpu()[off[i + 1] - m:off[i + 1]], k, None, 0.125, first=n - m)
+        before = w0[i, :, :n].cpu().double()
+        err = (w[i, :, :n].cpu().double() - (0.5 * before + p)).abs()
+        assert bool((err <= weight_bound(p, before, size, d, n + m * group)).all()), i
+        assert torch.equal(w[i, :, n:], w0[i, :, n:])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_prefill_weights_infinite_keys(pkv, dtype):
     """Keys whose score is -inf, more of them than a row's first tiles hold, before keys whose
