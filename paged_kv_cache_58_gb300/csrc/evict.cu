@@ -184,6 +184,10 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
             const int i = ib + u * NT;
             if (i - lane >= n) break;
             const bool in = i < n;
+            if (in && i0 + i < b) {   // most of these stay: step 4 overwrites the freed places
+                if (move_w) wo[i0 + i] = x[u];
+                if (move_p || i0 + i >= tracked) po[i0 + i] = p[u];
+            }
             const bool s = in && (p[u] < a.sinks || p[u] >= recent_from);
             const uint32_t ball = __ballot_sync(0xffffffffu, s);
             if (lane == 0) {
@@ -417,6 +421,17 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     uint32_t* mover_slot = reinterpret_cast<uint32_t*>(movers + most);
     float* mover_w = reinterpret_cast<float*>(mover_slot + most);
     int32_t* mover_pos = holes + 4 * static_cast<size_t>(most);
+    int room = most;
+    if (C == 1 && max(static_cast<int>(all >> 32), static_cast<int>(all & 0xffffffffu)) <= kList) {
+        // short lists of one CTA: where the threshold's bin and the histograms were
+        static_assert(kHist >= 2 * kList, "two lists in a histogram's place");
+        holes = sm.list_at;
+        movers = reinterpret_cast<int32_t*>(sm.list_key);
+        mover_slot = reinterpret_cast<uint32_t*>(sm.hist);
+        mover_w = reinterpret_cast<float*>(sm.cluster_hist);
+        mover_pos = sm.cluster_hist + kList;
+        room = kList;
+    }
     // Pool slots fit 32 bits: 2^32 rows of the least 128 bytes are more than this GPU holds.
     const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.max_blocks_per_seq;
     const uint32_t low = (1u << a.block_shift) - 1u;
@@ -434,13 +449,13 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     int h = static_cast<int>(first & 0xffffffffu), m = static_cast<int>(first >> 32);
     for (int x = w0; x < w1; ++x) {
         for (uint32_t bits = hole_mask(x); bits; bits &= bits - 1, ++h)
-            if (h < most) holes[h] = i0 + 32 * x + __ffs(bits) - 1;
+            if (h < room) holes[h] = i0 + 32 * x + __ffs(bits) - 1;
         for (uint32_t bits = mover_mask(x); bits; bits &= bits - 1, ++m)
-            if (m < most) movers[m] = i0 + 32 * x + __ffs(bits) - 1;
+            if (m < room) movers[m] = i0 + 32 * x + __ffs(bits) - 1;
     }
     __syncthreads();
     const int m0 = static_cast<int>(before >> 32);
-    const int m1 = min(m0 + static_cast<int>(total >> 32), most);
+    const int m1 = min(m0 + static_cast<int>(total >> 32), room);
     for (int kb = m0 + tid; kb < m1; kb += F * NT) {
         int j[F], p[F];
         uint32_t slot[F];
@@ -467,28 +482,8 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         }
     }
     __syncthreads();
-    // What stays keeps its place (the freed places are filled in step 4), and the places past
-    // the budget start at zero.
+    // The places past the budget start at zero.
     const int under = min(max(b - i0, 0), n);   // entries of the slice below the budget
-    if (move_w || move_p || i0 + under > tracked)
-        for (int ib = tid; ib < under; ib += F * NT) {
-            float x[F];
-            int p[F];
-#pragma unroll
-            for (int u = 0; u < F; ++u) {
-                const int i = ib + u * NT;
-                if (i >= under) continue;
-                if (move_w) x[u] = w[i0 + i];
-                if (move_p || i0 + i >= tracked) p[u] = position(i0 + i);
-            }
-#pragma unroll
-            for (int u = 0; u < F; ++u) {
-                const int i = ib + u * NT;
-                if (i >= under) continue;
-                if (move_w) wo[i0 + i] = x[u];
-                if (move_p || i0 + i >= tracked) po[i0 + i] = p[u];
-            }
-        }
     for (int i = under + tid; i < n; i += NT) wo[i0 + i] = 0.f;
     if (C > 1)
         cluster.sync();
