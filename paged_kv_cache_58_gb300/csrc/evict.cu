@@ -68,8 +68,7 @@ constexpr int kHist = kBins + kBins / 8;
 struct Shared {   // after it: three bits per entry
     int hist[kHist];
     int cluster_hist[kHist];          // the cluster's, in its first CTA
-    uint32_t list_key[kList];
-    int list_at[kList];
+    unsigned long long list[kList];   // key << 32 | ~index: a larger one ranks higher
     unsigned long long warp_sums[kWarps];
     unsigned long long cluster_sums[3][kMaxCluster];
     int pick[3];                      // bin, entries above it, entries in it
@@ -109,10 +108,13 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     uint32_t* safe_bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));   // protected
     uint32_t* keep_bits = safe_bits + words;
     uint32_t* tie_bits = keep_bits + words;      // equal to the threshold
-    griddep_wait();
-    griddep_launch_dependents();
     const int kvh = blockIdx.x / C, rank = blockIdx.x % C, seq = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < kHist; i += NT) sm.hist[i] = sm.cluster_hist[i] = 0;
+    if (tid == 0) sm.listed = 0;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
 
     const int row = a.row_ids ? __ldg(a.row_ids + seq) : seq;
     const int L = __ldg(a.context_lens + seq);
@@ -163,9 +165,6 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     cg::cluster_group cluster = cg::this_cluster();
 
     // ---------------------------------------------------------------- 1. classes, first digit
-    for (int i = tid; i < kHist; i += NT) sm.hist[i] = sm.cluster_hist[i] = 0;
-    if (tid == 0) sm.listed = 0;
-    __syncthreads();
     const int recent_from = seen - a.recent;
     int mine = 0;
     for (int ib = tid; ib - lane < n; ib += F * NT) {   // whole warps
@@ -316,10 +315,9 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
             if (inside) {
                 atomicAdd(&sm.hist[spread((key >> 10) & 2047u)], 1);
                 const int slot = atomicAdd(&sm.listed, 1);
-                if (slot < kList) {
-                    sm.list_key[slot] = key;
-                    sm.list_at[slot] = i;
-                }
+                if (slot < kList)
+                    sm.list[slot] = static_cast<unsigned long long>(key) << 32 |
+                                    ~static_cast<uint32_t>(i);
             }
         }
     }
@@ -328,13 +326,11 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     // A short list of one CTA is ranked outright, each entry against all.
     const bool ranked = open && C == 1 && listed <= NT;
     if (ranked && tid < listed) {
-        const uint32_t key = sm.list_key[tid];
-        const int i = sm.list_at[tid];
+        const unsigned long long entry = sm.list[tid];
+        const int i = static_cast<int>(~static_cast<uint32_t>(entry));
         int better = 0;
-        for (int q = 0; q < listed; ++q) {
-            const uint32_t k = sm.list_key[q];
-            better += k > key || (k == key && sm.list_at[q] < i);
-        }
+#pragma unroll 8
+        for (int q = 0; q < listed; ++q) better += sm.list[q] > entry;
         if (better < need) atomicOr(&keep_bits[i >> 5], 1u << (i & 31));
     }
     if (ranked) __syncthreads();
@@ -346,7 +342,9 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
             if (by_list) {
                 for (int q = tid; q - lane < listed; q += NT) {
                     const bool on = q < listed;
-                    f(on ? sm.list_at[q] : 0, on, on ? sm.list_key[q] : 0u);
+                    const unsigned long long entry = on ? sm.list[q] : 0xffffffffull;
+                    f(static_cast<int>(~static_cast<uint32_t>(entry)), on,
+                      static_cast<uint32_t>(entry >> 32));
                 }
             } else {
                 scan([&](int i, bool in, float x) {
@@ -425,8 +423,8 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     if (C == 1 && max(static_cast<int>(all >> 32), static_cast<int>(all & 0xffffffffu)) <= kList) {
         // short lists of one CTA: where the threshold's bin and the histograms were
         static_assert(kHist >= 2 * kList, "two lists in a histogram's place");
-        holes = sm.list_at;
-        movers = reinterpret_cast<int32_t*>(sm.list_key);
+        holes = reinterpret_cast<int32_t*>(sm.list);
+        movers = holes + kList;
         mover_slot = reinterpret_cast<uint32_t*>(sm.hist);
         mover_w = reinterpret_cast<float*>(sm.cluster_hist);
         mover_pos = sm.cluster_hist + kList;
