@@ -21,15 +21,19 @@
 //      select ends early when a bin is kept whole.
 //   3. freed places below the budget and kept entries past it are counted and numbered 32 at
 //      a time, a thread per word of the bits, and written to two lists, a mover with its
-//      weight and position, so that its old entry is cleared in the same scan.
+//      weight and position, so that its old entry is cleared in the same scan.  Short lists
+//      of a CTA with its row alone stay in shared memory.
 //   4. after one cluster barrier all threads copy the listed rows, 16 bytes of K and of V
-//      per lane, four rows in flight per lane and the places of the next four looked up
-//      meanwhile.
-// Measured (one call of many, from a graph): 64 x 8 rows of 1040 entries, 16 over budget, 13.9
-// us, the chain of dependent steps (about 1.7 us to start, 2 a scan, 1 a narrowing, 2 to list);
-// 512 to 4096 down to 1024, 68.5 us, 44 of them the moves at 5.7 TB/s; 16 x 8 rows of 16k to
-// 128k down to 8192, 241 us, 133 of them the moves at 7.3 TB/s, the rest three scans of 10.9 M
-// entries at about 90 issue slots per 32.
+//      per lane, three or four rows in flight per lane and the places of the next ones looked
+//      up meanwhile.  (A cluster looks the sources' up when it lists them: 239 us against 254
+//      for 16 x 128k; one CTA as it moves them, a chain of loads less: 64.4 us against 66.3 for
+//      64 x 4k.)
+// Measured (one call of many, from a graph): 64 x 8 rows of 1040 entries, 16 over budget, 10.3
+// us, a chain of dependent steps; 512 to 4096 down to 1024, 62.7 us, about 44 of them the
+// moves at 5.7 TB/s; 16 x 8 rows of 16k to 128k down to 8192, 240 us, 133 of them the moves at
+// 7.3 TB/s, the rest three scans of 10.9 M entries at about 90 issue slots per 32.  Four CTAs
+// per SM: with three and the registers that leaves, 320 rows take 52.7 us for 54.9 (3000 entries
+// down to 1024), but 512 rows a second wave, 14.4 us for 10.3 and 89.8 for 76.0.
 // With C = 1 there are no cluster barriers.  The scans read the weights where they are, in
 // L2 after the first: keys kept in shared memory left two CTAs on an SM and a row's
 // latencies uncovered.  Weights crowd into few exponents (and many may be zero), but counting
@@ -99,10 +103,11 @@ PKV_DEVINL V block_scan(V v, unsigned long long* warp_sums, V& total) {
     return before + incl - v;
 }
 
-// F: entries in flight per thread in a scan.
-template <int F>
+// F: entries in flight per thread in a scan.  ONE: a CTA has its row alone (C = 1).
+template <int F, bool ONE>
 __global__ void __launch_bounds__(NT, 4)
-evict_kernel(const EvictArgs a, const int C, const int words) {
+evict_kernel(const EvictArgs a, const int cluster_ctas, const int words) {
+    const int C = ONE ? 1 : cluster_ctas;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sm = *reinterpret_cast<Shared*>(raw);
     uint32_t* safe_bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));   // protected
@@ -416,18 +421,17 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     int32_t* holes = a.moves + (static_cast<size_t>(seq) * a.num_kv_heads + kvh) *
                                    (5 * static_cast<size_t>(most));
     int32_t* movers = holes + most;
-    uint32_t* mover_slot = reinterpret_cast<uint32_t*>(movers + most);
+    uint32_t* mover_slot = reinterpret_cast<uint32_t*>(movers + most);   // clusters
     float* mover_w = reinterpret_cast<float*>(mover_slot + most);
     int32_t* mover_pos = holes + 4 * static_cast<size_t>(most);
     int room = most;
     if (C == 1 && max(static_cast<int>(all >> 32), static_cast<int>(all & 0xffffffffu)) <= kList) {
         // short lists of one CTA: where the threshold's bin and the histograms were
-        static_assert(kHist >= 2 * kList, "two lists in a histogram's place");
+        static_assert(kHist >= kList, "a list in a histogram's place");
         holes = reinterpret_cast<int32_t*>(sm.list);
         movers = holes + kList;
-        mover_slot = reinterpret_cast<uint32_t*>(sm.hist);
-        mover_w = reinterpret_cast<float*>(sm.cluster_hist);
-        mover_pos = sm.cluster_hist + kList;
+        mover_w = reinterpret_cast<float*>(sm.hist);
+        mover_pos = sm.cluster_hist;
         room = kList;
     }
     // Pool slots fit 32 bits: 2^32 rows of the least 128 bytes are more than this GPU holds.
@@ -466,7 +470,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
 #pragma unroll
         for (int u = 0; u < F; ++u) {
             if (j[u] < 0) continue;
-            slot[u] = slot_of(j[u]);
+            if (!ONE) slot[u] = slot_of(j[u]);
             x[u] = w[j[u]];
             p[u] = position(j[u]);
         }
@@ -474,7 +478,7 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         for (int u = 0; u < F; ++u) {
             const int k = kb + u * NT;
             if (j[u] < 0) continue;
-            mover_slot[k] = slot[u];
+            if (!ONE) mover_slot[k] = slot[u];
             mover_w[k] = x[u];
             mover_pos[k] = p[u];
         }
@@ -504,18 +508,21 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
         const size_t blk = slot >> a.block_shift;
         return ((((blk * a.num_kv_heads + kvh) << a.block_shift) + (slot & low)) << csh) + ch;
     };
-    constexpr int U = 4;
+    constexpr int U = ONE ? 3 : 4;   // rows in flight: four cost registers that spill with ONE
     uint32_t from[U], to[U];
     auto look_up = [&](int k0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u * step;
-            from[u] = k < nmoves ? mover_slot[k] : kNoSlot;
+            from[u] = k >= nmoves ? kNoSlot : ONE ? static_cast<uint32_t>(movers[k]) : mover_slot[k];
             to[u] = k < nmoves ? static_cast<uint32_t>(holes[k]) : kNoSlot;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (to[u] != kNoSlot) to[u] = slot_of(static_cast<int>(to[u]));
+            if (to[u] != kNoSlot) {
+                if (ONE) from[u] = slot_of(static_cast<int>(from[u]));
+                to[u] = slot_of(static_cast<int>(to[u]));
+            }
     };
     int k0 = worker >> csh;
     look_up(k0);
@@ -543,9 +550,9 @@ evict_kernel(const EvictArgs a, const int C, const int words) {
     }
 }
 
-template <int F>
+template <int F, bool ONE>
 cudaError_t launch_f(const EvictArgs& a, int C, cudaStream_t stream) {
-    auto kern = evict_kernel<F>;
+    auto kern = evict_kernel<F, ONE>;
     const int words = ((a.max_context + C - 1) / C + 31) / 32;
     const int smem = static_cast<int>(sizeof(Shared)) + 3 * 4 * words;
     // allowed for the longest slice at once: host threads that raised the limit to what each
@@ -578,15 +585,15 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
     // us, 269 with slices of 32768, before the scans counted as they do now), and that about two CTAs per SM exist where there are few
     // rows.  More where rows fill the SMs only adds cluster barriers (512 rows with two each: a
     // block of 64 took 39 us against 15.6, 512 to 4096 entries 76 against 72).
-    // Entries in flight per thread: four in a CTA that has its row alone (eight: 16.3 and 73.2 us
-    // against 15.6 and 72.3), eight where clusters scan long rows (four 243.5 us, sixteen 258,
+    // Entries in flight per thread: four in a CTA that has its row alone (eight: 12.2 and 67.2 us
+    // against 11.4 and 66.3), eight where clusters scan long rows (four 243.5 us, sixteen 258,
     // against 241).
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
     int C = 1;
     while (C < kMaxCluster &&
            (a.max_context > 16384 * C || (rows * C < 304 && a.max_context > 1024 * C)))
         C *= 2;
-    return C == 1 ? launch_f<4>(a, C, stream) : launch_f<8>(a, C, stream);
+    return C == 1 ? launch_f<4, true>(a, C, stream) : launch_f<8, false>(a, C, stream);
 }
 
 }  // namespace pkv
