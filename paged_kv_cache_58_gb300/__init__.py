@@ -700,7 +700,8 @@ def rope(x, positions, inv_freq, *, interleaved=False, inverse=False, attn_scale
     st = _load().pkv_rope(_dtype_code(x), op, os_, xp, xs,
                           _arg(positions, "positions", dev, torch.int32, (T,)),
                           _arg(inv_freq, "inv_freq", dev, torch.float64, (half,)), 2 * half,
-                          bool(interleaved), bool(inverse), attn_scale, T, H, D, _stream_on(stream, dev))
+                          bool(interleaved), bool(inverse), attn_scale, T, H, D,
+                          _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_rope", st)
     return out
@@ -728,7 +729,8 @@ def rope_append(q, k, v, k_pool, v_pool, slot_mapping, positions, inv_freq, *, i
                                  os_, qp, qs, kr, ks, vr, vs,
                                  _arg(positions, "positions", dev, torch.int32, (T,)),
                                  _arg(inv_freq, "inv_freq", dev, torch.float64, (half,)),
-                                 2 * half, bool(interleaved), attn_scale, T, Hq, _stream_on(stream, dev))
+                                 2 * half, bool(interleaved), attn_scale, T, Hq,
+                                 _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_rope_append", st)
     return q_out
@@ -767,7 +769,8 @@ def paged_decode_weights(q, k_pool, v_pool, block_tables, context_lens, scale, w
         _arg(block_tables, "block_tables", dev, torch.int32, (S, block_tables.shape[1])),
         block_tables.shape[1], _arg(context_lens, "context_lens", dev, torch.int32, (S,)),
         max_context, S, Hq, scale, partition_blocks, wp, stride,
-        _opt(row_ids, "row_ids", dev, torch.int32, (S,)), rows, decay, ws, wsb, _stream_on(stream, dev))
+        _opt(row_ids, "row_ids", dev, torch.int32, (S,)), rows, decay, ws, wsb,
+        _stream_on(stream, dev))
     if st != 0:
         raise PkvError("pkv_paged_decode_weights", st)
     return out
