@@ -226,6 +226,7 @@ struct PrefillWeightsArgs {
     float* weights;           // [num_rows][Hkv][weights_stride]
     float2* stats;            // workspace: (reference, sum) [R][Hkv][splits][rows_pad];
                               // tensor cores: two of them, [..][splits][2][rows_pad]
+    int* next_item;           // workspace (tensor cores): pass 1's counter of items taken
     float* neg_lse;           // workspace (tensor cores): -log2(sum 2^s) [R][Hkv][rows_pad]
     int* status;
     int64_t num_blocks;

@@ -1168,6 +1168,7 @@ struct PrefillWeightsPlan {
 // What the kept scores of one launch may take (fp32): as many (request, kv head) pairs as fit
 // kScoreBytes, or one alone that fits kScoreMost.  A larger one has its scores computed twice.
 constexpr int64_t kScoreBytes = int64_t{256} << 20, kScoreMost = int64_t{1} << 30;
+constexpr size_t kCounterBytes = 16;   // at the start of the workspace
 bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_heads, int max_new,
                           int max_context, int window, PrefillWeightsPlan* p) {
     const int64_t rows = static_cast<int64_t>(window_rows(max_new, window)) *
@@ -1198,13 +1199,15 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
         p->splits = static_cast<int>(std::min<int64_t>(
             std::min<int64_t>(std::max<int64_t>(304 / ctas, 1), ceil_div(max_context, 64)), 32));
     } else {
-        // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 582 us for the
-        // call, 594 with 16, 609 with 8, where the parts' own first tiles and statistics
-        // count), shorter where there would be fewer than two items per SM, and at most 32 of
-        // them.  The lengths are not known here, only their bound.
+        // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 543 us for the
+        // call, 555 with 16, 551 with 32), shorter, down to 4, where there would be fewer than
+        // one item per SM, and at most 32 of them.  One request, its last 64 of 512 tokens after
+        // 8k, 32 heads on 8: 30.8 us; 58 with parts of 2, more than an item per SM, whose own
+        // first tiles and statistics count; 500 tokens after 2k, 8 heads on 1: 31.6 and 45.  The
+        // lengths are not known here, only their bound.
         const int64_t items = heads * ((row_tiles + 1) / 2);
         p->chunk_tiles = static_cast<int>(
-            std::max<int64_t>(2, std::min<int64_t>(24, (items * tiles + 303) / 304)));
+            std::max<int64_t>(4, std::min<int64_t>(24, (items * tiles + 151) / 152)));
         p->chunk_tiles = std::max(p->chunk_tiles, ceil_div(tiles, 32));
         p->splits = ceil_div(tiles, p->chunk_tiles);
     }
@@ -1218,7 +1221,7 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
     p->stats_bytes = static_cast<size_t>(heads) * p->splits * (f32 ? 1 : 2) * p->rows_pad *
                      sizeof(float2);
     p->lse_bytes = f32 ? 0 : static_cast<size_t>(heads) * p->rows_pad * sizeof(float);
-    p->bytes = p->stats_bytes + p->lse_bytes + p->score_bytes +
+    p->bytes = kCounterBytes + p->stats_bytes + p->lse_bytes + p->score_bytes +
                (p->row_parts > 1 ? static_cast<size_t>(heads) * p->row_parts *
                                        static_cast<size_t>(max_context) * sizeof(float)
                                  : 0);
@@ -1281,9 +1284,11 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     a.q_offsets = q_offsets;
     a.row_ids = row_ids;
     a.weights = weights;
-    a.stats = static_cast<float2*>(workspace);
-    a.neg_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes);
-    char* after = static_cast<char*>(workspace) + plan.stats_bytes + plan.lse_bytes;
+    char* base = static_cast<char*>(workspace) + kCounterBytes;
+    a.next_item = static_cast<int*>(workspace);
+    a.stats = reinterpret_cast<float2*>(base);
+    a.neg_lse = reinterpret_cast<float*>(base + plan.stats_bytes);
+    char* after = base + plan.stats_bytes + plan.lse_bytes;
     a.scores = plan.score_bytes ? reinterpret_cast<float*>(after) : nullptr;
     a.parts = reinterpret_cast<float*>(after + plan.score_bytes);
     a.key_pad = plan.key_pad;

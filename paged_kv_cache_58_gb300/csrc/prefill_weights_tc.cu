@@ -21,28 +21,29 @@
 // exponentials 512 cycles at 32 a cycle, and its operands are read from shared memory at 128
 // bytes a cycle, all there is, so that the copies' writes (32 KB per B tile) and pass 2's
 // reads of -lse slow the products down.  On the 16 x 512-token batch (every new token, 3.2e11
-// flop a pass) the two passes take 267 and 288 us; pass 1 takes 237 us without exponentials and
-// 220 with its products alone.  Measured there and not kept (before the A tiles of pass 1 went
-// into TMEM, when the call took 596 us): four A tiles
-// per B tile with one TMEM buffer each (half the copies): 653 us for the call instead of 596;
-// B tiles of 256, whose products read 96 bytes a cycle, with one TMEM buffer per A tile: 638
-// us (425 us without exponentials: a tile's product and its exponentials take turns); equal
+// flop a pass) the two passes take 253 and 288 us; pass 1 took 267 us before its items were
+// balanced, 237 without exponentials and 220 with its products alone.  Measured there and not
+// kept, before the A tiles of pass 1 went into TMEM, when the call took 596 us: four A tiles per
+// B tile with one TMEM buffer each (half the copies): 653 us; B tiles of 256, whose products
+// read 96 bytes a cycle, with one TMEM buffer per A tile: 638 us (425 us without exponentials:
+// a tile's product and its exponentials take turns); TMEM loads a step ahead: 639 us; equal
 // contiguous stretches of A tiles per CTA instead of every n-th item: 620 us.
 //
 // Pass 1 keeps the maximum of a row's first tile of the item (the first with a score above
-// -inf) as its reference and adds
-// 2^(s - m) from there on without looking for a larger one: there is no accumulator to
-// keep in range, only a sum in fp32, whose relative precision does not depend on the
-// reference.  Only a sum past 2^96 (later scores beyond the first tile's maximum by that
+// -inf) as its reference and adds 2^(s - m) from there on without looking for a larger one:
+// there is no accumulator to keep in range, only a sum in fp32, whose relative precision does
+// not depend on the reference.  Only a sum past 2^96 (later scores beyond the first tile's maximum by that
 // much) takes the tile again with a new reference.  The keys of a row tile are cut into
 // chunks that different CTAs take; a small launch merges the chunks' (m, sum) into
 // -log2(sum 2^s) per row, which is all that pass 2 needs:
 //   p = 2^(scale_log2 s - lse).
 //
-// Persistent CTAs, one per SM, each walking every gridDim.x-th item: producers run ahead into
-// the next item's tiles while the consumers finish the current one.  (Items sorted into large
-// ones first changed nothing: 593 us.)  Roles: warps 0-15 consumers, warp 16 A tiles, warp 17
-// B tiles, warp 18 MMA and TMEM, warp 19 the B rows' -lse (pass 2).
+// Persistent CTAs, one per SM: producers run ahead into the next item's tiles while the
+// consumers finish the current one.  Pass 1's items differ in length (the last chunk of keys,
+// the causal edge), and every gridDim.x-th item to a CTA left the longest with a quarter more
+// than the mean; taken from a shared counter, the call went from 573 to 543 us.  Pass 2's are
+// many and alike: every gridDim.x-th.  Roles: warps 0-15 consumers, warp 16 A tiles, warp 17 B
+// tiles, warp 18 MMA and TMEM, warp 19 the B rows' -lse (pass 2).
 #include <atomic>
 
 #include <cuda.h>
@@ -64,6 +65,7 @@ constexpr int kThreads = 640;
 constexpr int kConsumers = 16;      // warps
 constexpr int kWarpA = 16, kWarpB = 17, kWarpMma = 18, kWarpL = 19;
 constexpr int kMaxReqs = 256;       // requests per launch (the item offsets in shared memory)
+constexpr int kRing = 8;            // items announced (pass 1)
 constexpr int kStagesL = 3;         // tiles of -lse staged (pass 2), 512 B each
 constexpr int kBufs1 = 3, kColS1 = 128;   // pass 1: score buffers, behind two A tiles
 constexpr float kSumLimit = 7.9e28f;   // 2^96
@@ -83,10 +85,12 @@ struct Geom {
                          S_FULL = 4 + 2 * kStagesB, S_FREE = S_FULL + 4, L_FULL = S_FREE + 4,
                          L_EMPTY = L_FULL + kStagesL, X_FULL = L_EMPTY + kStagesL,
                          DRAIN = X_FULL + 16, T_FULL = X_FULL;   // T_FULL: pass 1 alone
-    static constexpr int kBars = DRAIN + 1;
+    static constexpr int R_FULL = DRAIN + 1;
+    static constexpr int kBars = R_FULL + kRing;
     static constexpr int kOffL = kOffBar + (kBars * 8 + 15) / 16 * 16;
     static constexpr int kOffCtl = kOffL + kStagesL * kTile * 4;   // TMEM address, abort flag
-    static constexpr int kOffItems = kOffCtl + 16;
+    static constexpr int kOffRing = kOffCtl + 16;
+    static constexpr int kOffItems = kOffRing + kRing * 4;
     static constexpr int kBytes = kOffItems + (kMaxReqs + 1) * 4;
 };
 // One CTA fills an SM; there is no room for slack to align by, so the kernel relies on the
@@ -151,16 +155,54 @@ struct Item {
     Request q;
 };
 
-// The walk over a CTA's items: item k of request r (off[r] <= k < off[r + 1]).
+// The walk over a CTA's items: item k of request r (off[r] <= k < off[r + 1]).  Pass 2, whose
+// items are many and alike, and launches with an item per CTA at most, take every gridDim.x-th.
+// Otherwise the A role takes the next one from a counter that all CTAs share whenever it is
+// ready for one, and announces it to the CTA's other roles in a ring.  The ring needs no
+// account of what has been read: an entry e is written once the A tiles of item e - 3 have
+// been taken, by consumers that were through with item e - 4 and so with all that the other
+// roles do for it.  Indices only grow, so the search for the request goes on where it was.
 template <int PASS>
 struct Walk {
     const PrefillWeightsArgs& a;
     const int* off;
-    int k, r = 0;
-    PKV_DEVINL Walk(const PrefillWeightsArgs& args, const int* offsets)
-        : a(args), off(offsets), k(blockIdx.x) {}
-    PKV_DEVINL bool next(Item& it) {
-        for (;; k += gridDim.x) {
+    const Ctl& ctl;
+    int* ring;
+    int ring_bar;
+    int k, r = 0, n = 0;
+    bool shared;
+    PKV_DEVINL Walk(const PrefillWeightsArgs& args, const int* offsets, const Ctl& c, int* entries,
+                    int first_bar)
+        : a(args), off(offsets), ctl(c), ring(entries), ring_bar(first_bar), k(blockIdx.x),
+          shared(PASS == 1 && args.next_item != nullptr) {}
+    // The whole warp calls, for the next item or the end of them.
+    PKV_DEVINL bool next(Item& it, bool announces = false) {
+        if (!shared) return decode(it, gridDim.x);
+        const int e = n % kRing;
+        if (announces) {
+            const int lane = threadIdx.x & 31;
+            bool found;
+            do {   // one item at a time: those without a tile to do are passed over
+                if (lane == 0) k = atomicAdd(a.next_item, 1);
+                k = __shfl_sync(0xffffffffu, k, 0);
+                found = k < off[a.num_reqs] && decode(it, 0);
+            } while (!found && k < off[a.num_reqs]);
+            if (lane == 0) {
+                ring[e] = found ? k : -1;
+                mbar_arrive(&ctl.bars[ring_bar + e]);
+            }
+            __syncwarp();
+            ++n;
+            return found;
+        }
+        if (!wait_bar(ctl, ring_bar + e, (n / kRing) & 1)) return false;
+        k = *static_cast<volatile int*>(ring + e);
+        ++n;
+        return k >= 0 && decode(it, 0);
+    }
+    // Item k; or, where it has nothing to do and `step` is not 0, the first `step`s further that has.
+    PKV_DEVINL bool decode(Item& it, int step) {
+        for (;; k += step) {
             if (k >= off[a.num_reqs]) return false;
             while (off[r + 1] <= k) ++r;
             it.r = r;
@@ -194,9 +236,10 @@ struct Walk {
                 it.nb = min(ceil_div(it.q.rows, kTile), (it.chunk + 1) * part) - it.b0;
             }
             if (it.nb > 0) {
-                k += gridDim.x;
+                k += step;
                 return true;
             }
+            if (step == 0) return false;
         }
     }
 };
@@ -329,13 +372,13 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Ctl ctl{bars, abort_flag, a.status};
-    Walk<PASS> walk(a, off);
+    Walk<PASS> walk(a, off, ctl, reinterpret_cast<int*>(smem + GM::kOffRing), GM::R_FULL);
     Item it;
 
     if (warp == kWarpA) {
         // ------------------------------------------------------------ A tiles
         int i = 0, issued = 0;
-        for (; walk.next(it); ++i) {
+        for (; walk.next(it, true); ++i) {
             const int s = i & 1;
             if (i >= 2 && !wait_bar(ctl, GM::A_EMPTY + s, ((i >> 1) - 1) & 1)) break;
             uint8_t* dst = smem + GM::kOffA + s * 2 * GM::kTileBytes;
@@ -737,6 +780,13 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
     }
 }
 
+// Pass 1's counter of items taken.
+__global__ void reset_items_kernel(const PrefillWeightsArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) *a.next_item = 0;
+}
+
 // -log2 of a row's sum over its chunks, and -inf for the rows that pad the last tile.
 // Grid (row blocks, kv head, request).
 __global__ void __launch_bounds__(128)
@@ -817,8 +867,14 @@ cudaError_t launch_d(const PrefillWeightsArgs& a, int group, cudaStream_t stream
         const int64_t heads = static_cast<int64_t>(g.num_reqs) * a.num_kv_heads;
         const int64_t items1 = heads * ((row_tiles + 1) / 2) * a.splits;
         const int64_t items2 = heads * key_pairs * a.row_parts;
-        if (items1 > INT32_MAX || items2 > INT32_MAX) return cudaErrorNotSupported;
+        if (items1 > INT32_MAX - 65536 || items2 > INT32_MAX) return cudaErrorNotSupported;
         const int sms = sm_count();
+        if (items1 > sms) {
+            e = launch_pdl(reset_items_kernel, dim3(1), dim3(32), 0, stream, g);
+            if (e != cudaSuccess) return e;
+        } else {
+            g.next_item = nullptr;
+        }
         e = launch_pdl(pass1, dim3(static_cast<unsigned>(items1 < sms ? items1 : sms)),
                        dim3(kThreads), GM::kBytes, stream, mq, mk, g);
         if (e != cudaSuccess) return e;
