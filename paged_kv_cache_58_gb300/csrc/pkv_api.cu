@@ -1199,11 +1199,11 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
         p->splits = static_cast<int>(std::min<int64_t>(
             std::min<int64_t>(std::max<int64_t>(304 / ctas, 1), ceil_div(max_context, 64)), 32));
     } else {
-        // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 543 us for the
-        // call, 555 with 16, 551 with 32), shorter, down to 4, where there would be fewer than
+        // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 582 us for the
+        // call, 594 with 16, 609 with 8, before pass 1 was balanced), shorter, down to 4, where there would be fewer than
         // one item per SM, and at most 32 of them.  One request, its last 64 of 512 tokens after
-        // 8k, 32 heads on 8: 30.8 us; 58 with parts of 2, more than an item per SM, whose own
-        // first tiles and statistics count; 500 tokens after 2k, 8 heads on 1: 31.6 and 45.  The
+        // 8k, 32 heads on 8: 30.6 us; 55 with parts of 2, more than an item per SM, whose own
+        // first tiles and statistics count; 500 tokens after 2k, 8 heads on 1: 30.9 and 44.  The
         // lengths are not known here, only their bound.
         const int64_t items = heads * ((row_tiles + 1) / 2);
         p->chunk_tiles = static_cast<int>(

@@ -9,30 +9,30 @@
 // TMEM lanes: a thread owns a query row (pass 1) or a key (pass 2) and reduces over its
 // own registers.  An item holds up to two A tiles (256 rows or keys) and streams B tiles
 // past them; every B tile staged serves both, which halves the copies per product.  Each A
-// tile has two consumer warpgroups, one per half of the columns: with 16 consumer warps a
-// scheduler has four to switch between while loads from TMEM, exponentials and barriers are
-// under way (8 warps took 1.2 times as long).  In pass 2 an A tile stays in shared memory and
-// has two TMEM buffers of 128 columns (all 512 columns).  In pass 1, whose items are longer,
-// the consumers move it into TMEM first, which takes half of the products' reads from shared
-// memory away; three buffers of scores are left then, taken in turn (285 -> 267 us, and 57.5
-// -> 52.7 for the last 64 tokens of each request).
+// tile has two TMEM buffers of 128 columns (all 512 columns) and two consumer warpgroups,
+// one per half of the columns: with 16 consumer warps a scheduler has four to switch
+// between while loads from TMEM, exponentials and barriers are under way (8 warps took 1.2
+// times as long).
 //
 // What bounds it: a product of 128 x 128 x 128 takes the tensor pipe 512 cycles, its 16384
 // exponentials 512 cycles at 32 a cycle, and its operands are read from shared memory at 128
 // bytes a cycle, all there is, so that the copies' writes (32 KB per B tile) and pass 2's
 // reads of -lse slow the products down.  On the 16 x 512-token batch (every new token, 3.2e11
-// flop a pass) the two passes take 253 and 288 us; pass 1 took 267 us before its items were
-// balanced, 237 without exponentials and 220 with its products alone.  Measured there and not
-// kept, before the A tiles of pass 1 went into TMEM, when the call took 596 us: four A tiles per
-// B tile with one TMEM buffer each (half the copies): 653 us; B tiles of 256, whose products
-// read 96 bytes a cycle, with one TMEM buffer per A tile: 638 us (425 us without exponentials:
-// a tile's product and its exponentials take turns); TMEM loads a step ahead: 639 us; equal
-// contiguous stretches of A tiles per CTA instead of every n-th item: 620 us.
+// flop a pass) the two passes take 265 and 288 us; pass 1 took 285 before its items were
+// balanced, 250 without exponentials and 240 with its products alone.  Measured there and not
+// kept, when the call took 596 us: four A tiles per B tile with one TMEM buffer each (half the
+// copies): 653 us; B tiles of 256, whose products read 96 bytes a cycle, with one TMEM buffer
+// per A tile: 638 us (425 us without exponentials: a tile's product and its exponentials take
+// turns); TMEM loads a step ahead: 639 us; equal contiguous stretches of A tiles per CTA
+// instead of every n-th item: 620 us.  A tiles in TMEM took pass 1 from 285 to 267 us, but leave
+// three score buffers for two groups of consumers: a group that sat out an item could pass
+// the wait for a buffer's next phase before the other group's phase was over.
 //
 // Pass 1 keeps the maximum of a row's first tile of the item (the first with a score above
-// -inf) as its reference and adds 2^(s - m) from there on without looking for a larger one:
-// there is no accumulator to keep in range, only a sum in fp32, whose relative precision does
-// not depend on the reference.  Only a sum past 2^96 (later scores beyond the first tile's maximum by that
+// -inf) as its reference and adds
+// 2^(s - m) from there on without looking for a larger one: there is no accumulator to
+// keep in range, only a sum in fp32, whose relative precision does not depend on the
+// reference.  Only a sum past 2^96 (later scores beyond the first tile's maximum by that
 // much) takes the tile again with a new reference.  The keys of a row tile are cut into
 // chunks that different CTAs take; a small launch merges the chunks' (m, sum) into
 // -log2(sum 2^s) per row, which is all that pass 2 needs:
@@ -41,7 +41,7 @@
 // Persistent CTAs, one per SM: producers run ahead into the next item's tiles while the
 // consumers finish the current one.  Pass 1's items differ in length (the last chunk of keys,
 // the causal edge), and every gridDim.x-th item to a CTA left the longest with a quarter more
-// than the mean; taken from a shared counter, the call went from 573 to 543 us.  Pass 2's are
+// than the mean; taken from a shared counter, the call went from 590 to 555 us.  Pass 2's are
 // many and alike: every gridDim.x-th.  Roles: warps 0-15 consumers, warp 16 A tiles, warp 17 B
 // tiles, warp 18 MMA and TMEM, warp 19 the B rows' -lse (pass 2).
 #include <atomic>
@@ -65,9 +65,9 @@ constexpr int kThreads = 640;
 constexpr int kConsumers = 16;      // warps
 constexpr int kWarpA = 16, kWarpB = 17, kWarpMma = 18, kWarpL = 19;
 constexpr int kMaxReqs = 256;       // requests per launch (the item offsets in shared memory)
-constexpr int kRing = 8;            // items announced (pass 1)
+constexpr int kRing = 4;            // items announced (pass 1)
+constexpr int kReaders = kConsumers + 2;   // warps that read them: consumers, B tiles, MMA
 constexpr int kStagesL = 3;         // tiles of -lse staged (pass 2), 512 B each
-constexpr int kBufs1 = 3, kColS1 = 128;   // pass 1: score buffers, behind two A tiles
 constexpr float kSumLimit = 7.9e28f;   // 2^96
 
 template <int D>
@@ -84,9 +84,10 @@ struct Geom {
     static constexpr int A_FULL = 0, A_EMPTY = 2, B_FULL = 4, B_EMPTY = 4 + kStagesB,
                          S_FULL = 4 + 2 * kStagesB, S_FREE = S_FULL + 4, L_FULL = S_FREE + 4,
                          L_EMPTY = L_FULL + kStagesL, X_FULL = L_EMPTY + kStagesL,
-                         DRAIN = X_FULL + 16, T_FULL = X_FULL;   // T_FULL: pass 1 alone
+                         DRAIN = X_FULL + 16;
     static constexpr int R_FULL = DRAIN + 1;
-    static constexpr int kBars = R_FULL + kRing;
+    static constexpr int R_EMPTY = R_FULL + kRing;
+    static constexpr int kBars = R_EMPTY + kRing;
     static constexpr int kOffL = kOffBar + (kBars * 8 + 15) / 16 * 16;
     static constexpr int kOffCtl = kOffL + kStagesL * kTile * 4;   // TMEM address, abort flag
     static constexpr int kOffRing = kOffCtl + 16;
@@ -158,10 +159,9 @@ struct Item {
 // The walk over a CTA's items: item k of request r (off[r] <= k < off[r + 1]).  Pass 2, whose
 // items are many and alike, and launches with an item per CTA at most, take every gridDim.x-th.
 // Otherwise the A role takes the next one from a counter that all CTAs share whenever it is
-// ready for one, and announces it to the CTA's other roles in a ring.  The ring needs no
-// account of what has been read: an entry e is written once the A tiles of item e - 3 have
-// been taken, by consumers that were through with item e - 4 and so with all that the other
-// roles do for it.  Indices only grow, so the search for the request goes on where it was.
+// ready for one, and announces it to the CTA's other roles in a ring; a place of the ring is
+// written again when all of them have read it.  Indices only grow, so the search for the
+// request goes on where it was.
 template <int PASS>
 struct Walk {
     const PrefillWeightsArgs& a;
@@ -187,6 +187,7 @@ struct Walk {
                 k = __shfl_sync(0xffffffffu, k, 0);
                 found = k < off[a.num_reqs] && decode(it, 0);
             } while (!found && k < off[a.num_reqs]);
+            if (n >= kRing && !wait_bar(ctl, ring_bar + kRing + e, (n / kRing - 1) & 1)) return false;
             if (lane == 0) {
                 ring[e] = found ? k : -1;
                 mbar_arrive(&ctl.bars[ring_bar + e]);
@@ -197,6 +198,8 @@ struct Walk {
         }
         if (!wait_bar(ctl, ring_bar + e, (n / kRing) & 1)) return false;
         k = *static_cast<volatile int*>(ring + e);
+        __syncwarp();
+        mbar_arrive_if((threadIdx.x & 31) == 0, &ctl.bars[ring_bar + kRing + e]);
         ++n;
         return k >= 0 && decode(it, 0);
     }
@@ -326,13 +329,12 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
     }
     if (warp == kWarpA) {
         if (lane == 0) {
-            for (int i = 0; i < GM::kBars; ++i) {   // arrivals: an A tile's consumers, all, or 1
-                const bool half = (i >= GM::S_FREE && i < GM::S_FREE + 4) ||
-                                  (PASS == 1 && i >= GM::T_FULL && i < GM::T_FULL + 2);
-                const bool all = (i >= GM::L_EMPTY && i < GM::L_EMPTY + kStagesL) ||
-                                 (PASS == 1 && i >= GM::A_EMPTY && i < GM::A_EMPTY + 2);
-                mbar_init(&bars[i], half ? kConsumers / 2 : all ? kConsumers : 1);
-            }
+            for (int i = 0; i < GM::kBars; ++i)   // arrivals: an A tile's consumers, all of them, 1
+                mbar_init(&bars[i],
+                          i >= GM::S_FREE && i < GM::S_FREE + 4 ? kConsumers / 2
+                          : i >= GM::L_EMPTY && i < GM::L_EMPTY + kStagesL ? kConsumers
+                          : i >= GM::R_EMPTY                               ? kReaders
+                                                                           : 1);
             *abort_flag = 0;
             fence_mbar_init();
             prefetch_tmap(&tm_q);
@@ -456,16 +458,10 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
         const uint32_t lo_b = smem_desc_sw128_lo(smem_u32(smem + GM::kOffB), 16);
         const bool leader = elect_one();
         int i = 0, g = 0, used[2] = {0, 0};   // items, B tiles, tiles given to warpgroup w
-        int p = 0, wrote[2] = {0, 0};         // pass 1: products, A tiles in TMEM so far
         bool ok = true;
         while (ok && walk.next(it)) {
             const int sa = i & 1;
-            if (PASS == 2) {
-                ok = wait_bar(ctl, GM::A_FULL + sa, (i >> 1) & 1);
-            } else {
-                for (int w = 0; ok && w < it.na; ++w)
-                    ok = wait_bar(ctl, GM::T_FULL + w, wrote[w]++ & 1);
-            }
+            ok = wait_bar(ctl, GM::A_FULL + sa, (i >> 1) & 1);
             for (int j = 0; ok && j < it.nb; ++j, ++g) {
                 const int sb = g % GM::kStagesB;
                 ok = wait_bar(ctl, GM::B_FULL + sb, (g / GM::kStagesB) & 1);
@@ -473,25 +469,6 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (w >= it.na) continue;
-                    if (PASS == 1) {
-                        const int buf = p % kBufs1;
-                        if (p >= kBufs1 &&
-                            !wait_bar(ctl, GM::S_FREE + buf, (p / kBufs1 - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        ++p;
-                        tc_fence_after();
-                        const uint32_t lb = lo_b + ((sb * GM::kTileBytes) >> 4);
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            umma_bf16_ta_if(leader, tmem + kColS1 + buf * 128,
-                                            tmem + w * (D / 2) + ks * 8,
-                                            desc_join(lb + (ks >> 2) * step_b + (ks & 3) * 2, hi_b),
-                                            idesc, ks > 0);
-                        umma_commit_if(leader, &bars[GM::S_FULL + buf]);
-                        continue;
-                    }
                     const int buf = w + 2 * (used[w] & 1);
                     if (used[w] >= 2 &&
                         !wait_bar(ctl, GM::S_FREE + buf, ((used[w] >> 1) - 1) & 1)) {
@@ -513,7 +490,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                 }
                 umma_commit_if(leader, &bars[GM::B_EMPTY + sb]);
             }
-            if (PASS == 2) umma_commit_if(leader, &bars[GM::A_EMPTY + sa]);
+            umma_commit_if(leader, &bars[GM::A_EMPTY + sa]);
             ++i;
         }
         // every product has completed before the TMEM goes
@@ -556,7 +533,6 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const float sl2 = a.scale_log2;
         int used = 0, gl = 0;   // tiles of this A tile's consumers; tiles of -lse
-        int item = 0, done = 0;   // pass 1: items, and products before the item
         uint32_t met_phase[2] = {0, 0};
         bool ok = true;
         while (ok && walk.next(it)) {
@@ -564,51 +540,16 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
             const bool mine = wg < it.na;
             const size_t head = static_cast<size_t>(it.r) * a.num_kv_heads + it.kvh;
             if (PASS == 1) {
-                // The A tile goes from shared memory to TMEM, a lane to a row, half of the
-                // elements to a warp.  The item before has no product left that reads it: this
-                // warp has waited for its last one.
-                const int sa = item & 1;
-                if (!wait_bar(ctl, GM::A_FULL + sa, (item >> 1) & 1)) { ok = false; break; }
-                ++item;
-                const int first = done;
-                done += it.nb * it.na;
-                if (mine) {
-                    constexpr int kPieces = D / 16;   // 16-byte pieces of a row's half
-                    const uint8_t* src = smem + GM::kOffA + (sa * 2 + wg) * GM::kTileBytes +
-                                         (D == 128 ? half * kHalf : 0) + (row >> 3) * 1024 +
-                                         (row & 7) * 128;
-                    uint32_t u[4 * kPieces];
-#pragma unroll
-                    for (int c = 0; c < kPieces; ++c) {
-                        const int piece = D == 128 ? c : half * kPieces + c;
-                        const uint4 v =
-                            *reinterpret_cast<const uint4*>(src + ((piece ^ (row & 7)) << 4));
-                        u[4 * c] = v.x; u[4 * c + 1] = v.y; u[4 * c + 2] = v.z; u[4 * c + 3] = v.w;
-                    }
-                    const uint32_t tA = tmem + lanes + wg * (D / 2) + half * (D / 4);
-                    tc_fence_after();
-                    if constexpr (D == 128)
-                        tmem_st32(tA, *reinterpret_cast<const float(*)[32]>(&u[0]));
-                    else
-                        tmem_st16(tA, u);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    mbar_arrive_if(lane == 0, &bars[GM::T_FULL + wg]);
-                }
-                __syncwarp();
-                mbar_arrive_if(lane == 0, &bars[GM::A_EMPTY + sa]);
                 if (!mine) continue;
                 const int rho = tile * kTile + row;
                 const int lim = it.base + (rho >> a.group_shift);        // last key seen
                 const int least = it.base + ((tile * kTile) >> a.group_shift);
                 float m = 0.f, l = 0.f;
-                for (int j = 0; j < it.nb; ++j) {
-                    const int p = first + j * it.na + wg;
-                    const int buf = p % kBufs1;
-                    if (!wait_bar(ctl, GM::S_FULL + buf, (p / kBufs1) & 1)) { ok = false; break; }
+                for (int j = 0; j < it.nb; ++j, ++used) {
+                    const int buf = wg + 2 * (used & 1);
+                    if (!wait_bar(ctl, GM::S_FULL + buf, (used >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t tS = tmem + lanes + kColS1 + buf * 128 + 64 * half;
+                    const uint32_t tS = tmem + lanes + buf * 128 + 64 * half;
                     const int key0 = (it.b0 + j) * kTile + 64 * half;
                     const int seen = lim - key0 + 1;   // the columns that the row sees
                     const bool whole = key0 + 63 <= least;
@@ -869,7 +810,7 @@ cudaError_t launch_d(const PrefillWeightsArgs& a, int group, cudaStream_t stream
         const int64_t items2 = heads * key_pairs * a.row_parts;
         if (items1 > INT32_MAX - 65536 || items2 > INT32_MAX) return cudaErrorNotSupported;
         const int sms = sm_count();
-        if (items1 > sms) {
+        if (items1 > sms) {   // the counter passes their number by one a CTA at most
             e = launch_pdl(reset_items_kernel, dim3(1), dim3(32), 0, stream, g);
             if (e != cudaSuccess) return e;
         } else {

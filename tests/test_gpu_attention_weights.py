@@ -319,6 +319,36 @@ def test_prefill_weights_growing_scores(pkv, dtype):
     assert bool((err <= p * 2.0 ** -12 + 160 * 2.0 ** -120).all()), (err / p.clamp(min=1e-30)).max()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_weights_odd_and_even_row_tiles(pkv, d):
+    """Requests of one and of three row tiles in turn, many items to a CTA: half of the consumers
+    sit some items out."""
+    g = gen(47)
+    R, hkv, group = 24, 4, 4
+    new = [(7, 90, 30, 5, 70, 96)[i % 6] for i in range(R)]
+    cached = [(911 * i) % 1300 + 200 * (i % 2) for i in range(R)]
+    total = [c + n for c, n in zip(cached, new)]
+    kp, _, table = paged(total, hkv, 16, d, torch.bfloat16, g)
+    q = torch.randn(sum(new), hkv * group, d, generator=g, device="cuda").bfloat16()
+    off = [sum(new[:i]) for i in range(R + 1)]
+
+    def call():
+        w = torch.zeros(R, hkv, max(total), device="cuda")
+        return pkv.paged_prefill_weights(q, kp, table, i32(cached), i32(new), i32(off), d ** -0.5, w,
+                                         max_new=max(new), max_context=max(total))
+
+    w = call()
+    assert pkv.read_device_status() == 0
+    for _ in range(20):
+        assert torch.equal(call(), w)
+    kc, tc, qc, wc = kp.cpu(), table.cpu(), q.cpu(), w.cpu().double()
+    for i, n in enumerate(total):
+        k = tokens(kc, tc[i], n)
+        _, p, size = attention(qc[off[i]:off[i + 1]], k, None, d ** -0.5, first=cached[i])
+        err = (wc[i, :, :n] - p).abs()
+        assert bool((err <= weight_bound(p, p * 0, size, d, n + new[i] * group)).all()), i
+
+
 @pytest.mark.parametrize("max_new,max_context", [(1024, 4096),     # a launch per kv head
                                                  (16384, 4096)])   # scores computed twice
 @pytest.mark.parametrize("window", [0, 50])
