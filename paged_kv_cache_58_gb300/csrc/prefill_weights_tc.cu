@@ -187,7 +187,8 @@ struct Walk {
                 k = __shfl_sync(0xffffffffu, k, 0);
                 found = k < off[a.num_reqs] && decode(it, 0);
             } while (!found && k < off[a.num_reqs]);
-            if (n >= kRing && !wait_bar(ctl, ring_bar + kRing + e, (n / kRing - 1) & 1)) return false;
+            if (n >= kRing && !wait_bar(ctl, ring_bar + kRing + e, (n / kRing - 1) & 1))
+                return false;
             if (lane == 0) {
                 ring[e] = found ? k : -1;
                 mbar_arrive(&ctl.bars[ring_bar + e]);
@@ -203,7 +204,8 @@ struct Walk {
         ++n;
         return k >= 0 && decode(it, 0);
     }
-    // Item k; or, where it has nothing to do and `step` is not 0, the first `step`s further that has.
+    // Item k; or, where it has nothing to do and `step` is not 0, the first of the items `step`
+    // apart from there on that has.
     PKV_DEVINL bool decode(Item& it, int step) {
         for (;; k += step) {
             if (k >= off[a.num_reqs]) return false;
