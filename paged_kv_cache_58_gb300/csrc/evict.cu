@@ -168,6 +168,10 @@ evict_kernel(const EvictArgs a, const int cluster_ctas, const int words) {
         return;
     }
     cg::cluster_group cluster = cg::this_cluster();
+    // No CTA touches another's shared memory before all of the cluster are known to run: they
+    // arrive here (the returns above are taken by all of a cluster or by none) and wait ahead
+    // of the first remote access, behind the first scan.
+    if (!ONE) cluster.barrier_arrive();
 
     // ---------------------------------------------------------------- 1. classes, first digit
     const int recent_from = seen - a.recent;
@@ -203,6 +207,7 @@ evict_kernel(const EvictArgs a, const int cluster_ctas, const int words) {
     }
     int cta_safe;
     block_scan(mine, sm.warp_sums, cta_safe);
+    if (!ONE) cluster.barrier_wait();
     // Totals of the CTAs before this one, and of all, through `slot` of the exchange array.
     auto gather = [&](unsigned long long v, int slot, unsigned long long& before,
                       unsigned long long& all) {
