@@ -390,7 +390,8 @@ pkv_status pkv_rope_frequencies(double* inv_freq, float* attn_scale, int rotary_
  *   x, out      device, dtype (pkv_dtype), 16-byte aligned; token t's heads start at element
  *               t * stride (a multiple of 16 bytes; heads of a token contiguous), so a slice
  *               of a fused projection is read in place.  out_stride >= num_heads * head_dim.
- *               out may be x itself (same address and stride), else must not overlap it.
+ *               out may be x itself (same address and stride); rows that overlap it in any
+ *               other way are refused (PKV_ERR_INVALID).
  *   positions   device int32 [num_tokens] (negative ones turn the other way).
  *   inv_freq    device double [rotary_dim / 2], radians per position.
  *   rotary_dim  a multiple of 16, 16 .. head_dim; head_dim 64 or 128 (PKV_ERR_UNSUPPORTED).
@@ -403,7 +404,8 @@ pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int
 
 /* pkv_rope of a step's q rows into q_out, and pkv_kv_append of its k rows, turned, and v
  * rows, in one launch.  q, k, v: [num_tokens][heads][head_dim] with token strides as above
- * (q has num_q_heads heads, k and v the pool's); q_out may be q itself (same stride).
+ * (q has num_q_heads heads, k and v the pool's); q_out may be q itself (same stride), and is
+ * refused where it overlaps q in any other way, or k or v.
  * Slots as pkv_kv_append, no two tokens with the same one: a negative slot skips the token's K
  * and V (its q is turned all the same), one past the pool raises PKV_ERR_OOB in the device
  * status word. */

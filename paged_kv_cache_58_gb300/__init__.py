@@ -680,7 +680,7 @@ def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, low
 def rope(x, positions, inv_freq, *, interleaved=False, inverse=False, attn_scale=1.0, out=None,
          stream=None):
     """Rows x [T, H, D] turned by their token's position (int32 [T]); returns out (a new
-    contiguous tensor, or the one given, which may be x itself).
+    contiguous tensor, or the one given, which may be x itself but not overlap it otherwise).
 
     The first 2 * len(inv_freq) elements of a row turn (inv_freq float64, radians per
     position: rope_frequencies).  x may be a slice of a fused projection: its tokens any

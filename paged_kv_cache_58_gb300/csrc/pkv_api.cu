@@ -1056,6 +1056,36 @@ bool stride_ok(int64_t stride, int64_t least, int es) {
     return stride >= least && (stride * es) % 16 == 0;
 }
 
+// n rows of `bytes` each, `step` bytes apart (0: the same row n times).
+struct Rows {
+    const void* at;
+    int64_t step, bytes;
+};
+// Whether n rows `out` have no byte in common with n rows `in`: a kernel's CTAs read and write
+// them in any order.  Rows of one step may lie between one another (slices of one projection).
+bool rows_apart(const Rows& out, const Rows& in, int64_t n) {
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(in.at) -
+                                           reinterpret_cast<uintptr_t>(out.at));
+    if (d >= (n - 1) * out.step + out.bytes || -d >= (n - 1) * in.step + in.bytes) return true;
+    // The first row of `out`, from row `first` on, that ends behind a row of `in` which begins e
+    // bytes from out's row 0: apart where it is none of them or begins behind that row.
+    const int64_t step = std::max<int64_t>(out.step, 1);
+    auto apart_from = [&](int64_t e, int64_t first) {
+        const int64_t gap = e - out.bytes;
+        const int64_t below = gap >= 0 ? gap / step : -((-gap + step - 1) / step);   // rounded down
+        const int64_t u = std::max(below + 1, first);
+        return u >= n || u * step >= e + in.bytes;
+    };
+    if (in.step == out.step) return apart_from(d, 1 - n);   // by the difference of the rows' numbers
+    for (int64_t t = 0; t < (in.step ? n : 1); ++t)
+        if (!apart_from(d + t * in.step, 0)) return false;
+    return true;
+}
+// The same rows, turned in place, or apart.
+bool same_or_rows_apart(const Rows& out, const Rows& in, int64_t n) {
+    return (out.at == in.at && (out.step == in.step || n == 1)) || rows_apart(out, in, n);
+}
+
 }  // namespace
 
 pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int64_t x_stride,
@@ -1076,6 +1106,9 @@ pkv_status pkv_rope(int dtype, void* out, int64_t out_stride, const void* x, int
     const int es = elem_bytes(dtype);
     if (!stride_ok(out_stride, static_cast<int64_t>(num_heads) * head_dim, es) ||
         !stride_ok(x_stride, 0, es))
+        return PKV_ERR_INVALID;
+    const int64_t row = static_cast<int64_t>(num_heads) * head_dim * es;
+    if (!same_or_rows_apart({out, out_stride * es, row}, {x, x_stride * es, row}, num_tokens))
         return PKV_ERR_INVALID;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;
@@ -1122,6 +1155,13 @@ pkv_status pkv_rope_append(const pkv_pool_desc* pool, void* k_pool, void* v_pool
     const int es = elem_bytes(pool->dtype);
     if (!stride_ok(q_out_stride, static_cast<int64_t>(num_q_heads) * pool->head_dim, es) ||
         !stride_ok(q_stride, 0, es) || !stride_ok(k_stride, 0, es) || !stride_ok(v_stride, 0, es))
+        return PKV_ERR_INVALID;
+    const int64_t head = static_cast<int64_t>(pool->head_dim) * es;
+    const int64_t q_row = num_q_heads * head, kv_row = pool->num_kv_heads * head;
+    const Rows turned = {q_out, q_out_stride * es, q_row};
+    if (!same_or_rows_apart(turned, {q, q_stride * es, q_row}, num_tokens) ||
+        !rows_apart(turned, {k, k_stride * es, kv_row}, num_tokens) ||
+        !rows_apart(turned, {v, v_stride * es, kv_row}, num_tokens))
         return PKV_ERR_INVALID;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;

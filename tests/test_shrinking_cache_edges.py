@@ -1,10 +1,14 @@
 """Host side of the corners of the operators around a shrinking cache."""
+import ctypes
 import os
+import random
 import re
 
 import pytest
+import torch
 
-OK, INVALID = 0, 1
+INVALID = 1
+A = 0x1000000
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "paged_kv_cache_58_gb300", "csrc")
 
@@ -28,3 +32,64 @@ def test_evict_waits_for_its_cluster_before_it_touches_it():
     assert barrier < kernel.index("map_shared_rank")
     if kernel.index("cluster.barrier_wait()") == barrier:
         assert kernel.index("cluster.barrier_arrive()") < barrier
+
+
+# ------------------------------------------------------------------ rows that overlap
+
+fake = pytest.mark.skipif(torch.cuda.is_available(), reason="fake device pointers")
+
+
+def touch(n, a, a_step, a_bytes, b, b_step, b_bytes):
+    """Whether any of n rows at a has a byte in common with any of n rows at b."""
+    return any(a + i * a_step < b + j * b_step + b_bytes and b + j * b_step < a + i * a_step + a_bytes
+               for i in range(n) for j in range(n))
+
+
+@fake
+def test_rope_refuses_rows_that_overlap(pkv):
+    """The output in its input's place, between its rows and apart from them is taken, rows that
+    share a byte are not; against every pair of rows looked at."""
+    H, D, es = 2, 64, 2
+    row = H * D * es
+    r = random.Random(7)
+
+    def taken(out, so, x, sx, n):
+        # on a host without a GPU a call whose arguments are accepted ends with the CUDA error
+        return pkv.lib().pkv_rope(1, out, so // es, x, sx // es, A, A, 64, 0, 0, 1.0, n, H, D,
+                                  None) != INVALID
+
+    assert taken(A, row, A, row, 5) and taken(A, 3 * row, A, 3 * row, 5)       # in place
+    assert taken(A, 4 * row, A, row, 1)                                        # one token
+    assert taken(A, 3 * row, A + row, 3 * row, 5)                              # a neighbour slice
+    assert not taken(A, row, A + 16, row, 5) and not taken(A + 16, row, A, row, 5)
+    assert not taken(A, 2 * row, A, row, 5) and not taken(A, row, A, 0, 2)
+    assert not taken(A, 3 * row, A + 3 * row, 3 * row, 2)                      # a token later
+    both = [0, 0]
+    for _ in range(4000):
+        n = r.choice([1, 2, 3, 7])
+        so = row + 16 * r.choice([0, 1, 8, 16, 17, 40])
+        sx = r.choice([so, 0, 16, row, row + 16 * r.randint(0, 40)])
+        x = A + 16 * r.randint(-150, 150)
+        want = (x == A and (so == sx or n == 1)) or not touch(n, A, so, row, x, sx, row)
+        assert taken(A, so, x, sx, n) == want, (n, so, sx, x - A)
+        both[want] += 1
+    assert min(both) > 500
+
+
+@fake
+def test_rope_append_refuses_an_output_over_its_inputs(pkv):
+    d, far = pkv.PoolDesc(64, 16, 2, 64, 1), A + (1 << 24)
+    es, step, T = 2, 8 * 64 * 2, 4       # tokens of 4 + 2 + 2 heads
+
+    def taken(qo, q, k, v, qos=step):
+        return pkv.lib().pkv_rope_append(
+            ctypes.byref(d), far, far, far, qo, qos // es, q, step // es, k, step // es, v,
+            step // es, far, far, 64, 0, 1.0, T, 4, None) != INVALID
+
+    q, k, v = A, A + 4 * 128, A + 6 * 128
+    assert taken(q, q, k, v)                           # in place, in one projection
+    assert taken(far + (1 << 20), q, k, v)
+    assert not taken(q + 16, q, k, v) and not taken(q, q, k, v, qos=2 * step)
+    assert not taken(q + 128, q, k, v)                 # its last head is k's first
+    assert not taken(q, A + (1 << 20), q + 3 * 128, v) and not taken(q, q, k, q + 3 * step)
+    assert taken(A + T * step, q, k, v) and not taken(A + T * step - 16, q, k, v)
