@@ -669,7 +669,7 @@ def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, low
     sc = RopeScaling(ROPE_KINDS[scaling], float(factor), float(1 if low is None else low),
                      float((32 if scaling == "yarn" else 4) if high is None else high),
                      float(original_context))
-    out = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    out = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64, device="cpu")
     scale = ctypes.c_float(1.0)
     _check("pkv_rope_frequencies", _load().pkv_rope_frequencies(
         ctypes.cast(out.data_ptr(), ctypes.POINTER(ctypes.c_double)), ctypes.byref(scale),

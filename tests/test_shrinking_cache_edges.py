@@ -34,6 +34,16 @@ def test_evict_waits_for_its_cluster_before_it_touches_it():
         assert kernel.index("cluster.barrier_arrive()") < barrier
 
 
+# ------------------------------------------------------------------ frequencies
+
+def test_frequencies_under_another_default_device(pkv):
+    """They are computed on the host: torch's default device must not name where."""
+    want, _ = pkv.rope_frequencies(64, device="cpu")
+    with torch.device("meta"):
+        got, _ = pkv.rope_frequencies(64, device="cpu")
+    assert got.device.type == "cpu" and torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ rows that overlap
 
 fake = pytest.mark.skipif(torch.cuda.is_available(), reason="fake device pointers")
