@@ -941,7 +941,7 @@ class BlockAllocator:
 
     def block_table(self, seq_ids, max_blocks: int) -> torch.Tensor:
         ids = (ctypes.c_int64 * len(seq_ids))(*seq_ids)
-        out = torch.empty((len(seq_ids), max_blocks), dtype=torch.int32)
+        out = torch.empty((len(seq_ids), max_blocks), dtype=torch.int32, device="cpu")
         _check("pkv_alloc_block_table", self._lib.pkv_alloc_block_table(
             self._h, ids, len(seq_ids),
             ctypes.cast(out.data_ptr(), ctypes.POINTER(ctypes.c_int32)), max_blocks))

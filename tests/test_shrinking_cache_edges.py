@@ -44,6 +44,15 @@ def test_frequencies_under_another_default_device(pkv):
     assert got.device.type == "cpu" and torch.equal(got, want)
 
 
+def test_block_table_under_another_default_device(pkv):
+    a = pkv.BlockAllocator(4, 16)
+    a.add_seq(1, 40)
+    want = a.block_table([1], 4)
+    with torch.device("meta"):
+        got = a.block_table([1], 4)
+    assert got.device.type == "cpu" and torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ rows that overlap
 
 fake = pytest.mark.skipif(torch.cuda.is_available(), reason="fake device pointers")
