@@ -371,13 +371,19 @@ pkv_status pkv_copy_blocks(const pkv_pool_desc* pool, void* k_pool, void* v_pool
  * original_context > 0: PKV_ERR_INVALID otherwise.  With n_i = original_context * f_i /
  * (2 pi) turns over the trained context, PKV_ROPE_LLAMA3 and PKV_ROPE_YARN divide a
  * frequency by `factor` where n_i <= low, keep it where n_i >= high, and blend the two
- * linearly in n_i between. */
+ * linearly in n_i between.  PKV_ROPE_YARN_PAIRS has PKV_ROPE_YARN's bands and scale, but blends
+ * linearly in the pair index i, from the last whole index at which n_i >= high to the first at
+ * which n_i <= low (theta > 1: PKV_ERR_INVALID otherwise).  The released models that name YaRN
+ * were trained that way; PKV_ROPE_YARN is the ramp of the method's paper.  The two differ inside
+ * the band (base 1e6, 128 dimensions, 32768 tokens, factor 4: pair 32 is 6.0e-4 by pair index,
+ * 3.5e-4 by turns), so a model's keys only fit with its own. */
 typedef enum pkv_rope_kind {
     PKV_ROPE_PLAIN = 0,
     PKV_ROPE_LINEAR = 1, /* every frequency divided by factor */
     PKV_ROPE_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)) */
     PKV_ROPE_LLAMA3 = 3, /* by bands of n_i (usual: low 1, high 4) */
-    PKV_ROPE_YARN = 4    /* by bands of n_i (usual: low 1, high 32), with an attn_scale */
+    PKV_ROPE_YARN = 4,   /* by bands of n_i (usual: low 1, high 32), with an attn_scale */
+    PKV_ROPE_YARN_PAIRS = 5 /* the same, blended by pair index: what released models use */
 } pkv_rope_kind;
 typedef struct pkv_rope_scaling {
     int32_t kind; /* pkv_rope_kind */

@@ -656,18 +656,21 @@ def _weights_arg(weights, dev, dtype, hkv, name="weights"):
     return _arg(weights, name, dev, dtype, weights.shape), weights.shape[0], weights.shape[2]
 
 
-ROPE_KINDS = {None: 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+ROPE_KINDS = {None: 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4, "yarn_pairs": 5}
 
 
 def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, low=None, high=None,
                      original_context=0, device="cuda"):
     """Rotary frequencies (float64 [rotary_dim / 2] on `device`) and the attention scale that
-    goes with them.  `scaling`: None, "linear", "ntk", "llama3" (low 1, high 4 unless given) or
-    "yarn" (low 1, high 32), the last two over a trained context of `original_context`."""
+    goes with them.  `scaling`: None, "linear", "ntk", "llama3" (low 1, high 4 unless given),
+    "yarn" or "yarn_pairs" (low 1, high 32), the last three over a trained context of
+    `original_context`.  "yarn_pairs" is what released YaRN models were trained with: the blend
+    between kept and stretched frequencies goes by pair index; "yarn" blends by turns, as the
+    method's paper has it."""
     if scaling not in ROPE_KINDS:
         raise ValueError(f"scaling must be one of {list(ROPE_KINDS)}")
     sc = RopeScaling(ROPE_KINDS[scaling], float(factor), float(1 if low is None else low),
-                     float((32 if scaling == "yarn" else 4) if high is None else high),
+                     float((4 if scaling == "llama3" else 32) if high is None else high),
                      float(original_context))
     out = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64, device="cpu")
     scale = ctypes.c_float(1.0)

@@ -1,5 +1,6 @@
 """Host side of the corners of the operators around a shrinking cache."""
 import ctypes
+import math
 import os
 import random
 import re
@@ -42,6 +43,54 @@ def test_frequencies_under_another_default_device(pkv):
     with torch.device("meta"):
         got, _ = pkv.rope_frequencies(64, device="cpu")
     assert got.device.type == "cpu" and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("r,theta,factor,trained,low,high", [
+    (128, 1e6, 4.0, 32768, 1, 32), (64, 1e4, 40.0, 4096, 1, 32), (128, 500000.0, 8.0, 8192, 2, 20),
+    (16, 150000.0, 32.0, 4096, 1, 32), (64, 1e4, 16.0, 4096, 0, 32), (32, 1e4, 2.0, 40, 1, 4)])
+def test_yarn_by_pair_index(pkv, r, theta, factor, trained, low, high):
+    """The blend that released models use: linear in the pair index, from the last whole index
+    with at least `high` turns over the trained context to the first with at most `low`."""
+    f, s = pkv.rope_frequencies(r, theta, scaling="yarn_pairs", factor=factor, low=low, high=high,
+                                original_context=trained, device="cpu")
+    assert s == pytest.approx(0.1 * math.log(factor) + 1, rel=1e-7)
+    plain = [theta ** (-2 * i / r) for i in range(r)]          # past r / 2 as well: the borders
+    turns = [trained * x / (2 * math.pi) for x in plain]
+    first = max([i for i in range(r) if turns[i] >= high], default=0)
+    last = min([i for i in range(r) if turns[i] <= low], default=r - 1)
+    assert last > first
+    for i, got in enumerate(f.tolist()):
+        stretched = min(max((i - first) / (last - first), 0.0), 1.0)
+        want = stretched * plain[i] / factor + (1 - stretched) * plain[i]
+        assert abs(got - want) <= 1e-12 * want, i
+
+
+def test_yarn_ramps_differ(pkv):
+    """Base 1e6, 32768 trained tokens, factor 4, 128 dimensions: pair 32 by index, worked out by
+    hand (between pairs 23 and 40: 8/17 kept), and by turns."""
+    kw = dict(factor=4, original_context=32768, device="cpu")
+    by_pair, _ = pkv.rope_frequencies(128, 1e6, scaling="yarn_pairs", **kw)
+    by_turns, _ = pkv.rope_frequencies(128, 1e6, scaling="yarn", **kw)
+    assert float(by_pair[32]) == pytest.approx(1e-3 * (8 / 17 + 9 / 17 / 4), rel=1e-12)
+    assert float(by_turns[32]) == pytest.approx(3.52e-4, rel=1e-2)
+    assert torch.equal(by_pair[:18], by_turns[:18]) and torch.equal(by_pair[40:], by_turns[40:])
+
+
+def test_yarn_by_pair_index_refusals(pkv):
+    kw = dict(scaling="yarn_pairs", device="cpu")
+    for bad in (dict(factor=4), dict(factor=4, original_context=4096, theta=1.0),
+                dict(factor=0.5, original_context=4096),
+                dict(factor=4, original_context=4096, low=4, high=4)):
+        with pytest.raises(pkv.PkvError) as e:
+            pkv.rope_frequencies(64, **bad, **kw)
+        assert e.value.status == INVALID
+    # the whole of a head turns more than `high` times, or less than `low`
+    f, _ = pkv.rope_frequencies(64, 2.0, factor=4, original_context=1 << 20, **kw)
+    g, _ = pkv.rope_frequencies(64, 2.0, device="cpu")
+    assert torch.equal(f, g)
+    f, _ = pkv.rope_frequencies(64, 1e4, factor=4, original_context=1, **kw)
+    g, _ = pkv.rope_frequencies(64, 1e4, device="cpu")
+    assert torch.equal(f, g / 4)
 
 
 def test_block_table_under_another_default_device(pkv):
