@@ -161,3 +161,22 @@ def test_rope_append_refuses_an_output_over_its_inputs(pkv):
     assert not taken(q + 128, q, k, v)                 # its last head is k's first
     assert not taken(q, A + (1 << 20), q + 3 * 128, v) and not taken(q, q, k, q + 3 * step)
     assert taken(A + T * step, q, k, v) and not taken(A + T * step - 16, q, k, v)
+
+
+# ------------------------------------------------------------------ plans
+
+@pytest.mark.parametrize("hkv", [2, 8])
+def test_prompt_weights_split_keys_by_the_ctas_of_a_launch(pkv, hkv):
+    """fp32: where the scores of one kv head fill a launch's share, a launch has that head's CTAs
+    alone, and its keys are cut for those as with one kv head: the statistics of a head take the
+    same room."""
+    ask = pkv.lib().pkv_paged_prefill_weights_workspace_bytes
+
+    def need(heads):
+        d = pkv.PoolDesc(4096, 16, heads, 64, 0)
+        return ask(ctypes.byref(d), 1, 4 * heads, 512, 32768, 0)
+
+    scores = 4 * 512 * 32768 * 4                       # one kv head's, all of the share
+    one = need(1) - scores - 16                        # a counter is in every workspace
+    assert one % (4 * 512 * 8) == 0 and one // (4 * 512 * 8) > 1     # parts of the keys
+    assert need(hkv) - scores - 16 == hkv * one
