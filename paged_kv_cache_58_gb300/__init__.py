@@ -688,8 +688,38 @@ def rope(x, positions, inv_freq, *, interleaved=False, inverse=False, attn_scale
     The first 2 * len(inv_freq) elements of a row turn (inv_freq float64, radians per
     position: rope_frequencies).  x may be a slice of a fused projection: its tokens any
     multiple of 16 bytes apart.  `inverse` turns the other way: it undoes the turn, and takes
-    a gradient with respect to the output to one with respect to x.
+    a gradient with respect to the output to one with respect to x.  Gradients flow to x through
+    the new tensor; where one is asked for, `out` is refused.
     """
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("rope: no gradient flows through out=; leave it out, or call under "
+                             "torch.no_grad()")
+        return _Rope.apply(x, positions, inv_freq, interleaved, inverse, attn_scale, stream)
+    return _rope(x, positions, inv_freq, interleaved, inverse, attn_scale, out, stream)
+
+
+class _Rope(torch.autograd.Function):
+    """The turn with its gradient: the opposite turn, same scale, of the output's gradient."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, interleaved, inverse, attn_scale, stream):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = interleaved, inverse, attn_scale
+        return _rope(x, positions, inv_freq, interleaved, inverse, attn_scale, None, stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        positions, inv_freq = ctx.saved_tensors
+        interleaved, inverse, attn_scale = ctx.how
+        grad = grad.contiguous()
+        if grad.data_ptr() % 16:
+            grad = grad.clone()
+        return (rope(grad, positions, inv_freq, interleaved=interleaved, inverse=not inverse,
+                     attn_scale=attn_scale),) + (None,) * 6
+
+
+def _rope(x, positions, inv_freq, interleaved, inverse, attn_scale, out, stream):
     dev = _device(x, "x")
     shape = x.shape
     if len(shape) != 3:
@@ -714,7 +744,8 @@ def rope_append(q, k, v, k_pool, v_pool, slot_mapping, positions, inv_freq, *, i
                 attn_scale=1.0, q_out=None, stream=None):
     """One launch for a step's new tokens: q [T, Hq, D] turned into q_out (returned), k [T, Hkv,
     D] turned and v [T, Hkv, D] as it is stored into their pool slots (slot < 0 = skip).
-    Arguments as rope and kv_append; q, k and v may be slices of one fused projection."""
+    Arguments as rope and kv_append; q, k and v may be slices of one fused projection.  As with
+    every call that writes the cache, no gradient flows."""
     d, dev, kp, vp_ = _pools(k_pool, v_pool)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")

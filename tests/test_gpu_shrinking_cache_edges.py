@@ -1,8 +1,9 @@
 """Corners of the operators around a shrinking cache that their own files do not reach: wide
-clusters over short rows."""
+clusters over short rows, the rotation inside a differentiated program."""
 import pytest
 import torch
 
+from tests.shrink_refs import rotate, rotate_bound
 from tests.test_gpu_evict import bits, expect, gen, i32, same_positions, setup
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +40,70 @@ def test_evict_wide_clusters_over_short_rows(pkv, kind):
     assert torch.equal(bits(kp), bits(want[0])) and torch.equal(bits(vp), bits(want[1]))
     assert torch.equal(w.cpu(), want[2])
     assert same_positions(pos, want[3], rows, want[4])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("interleaved,inverse", [(False, False), (True, True)])
+def test_rope_in_a_differentiated_program(pkv, dtype, interleaved, inverse):
+    """The output carries a gradient: the opposite turn of the output's, for gradients of any
+    layout (expanded, strided, off the 16-byte grid); and it has one itself."""
+    g = gen(41)
+    f, _ = pkv.rope_frequencies(48)
+    pos = torch.tensor([5, 77777, 3], dtype=torch.int32, device="cuda")
+    leaf = torch.randn(3, 6, 64, generator=g, device="cuda").to(dtype).requires_grad_()
+    x = leaf[:, 2:4]                                        # a slice of a fused projection
+    kw = dict(interleaved=interleaved, attn_scale=1.5)
+    y = pkv.rope(x, pos, f, inverse=inverse, **kw)
+    assert y.requires_grad
+    with torch.no_grad():
+        plain = pkv.rope(x, pos, f, inverse=inverse, **kw)
+    assert not plain.requires_grad and torch.equal(plain, y.detach())
+    w = torch.randn(3, 2, 64, generator=g, device="cuda").to(dtype)
+    flat = torch.randn(3 * 2 * 64 + 1, generator=g, device="cuda").to(dtype)
+    for out_grad in (w, w[:, :1].expand(3, 2, 64), w.transpose(0, 1).contiguous().transpose(0, 1),
+                     flat[1:].view(3, 2, 64)):
+        got, = torch.autograd.grad(y, leaf, out_grad, retain_graph=True)
+        ref = rotate(out_grad, pos, f, inverse=not inverse, **kw)
+        bound = rotate_bound(out_grad, pos, f, ref, dtype, **kw)
+        assert got.dtype == dtype
+        assert bool(((got[:, 2:4].cpu().double() - ref).abs() <= bound).all())
+        assert not got[:, :2].any() and not got[:, 4:].any()
+    # the gradient is linear in the output's gradient: its own is the turn again
+    v = w.clone().requires_grad_()
+    gx, = torch.autograd.grad(y, x, v, create_graph=True)
+    again, = torch.autograd.grad(gx, v, w)
+    assert torch.equal(again, pkv.rope(w, pos, f, inverse=inverse, **kw))
+    # a lost gradient is refused, not passed over
+    for out in (torch.empty_like(w), x):
+        with pytest.raises(ValueError):
+            pkv.rope(x, pos, f, out=out)
+    with torch.no_grad():
+        assert torch.equal(pkv.rope(x, pos, f, inverse=inverse, out=torch.empty_like(w), **kw), plain)
+    # positions that changed since would give another gradient: torch refuses
+    pos.add_(1)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, leaf, w)
+
+
+def test_rope_gradient_captured(pkv):
+    """Forward and backward captured on a side stream and replayed over new inputs."""
+    g = gen(42)
+    f, _ = pkv.rope_frequencies(64)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    x = torch.randn(9, 4, 64, generator=g, device="cuda").bfloat16()
+    w = torch.randn(9, 4, 64, generator=g, device="cuda").bfloat16()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        leaf = x.detach().requires_grad_()
+        y = pkv.rope(leaf, pos, f)
+        grad, = torch.autograd.grad(y, leaf, w)
+    torch.cuda.synchronize()
+    w.mul_(-2.0)
+    pos.add_(70)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y.detach(), pkv.rope(x, pos, f))
+    assert torch.equal(grad, pkv.rope(w, pos, f, inverse=True))
+    assert pkv.read_device_status() == 0
