@@ -93,6 +93,14 @@ def test_yarn_by_pair_index_refusals(pkv):
     assert torch.equal(f, g / 4)
 
 
+def test_readme_passes_the_scale_on():
+    """YaRN's scale goes with its frequencies: the example that takes both passes both."""
+    with open(os.path.join(os.path.dirname(CSRC), "..", "README.md")) as f:
+        example = f.read().split("freq, attn_scale = pkv.rope_frequencies(", 1)[1].split("```")[0]
+    for call in re.findall(r"pkv\.rope(?:_append)?\(((?:[^()]|\([^()]*\))*)\)", example):
+        assert "freq" in call and "attn_scale=attn_scale" in call
+
+
 def test_block_table_under_another_default_device(pkv):
     a = pkv.BlockAllocator(4, 16)
     a.add_seq(1, 40)
