@@ -567,9 +567,11 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
     const int seq = idx / a.num_kv_heads;
     // The lengths, rows and old weights come from before the split kernel.  That kernel lets
     // this one start only once all its CTAs have seen their own predecessors complete, so
-    // these are read while it still runs; its scores and partials only after the wait.
-    const int row = a.row_ids ? __ldg(a.row_ids + seq) : seq;
-    int L = min(__ldg(a.context_lens + seq), a.score_tokens);
+    // these are read while it still runs; its scores and partials only after the wait.  From
+    // L2, where those predecessors' writes are: a line that this SM kept from before them, as
+    // where two kv heads' rows meet in one, is not looked at.
+    const int row = a.row_ids ? __ldcg(a.row_ids + seq) : seq;
+    int L = min(__ldcg(a.context_lens + seq), a.score_tokens);
     L = min(L, (a.max_blocks_per_seq << a.chunk_shift) * kBlock);
     int j0 = first * kWeightTile + static_cast<int>(threadIdx.x);
     const bool idle = row < 0 || first * kWeightTile >= L;   // padding, or past the sequence
@@ -581,11 +583,11 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
     float* wp = a.weights + (static_cast<size_t>(idle || lost ? 0 : row) * a.num_kv_heads + kvh) *
                                 static_cast<size_t>(a.weights_stride);
     const int end = idle || lost ? 0 : min(L, (first + run) * kWeightTile);
-    auto load_weights = [&](int j, float (&w)[PER]) {
+    auto load_weights = [&](int j, float (&w)[PER], bool ahead) {   // ahead of the wait
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int ju = j + u * kThr;
-            w[u] = (ju < end && a.decay != 0.f) ? wp[ju] : 0.f;
+            w[u] = (ju < end && a.decay != 0.f) ? (ahead ? __ldcg(wp + ju) : wp[ju]) : 0.f;
         }
     };
     auto load = [&](int j, float (&s)[PER][G]) {
@@ -596,7 +598,7 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
         }
     };
     float s[PER][G], w[PER];
-    load_weights(j0, w);
+    load_weights(j0, w, true);
     griddep_wait();
     griddep_launch_dependents();
     if (threadIdx.x == 0 && (lost || beyond)) raise_status(a.status, PKV_ERR_OOB);
@@ -629,7 +631,7 @@ decode_finish_kernel(const DecodeArgs a, const int combine_ctas, const int runs,
         float sn[PER][G], wn[PER];
         if (more) {
             load(next, sn);
-            load_weights(next, wn);
+            load_weights(next, wn, false);
         }
 #pragma unroll
         for (int u = 0; u < PER; ++u) {

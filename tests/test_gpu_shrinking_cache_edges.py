@@ -1,5 +1,6 @@
 """Corners of the operators around a shrinking cache that their own files do not reach: wide
-clusters over short rows, the rotation inside a differentiated program."""
+clusters over short rows, the rotation inside a differentiated program,
+decode steps that follow each other without a pause."""
 import pytest
 import torch
 
@@ -106,4 +107,42 @@ def test_rope_gradient_captured(pkv):
     torch.cuda.synchronize()
     assert torch.equal(y.detach(), pkv.rope(x, pos, f))
     assert torch.equal(grad, pkv.rope(w, pos, f, inverse=True))
+    assert pkv.read_device_status() == 0
+
+
+@pytest.mark.parametrize("S,hkv,group,d,n,pb", [(3, 3, 4, 128, 700, 8), (16, 2, 8, 64, 2000, 16),
+                                                (2, 1, 1, 64, 5000, 4), (5, 4, 2, 128, 90, 0)])
+def test_decode_weights_steps_back_to_back(pkv, S, hkv, group, d, n, pb):
+    """Steps that start before the one before them has ended, over growing contexts and rows
+    whose ends share cache lines, against the same steps one at a time: the same bits."""
+    g = gen(n)
+    blocks, W = -(-n // 16), n + 7
+    kp = torch.randn(S * blocks, hkv, 16, d, generator=g, device="cuda").bfloat16()
+    vp = torch.randn(S * blocks, hkv, 16, d, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(S * blocks, generator=g, device="cuda").view(S, -1).to(torch.int32)
+    lens = torch.randint(n // 2, n - 24, (S,), generator=g, device="cuda", dtype=torch.int32)
+    w0 = torch.rand(S, hkv, W, generator=g, device="cuda")
+    q = torch.randn(24, S, hkv * group, d, generator=g, device="cuda").bfloat16()
+    kn = torch.randn(24, S, hkv, d, generator=g, device="cuda").bfloat16()
+    ids = torch.randperm(S, generator=g, device="cuda").to(torch.int32)
+    need = pkv.decode_weights_workspace_bytes(kp, S, hkv * group, n, pb)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def steps(pause):
+        k, v, w, cl = kp.clone(), vp.clone(), w0.clone(), lens.clone()
+        out = torch.empty_like(q)
+        for i in range(24):
+            cl.add_(1)
+            for new, decay in ((kn[i], 0.9), (None, 0.99)):
+                pkv.paged_decode_weights(q[i], k, v, table, cl, d ** -0.5, w, max_context=n,
+                                         k_new=new, v_new=new, row_ids=ids, decay=decay,
+                                         partition_blocks=pb, out=out[i], workspace=ws)
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return out, w, k
+
+    want = steps(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
     assert pkv.read_device_status() == 0
