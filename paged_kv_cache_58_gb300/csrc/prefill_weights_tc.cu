@@ -544,9 +544,13 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (PASS == 1) {
                 if (!mine) continue;
                 const int rho = tile * kTile + row;
+                // Rows that pad the request's last tile have a say in no vote (their sum is NaN from
+                // the start): what they look at is other requests' queries and whatever the last
+                // key tile's shared memory held, and a vote moves the references of its warp's rows.
+                const bool there = rho < it.q.rows;
                 const int lim = it.base + (rho >> a.group_shift);        // last key seen
                 const int least = it.base + ((tile * kTile) >> a.group_shift);
-                float m = 0.f, l = 0.f;
+                float m = 0.f, l = there ? 0.f : NAN;
                 for (int j = 0; j < it.nb; ++j, ++used) {
                     const int buf = wg + 2 * (used & 1);
                     if (!wait_bar(ctl, GM::S_FULL + buf, (used >> 1) & 1)) { ok = false; break; }
@@ -610,7 +614,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                     __syncwarp();
                     mbar_arrive_if(lane == 0, &bars[GM::S_FREE + buf]);
                 }
-                if (ok && rho < it.q.rows)
+                if (ok && there)
                     a.stats[((head * a.splits + it.chunk) * 2 + half) * a.rows_pad + rho] =
                         make_float2(m, l);
             } else {

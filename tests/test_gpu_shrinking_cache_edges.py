@@ -1,6 +1,7 @@
 """Corners of the operators around a shrinking cache that their own files do not reach: wide
 clusters over short rows, the rotation inside a differentiated program,
-decode steps that follow each other without a pause."""
+decode steps that follow each other without a pause, prompt
+weights whose bits must not depend on what ran before."""
 import pytest
 import torch
 
@@ -145,4 +146,39 @@ def test_decode_weights_steps_back_to_back(pkv, S, hkv, group, d, n, pb):
     want = steps(True)
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
+    assert pkv.read_device_status() == 0
+
+
+@pytest.mark.parametrize("reqs,d,hkv,group,new,n", [(50, 64, 4, 2, 40, 300), (50, 128, 4, 2, 40, 300),
+                                                    (2, 128, 4, 2, 40, 300), (70, 64, 2, 8, 9, 130),
+                                                    (9, 128, 8, 1, 200, 1000)])
+def test_prefill_weights_give_the_same_bits(pkv, reqs, d, hkv, group, new, n):
+    """Query and key tiles that end inside, so that rows and keys beyond them are whatever shared
+    memory held: the same call gives the same bits, whatever ran before it and whatever the
+    padding is."""
+    g = gen(52)
+    blocks = -(-n // 16)
+    kp = torch.randn(reqs * blocks, hkv, 16, d, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(reqs * blocks, generator=g, device="cuda").view(reqs, -1).to(torch.int32)
+    q = torch.randn(reqs * new, hkv * group, d, generator=g, device="cuda").bfloat16()
+    cached, news = i32([n - new] * reqs), i32([new] * reqs)
+    off = i32([new * i for i in range(reqs + 1)])
+
+    def call(q, kp):
+        w = torch.zeros(reqs, hkv, n, device="cuda")
+        pkv.paged_prefill_weights(q, kp, table, cached, news, off, d ** -0.5, w, max_new=new,
+                                  max_context=n)
+        return w
+
+    want = call(q, kp)
+    # wild values in tiles of another call, which stay behind in shared memory
+    wild = torch.where(torch.rand(kp.shape, generator=g, device="cuda") < 0.5, 1e30, -1e30).bfloat16()
+    for other in (None, wild, kp):
+        if other is not None:
+            call(q * 100, other)
+        for _ in range(8):
+            assert torch.equal(call(q, kp), want)
+    # the last request's neighbours are not its own: longer arrays, wild rows behind them
+    longer = torch.cat([q, torch.full_like(q[:new], 1e30)])
+    assert torch.equal(call(longer, kp), want)
     assert pkv.read_device_status() == 0
