@@ -259,6 +259,9 @@ struct PrefillWeightsArgs {
     int heads_per_launch;
     float scale_log2;
     float decay;
+    // Tensor cores, tests only: 1 or 2 makes the first wait of CTA 0 for that pass's A tiles run
+    // out of time (its barrier waits for 16 bytes more than the copies deliver).
+    int test_stall;
 };
 // fp32 pools, on the CUDA cores.
 cudaError_t launch_prefill_weights(const PrefillWeightsArgs& a, int head_dim, int group,

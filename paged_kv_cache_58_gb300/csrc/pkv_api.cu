@@ -164,6 +164,13 @@ int decode_test_stall() {
     return v != nullptr && std::strcmp(v, "1") == 0;
 }
 
+// PKV_TEST_PREFILL_WEIGHTS_STALL=1 or 2 does the same in that pass of the bf16 prompt weights
+// (read at each call; tests only).
+int prefill_weights_test_stall() {
+    const char* v = std::getenv("PKV_TEST_PREFILL_WEIGHTS_STALL");
+    return v == nullptr ? 0 : std::strcmp(v, "1") == 0 ? 1 : std::strcmp(v, "2") == 0 ? 2 : 0;
+}
+
 // PKV_TEST_CASCADE_SUFFIX_FAIL=1 makes the cascade decode report a failed suffix launch
 // (without launching it) after its prefix pass was forked onto the side stream, so that
 // tests reach that error path (read at each call; tests only).
@@ -1356,6 +1363,7 @@ pkv_status pkv_paged_prefill_weights(const pkv_pool_desc* pool, const void* q, c
     a.rows_pad = plan.rows_pad;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
     a.decay = decay;
+    a.test_stall = prefill_weights_test_stall();
     const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
     const cudaError_t e = pool->dtype == PKV_BF16
                               ? pkv::launch_prefill_weights_tc(a, pool->head_dim, group, st_)

@@ -263,15 +263,17 @@ PKV_DEVINL float sum8(const float (&v)[8]) {
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
-// The K boxes of one tile: lane b < nb copies 16-token chunk `chunk`, in block `phys`.
+// The K boxes of one tile: lane b < nb copies 16-token chunk `chunk`, in block `phys`.  `bar` waits
+// for more_bytes more than they are (see PrefillWeightsArgs::test_stall).
 template <int D>
 PKV_DEVINL void copy_k_boxes(const PrefillWeightsArgs& a, const void* tm_k, const Item& it,
-                             int chunk, int phys, int nb, uint8_t* dst, uint64_t* bar, int lane) {
+                             int chunk, int phys, int nb, uint8_t* dst, uint64_t* bar, int lane,
+                             int more_bytes = 0) {
     using GM = Geom<D>;
     const int csh = a.block_shift - 4;
     const int row = ((phys * a.num_kv_heads + it.kvh) << a.block_shift) +
                     (chunk & ((1 << csh) - 1)) * kChunk;
-    mbar_arrive_expect_tx_if(lane == 0, bar, nb * GM::kChunkBytes);
+    mbar_arrive_expect_tx_if(lane == 0, bar, nb * GM::kChunkBytes + more_bytes);
     __syncwarp();
     if constexpr (D == 128)
         tma_load_4d_if(lane < nb, dst + lane * GM::kChunkBytes, tm_k, 0, 0, 0, row / 8, bar);
@@ -387,10 +389,12 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (i >= 2 && !wait_bar(ctl, GM::A_EMPTY + s, ((i >> 1) - 1) & 1)) break;
             uint8_t* dst = smem + GM::kOffA + s * 2 * GM::kTileBytes;
             uint64_t* bar = &bars[GM::A_FULL + s];
+            // test hook: the first item's tiles are waited for in vain
+            const int stall = a.test_stall == PASS && i == 0 && blockIdx.x == 0 ? 16 : 0;
             if (PASS == 1) {
                 const int token = it.q.qoff + it.q.n - it.q.m + ((it.a0 * kTile) >> a.group_shift);
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, it.na * GM::kTileBytes);
+                    mbar_arrive_expect_tx(bar, it.na * GM::kTileBytes + stall);
                     for (int t = 0; t < it.na; ++t)
 #pragma unroll
                         for (int h = 0; h < GM::kHalves; ++h)
@@ -405,7 +409,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                 const int first = it.a0 * kBoxes;
                 const int n = min(2 * kBoxes, chunks - first);
                 const int phys = block_of(a, it, lane < n ? first + lane : chunks, chunks);
-                copy_k_boxes<D>(a, &tm_k, it, first + lane, phys, n, dst, bar, lane);
+                copy_k_boxes<D>(a, &tm_k, it, first + lane, phys, n, dst, bar, lane, stall);
             }
             ++issued;
         }
@@ -492,7 +496,8 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                 }
                 umma_commit_if(leader, &bars[GM::B_EMPTY + sb]);
             }
-            umma_commit_if(leader, &bars[GM::A_EMPTY + sa]);
+            // not after a wait that ran out: the place's copies may still be on their way
+            if (ok) umma_commit_if(leader, &bars[GM::A_EMPTY + sa]);
             ++i;
         }
         // every product has completed before the TMEM goes

@@ -1,7 +1,7 @@
 """Corners of the operators around a shrinking cache that their own files do not reach: wide
 clusters over short rows, the rotation inside a differentiated program,
 decode steps that follow each other without a pause, prompt
-weights whose bits must not depend on what ran before."""
+weights whose bits must not depend on what ran before, and whose waits run out."""
 import pytest
 import torch
 
@@ -181,4 +181,38 @@ def test_prefill_weights_give_the_same_bits(pkv, reqs, d, hkv, group, new, n):
     # the last request's neighbours are not its own: longer arrays, wild rows behind them
     longer = torch.cat([q, torch.full_like(q[:new], 1e30)])
     assert torch.equal(call(longer, kp), want)
+    assert pkv.read_device_status() == 0
+
+
+@pytest.mark.parametrize("stall", ["1", "2"])
+@pytest.mark.parametrize("reqs,d", [(2, 128), (50, 64)])   # an item a CTA; items from the counter
+def test_prefill_weights_after_a_timeout(pkv, monkeypatch, stall, reqs, d):
+    """A wait of either pass that runs out (its copies all land, but its barrier waits for 16
+    bytes more) is reported within a few seconds, and the next call is right."""
+    g = gen(51)
+    hkv, group, new, n = 4, 2, 40, 300
+    blocks = -(-n // 16)
+    kp = torch.randn(reqs * blocks, hkv, 16, d, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(reqs * blocks, generator=g, device="cuda").view(reqs, -1).to(torch.int32)
+    q = torch.randn(reqs * new, hkv * group, d, generator=g, device="cuda").bfloat16()
+    cached, news = i32([n - new] * reqs), i32([new] * reqs)
+    off = i32([new * i for i in range(reqs + 1)])
+    need = pkv.prefill_weights_workspace_bytes(kp, reqs, hkv * group, new, n)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def call():
+        w = torch.zeros(reqs, hkv, n, device="cuda")
+        pkv.paged_prefill_weights(q, kp, table, cached, news, off, d ** -0.5, w, max_new=new,
+                                  max_context=n, workspace=ws)
+        return w
+
+    want = call()
+    assert pkv.read_device_status() == 0
+    total = want.double().sum(-1)                       # each row's probabilities add up to 1
+    assert float((total - new * group).abs().max()) < 1e-3 * new * group
+    monkeypatch.setenv("PKV_TEST_PREFILL_WEIGHTS_STALL", stall)
+    call()
+    assert pkv.read_device_status() == 4
+    monkeypatch.delenv("PKV_TEST_PREFILL_WEIGHTS_STALL")
+    assert torch.equal(call(), want)
     assert pkv.read_device_status() == 0
