@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "prefill_weights.cuh"
 
 namespace pkv {
 
@@ -39,29 +40,6 @@ namespace {
 
 constexpr int kTile = 64;       // rows, and keys, of a score tile
 constexpr int kThreads = 256;   // 16 x 16 threads, 4 x 4 scores each
-
-// What a request asks for, checked; `rows` = 0: nothing to do.
-struct Request {
-    int n, c, m, rows, qoff, wrow;
-};
-PKV_DEVINL Request request_of(const PrefillWeightsArgs& a, int r, int group, bool report) {
-    Request q;
-    q.n = __ldg(a.new_lens + r);
-    q.c = __ldg(a.cached_lens + r);
-    q.qoff = __ldg(a.q_offsets + r);
-    q.wrow = a.row_ids ? __ldg(a.row_ids + r) : r;
-    q.m = a.window > 0 ? min(a.window, q.n) : q.n;
-    q.rows = 0;
-    if (q.n <= 0 || q.wrow < 0) return q;   // no new tokens, or a padding row
-    const int64_t L = static_cast<int64_t>(q.c) + q.n;
-    if (q.c < 0 || L > a.max_context || q.n > a.max_new || q.wrow >= a.num_rows || q.qoff < 0 ||
-        static_cast<int64_t>(q.qoff) + q.n > a.total_new) {
-        if (report) raise_status(a.status, PKV_ERR_OOB);
-        return q;
-    }
-    q.rows = q.m * group;
-    return q;
-}
 
 template <int D>
 struct Smem {

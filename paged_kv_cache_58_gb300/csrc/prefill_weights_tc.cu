@@ -51,6 +51,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "prefill_weights.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -123,29 +124,6 @@ PKV_DEVINL bool wait_bar(const Ctl& c, int idx, uint32_t parity) {
     }
 }
 
-// Request r's window, or rows = 0: nothing to do (or out of range, which is reported).
-struct Request {
-    int n, c, m, rows, qoff, wrow;
-};
-PKV_DEVINL Request request_of(const PrefillWeightsArgs& a, int r, bool report) {
-    Request q;
-    q.n = __ldg(a.new_lens + r);
-    q.c = __ldg(a.cached_lens + r);
-    q.qoff = __ldg(a.q_offsets + r);
-    q.wrow = a.row_ids ? __ldg(a.row_ids + r) : r;
-    q.m = a.window > 0 ? min(a.window, q.n) : q.n;
-    q.rows = 0;
-    if (q.n <= 0 || q.wrow < 0) return q;
-    if (q.c < 0 || static_cast<int64_t>(q.c) + q.n > a.max_context || q.n > a.max_new ||
-        q.wrow >= a.num_rows || q.qoff < 0 ||
-        static_cast<int64_t>(q.qoff) + q.n > a.total_new) {
-        if (report) raise_status(a.status, PKV_ERR_OOB);
-        return q;
-    }
-    q.rows = q.m << a.group_shift;
-    return q;
-}
-
 PKV_DEVINL int ceil_div(int x, int y) { return (x + y - 1) / y; }
 
 // One item: A tiles a0, a0 + 1 (na of them) against B tiles [b0, b0 + nb), which are those of
@@ -211,7 +189,7 @@ struct Walk {
             if (k >= off[a.num_reqs]) return false;
             while (off[r + 1] <= k) ++r;
             it.r = r;
-            it.q = request_of(a, r, false);
+            it.q = request_of(a, r, 1 << a.group_shift, false);
             it.base = it.q.c + it.q.n - it.q.m;
             const int keys = it.q.c + it.q.n;
             int rem = k - off[r];
@@ -353,7 +331,8 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
         for (int r0 = 0; r0 < a.num_reqs; r0 += 32) {
             int n = 0;
             if (r0 + lane < a.num_reqs) {
-                const Request q = request_of(a, r0 + lane, PASS == 1 && blockIdx.x == 0);
+                const Request q = request_of(a, r0 + lane, 1 << a.group_shift,
+                                             PASS == 1 && blockIdx.x == 0);
                 if (q.rows > 0) {
                     const int key_tiles = ceil_div(q.c + q.n, kTile);
                     n = PASS == 1 ? (ceil_div(q.rows, kTile) + 1) / 2 *
@@ -746,7 +725,7 @@ merge_stats_kernel(const PrefillWeightsArgs a) {
     griddep_wait();
     griddep_launch_dependents();
     const int rho = blockIdx.x * 128 + threadIdx.x;
-    const Request q = request_of(a, blockIdx.z, false);
+    const Request q = request_of(a, blockIdx.z, 1 << a.group_shift, false);
     if (q.rows == 0 || blockIdx.x * 128 >= q.rows) return;
     const size_t head = static_cast<size_t>(blockIdx.z) * a.num_kv_heads + blockIdx.y;
     float neg = -INFINITY;
