@@ -586,9 +586,9 @@ cudaError_t launch_f(const EvictArgs& a, int C, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-    // CTAs per row: enough that a slice has at most 16384 entries (128 rows of 16k to 128k: 256
-    // us, 269 with slices of 32768, before the scans counted as they do now), and that about two CTAs per SM exist where there are few
-    // rows.  More where rows fill the SMs only adds cluster barriers (512 rows with two each: a
+    // CTAs per row: enough that a slice has at most 16384 entries (128 rows of 16k to 128k: 241 us,
+    // 247 with slices of 32768, 241 with 8192; 512 rows of 16k to 20k: 364, 375 and 361), and that
+    // about two CTAs per SM exist where there are few rows.  More where rows fill the SMs only adds cluster barriers (512 rows with two each: a
     // block of 64 took 39 us against 15.6, 512 to 4096 entries 76 against 72).
     // Entries in flight per thread: four in a CTA that has its row alone (eight: 12.2 and 67.2 us
     // against 11.4 and 66.3), eight where clusters scan long rows (four 243.5 us, sixteen 258,

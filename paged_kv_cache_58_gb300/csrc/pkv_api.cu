@@ -1214,6 +1214,9 @@ struct PrefillWeightsPlan {
 };
 // What the kept scores of one launch may take (fp32): as many (request, kv head) pairs as fit
 // kScoreBytes, or one alone that fits kScoreMost.  A larger one has its scores computed twice.
+// Both bound a caller's workspace rather than the time.  16 pairs of 32 MB, D 64: 839 us for the
+// call with a share of 64 MB, 783 with 256, 727 with 1 GB; 16 pairs of 128 MB, D 128: 5.13, 5.23
+// and 4.85 ms; computed twice 1071 us and 7.61 ms, and one pair of 512 MB 2.11 ms for 1.30.
 constexpr int64_t kScoreBytes = int64_t{256} << 20, kScoreMost = int64_t{1} << 30;
 constexpr size_t kCounterBytes = 16;   // at the start of the workspace
 bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_heads, int max_new,
@@ -1247,19 +1250,23 @@ bool prefill_weights_plan(const pkv_pool_desc* pool, int num_reqs, int num_q_hea
         p->splits = static_cast<int>(std::min<int64_t>(
             std::min<int64_t>(std::max<int64_t>(304 / ctas, 1), ceil_div(max_context, 64)), 32));
     } else {
-        // Tensor cores: parts of 24 tiles of 128 keys (16 x 512 tokens, 32 heads: 582 us for the
-        // call, 594 with 16, 609 with 8, before pass 1 was balanced), shorter, down to 4, where there would be fewer than
-        // one item per SM, and at most 32 of them.  One request, its last 64 of 512 tokens after
-        // 8k, 32 heads on 8: 30.6 us; 55 with parts of 2, more than an item per SM, whose own
-        // first tiles and statistics count; 500 tokens after 2k, 8 heads on 1: 30.9 and 44.  The
-        // lengths are not known here, only their bound.
+        // Tensor cores: parts of 24 tiles of 128 keys, shorter, down to 4, where there would be
+        // fewer than one item per SM, and at most 32 of them: an item's own first tiles and
+        // statistics count for more than evener CTAs.  The call with parts of
+        //                                            32     24     16     12      8      6
+        // 16 x 512 tokens, 32 heads, to 8k: us      559    553    562    567    583    599
+        // their last 64 tokens                    128.0  115.1  119.1  119.6  120.5  123.6
+        // 4 x 512 tokens                          220.9  199.9  202.7  200.9  205.7  214.7
+        // The lengths are not known here, only their bound.
         const int64_t items = heads * ((row_tiles + 1) / 2);
         p->chunk_tiles = static_cast<int>(
             std::max<int64_t>(4, std::min<int64_t>(24, (items * tiles + 151) / 152)));
         p->chunk_tiles = std::max(p->chunk_tiles, ceil_div(tiles, 32));
         p->splits = ceil_div(tiles, p->chunk_tiles);
     }
-    // Pass 2: parts of the rows, of two tiles of 128 at least, up to two items per SM.
+    // Pass 2: parts of the rows, of two tiles of 128 at least, up to two items per SM.  500 tokens
+    // after 2k, 8 heads on 1, fp32: 126 us with up to one item per SM, 108 with two, 103 with four;
+    // bf16 26.9, 30.4 and 30.3.
     const int64_t items2 = static_cast<int64_t>(p->heads_per_launch) *
                            (f32 ? ceil_div(max_context, 64) : (tiles + 1) / 2);
     const int most = std::min(16, std::max(1, row_tiles / 2));

@@ -18,7 +18,7 @@
 // exponentials 512 cycles at 32 a cycle, and its operands are read from shared memory at 128
 // bytes a cycle, all there is, so that the copies' writes (32 KB per B tile) and pass 2's
 // reads of -lse slow the products down.  On the 16 x 512-token batch (every new token, 3.2e11
-// flop a pass) the two passes take 265 and 288 us; pass 1 took 285 before its items were
+// flop a pass) the two passes take 260 and 287 us; pass 1 took 285 before its items were
 // balanced, 250 without exponentials and 240 with its products alone.  Measured there and not
 // kept, when the call took 596 us: four A tiles per B tile with one TMEM buffer each (half the
 // copies): 653 us; B tiles of 256, whose products read 96 bytes a cycle, with one TMEM buffer
@@ -41,7 +41,7 @@
 // Persistent CTAs, one per SM: producers run ahead into the next item's tiles while the
 // consumers finish the current one.  Pass 1's items differ in length (the last chunk of keys,
 // the causal edge), and every gridDim.x-th item to a CTA left the longest with a quarter more
-// than the mean; taken from a shared counter, the call went from 590 to 555 us.  Pass 2's are
+// than the mean; taken from a shared counter, the call went from 590 to 552 us.  Pass 2's are
 // many and alike: every gridDim.x-th.  Roles: warps 0-15 consumers, warp 16 A tiles, warp 17 B
 // tiles, warp 18 MMA and TMEM, warp 19 the B rows' -lse (pass 2).
 #include <atomic>

@@ -8,12 +8,15 @@
 //
 // Angles without rounding trouble at far positions: only the angle modulo one turn
 // matters, and positions are integers.  inv_freq[i] / (2 pi) becomes a 64-bit binary
-// fraction of a turn once; its product with the position modulo 2^64 is the angle's
-// fraction of a turn, exactly, whatever the position (the fraction's own rounding, at
-// most 2^-54 of a turn, times a position below 2^31 stays under 2^-23 of a turn at the
-// very end of that range and under 2^-33 at 2^20).  The top two bits after rounding
-// are the quadrant; the rest, within an eighth of a turn, goes through sincospif.  No
-// 64-bit floating point is spent per position, which this GPU runs at 1/60 of fp32.
+// fraction of a turn; its product with the position modulo 2^64 is the angle's fraction
+// of a turn, exactly, whatever the position.  The fraction's own rounding, at most 2^-54 of
+// a turn for frequencies up to one radian a position and in proportion above that, times a
+// position below 2^31 stays under 2^-23 of a turn at the very end of that range and under
+// 2^-33 at 2^20.  The top two bits after rounding are the quadrant; the rest, within an
+// eighth of a turn, goes through sincospif.  The fraction is made anew for each (token,
+// pair): five operations in fp64, which this GPU runs at 1/60 of fp32.  At 8192 tokens of 64
+// pairs they keep the fp64 pipes busy for some 4 us of the 37 that the rows take (6.5 % of an
+// fp32 call's 65 us); the sine, the cosine and the reduction of the angle need none.
 //
 // Work split: a CTA takes TT consecutive tokens.  It computes each (token, pair) angle
 // once, into shared memory, and a thread then keeps the cosines and sines of its
