@@ -366,8 +366,8 @@ pkv_status pkv_copy_blocks(const pkv_pool_desc* pool, void* k_pool, void* v_pool
  *
  * pkv_rope_frequencies fills host inv_freq[rotary_dim / 2] with theta^(-2 i / rotary_dim),
  * scaled for contexts longer than the trained one as `scaling` says (NULL: plain), and
- * *attn_scale (may be NULL) with the scale that goes with it (1, or for PKV_ROPE_YARN
- * 0.1 ln(factor) + 1).  rotary_dim even, theta > 0, factor >= 1, 0 <= low < high,
+ * *attn_scale (may be NULL) with the scale that goes with it (1, or for both YaRN
+ * kinds 0.1 ln(factor) + 1).  rotary_dim even, theta > 0, factor >= 1, 0 <= low < high,
  * original_context > 0: PKV_ERR_INVALID otherwise.  With n_i = original_context * f_i /
  * (2 pi) turns over the trained context, PKV_ROPE_LLAMA3 and PKV_ROPE_YARN divide a
  * frequency by `factor` where n_i <= low, keep it where n_i >= high, and blend the two
