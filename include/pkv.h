@@ -517,6 +517,96 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
                      const int32_t* row_ids, int num_rows, int32_t* new_lens, void* workspace,
                      size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- quantised cache
+ * A paged cache whose rows are held in 8 or 4 bits, beside or in place of a pool: the same
+ * blocks, slots and tables (and so the same allocator, prefix cache and radix tree), at about
+ * a half or 0.29 of bf16's bytes (head_dim 128: 129 or 73 bytes a row, bf16 256).
+ *
+ * A row x of D elements (one token, one kv head, K or V) has an exponent e, the least in
+ * -90 .. 90 for which no element is beyond the format's largest value times 2^e.
+ *   PKV_FP8: x_i = code_i 2^e, code_i the e4m3 value nearest to x_i 2^-e (largest 448).
+ *   PKV_FP4: x_i = code_i s 2^e with an e4m3 scale s for each 16 elements, the nearest to a sixth
+ *            of their largest magnitude times 2^-e; code_i the e2m1 value nearest to
+ *            x_i 2^-e / s (largest value 6 * 448).
+ * Ties go to the even code; a magnitude beyond the largest value, an infinity among them, takes
+ * it.  A NaN stays one (fp4: so do the other 15 elements that share its scale).  x_i 2^-e is
+ * exact, so a code rounds once.  A row's values are relative to its own largest element: off by
+ * 2^-4 of themselves at most in fp8 (rows' smallest elements, below 2^-6 in the code, by 2^-10 of
+ * the unit 2^e).
+ *
+ * Layout.  Device pointers, 16-byte aligned, each array its own:
+ *   k_codes, v_codes   [num_blocks][num_kv_heads][block_size][D] e4m3 bytes, or [D / 2] pairs of
+ *                      e2m1 (element 2 i in byte i's low half).
+ *   k_scales, v_scales [num_blocks][num_kv_heads][block_size / 16] runs of, for PKV_FP4, the D
+ *                      scales of 16 tokens (K: [16 tokens][D / 16]; V: [4][D / 16][4 tokens],
+ *                      token 4 a + b at [a][.][b]), then 16 exponents as e + 127.
+ * Memory of a slot that was never written may hold anything.
+ * block_size 16 or 32, head_dim 64 or 128, num_blocks * num_kv_heads * block_size below 2^31
+ * (PKV_ERR_UNSUPPORTED otherwise).  Rows outside the cache are fp32 or bf16 (`dtype`). */
+typedef enum pkv_quant_format { PKV_FP8 = 0, PKV_FP4 = 1 } pkv_quant_format;
+typedef struct pkv_quant_cache {
+    int64_t num_blocks;
+    int32_t block_size, num_kv_heads, head_dim;
+    int32_t format; /* pkv_quant_format */
+    void *k_codes, *v_codes, *k_scales, *v_scales;
+} pkv_quant_cache;
+
+/* Bytes of k_codes (and of v_codes), and of k_scales; 0 for an invalid description.  The
+ * pointers are not looked at. */
+uint64_t pkv_quant_codes_bytes(const pkv_quant_cache* cache);
+uint64_t pkv_quant_scales_bytes(const pkv_quant_cache* cache);
+
+/* New tokens' rows, quantised into their slots: pkv_kv_append for a quantised cache.
+ *   slot_mapping  device int64 [num_tokens], as pkv_kv_append; no two tokens with the same.
+ *   k, v          device [num_tokens][num_kv_heads][head_dim] of `dtype`, 16-byte aligned; token
+ *                 t's heads start at element t * stride (a multiple of 16 bytes; heads of a
+ *                 token contiguous), so a slice of a fused projection is read in place.
+ * num_tokens * num_kv_heads below 2^31. */
+pkv_status pkv_kv_append_quant(const pkv_quant_cache* cache, const int64_t* slot_mapping,
+                               int dtype, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int64_t num_tokens, void* stream);
+
+/* Rows read back by slot: k_out, v_out as k, v above (strides >= num_kv_heads * head_dim),
+ * rounded to bf16 where that is their type (exact, within bf16's range).  A negative slot reads
+ * zeros; one past the cache does too and raises PKV_ERR_OOB in the device status word. */
+pkv_status pkv_kv_read_quant(const pkv_quant_cache* cache, const int64_t* slot_mapping, int dtype,
+                             void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                             int64_t num_tokens, void* stream);
+
+/* Whole blocks between a pool and the cache: a finished prompt's blocks move into the quantised
+ * cache, a cached prefix comes back into a pool for pkv_paged_prefill, which reads every key many
+ * times.  Every row of a block is moved, also ones never written.
+ *   pool   k_pool / v_pool's description; block_size, num_kv_heads and head_dim as the cache's.
+ *   pairs  device int32 [num_pairs][2] = (source block, destination block); destinations distinct.
+ * An id outside its own side's blocks skips that pair and raises PKV_ERR_OOB in the device status
+ * word.  num_pairs * num_kv_heads * block_size below 2^31. */
+pkv_status pkv_quantize_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
+                               const void* k_pool, const void* v_pool, const int32_t* pairs,
+                               int num_pairs, void* stream);
+pkv_status pkv_dequantize_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
+                                 void* k_pool, void* v_pool, const int32_t* pairs, int num_pairs,
+                                 void* stream);
+
+/* pkv_copy_blocks within a quantised cache (codes and scales). */
+pkv_status pkv_copy_blocks_quant(const pkv_quant_cache* cache, const int32_t* pairs,
+                                 int num_pairs, void* stream);
+
+/* pkv_paged_decode (k_new and v_new NULL) or pkv_paged_decode_append (both given) over a
+ * quantised cache: q, out, k_new and v_new are of `dtype`, the new tokens' rows are quantised as
+ * pkv_kv_append_quant does, into the slots the block tables give for them, and attended as they
+ * come back from there.  Attention is over the rows as held, in fp16 products that represent them
+ * exactly and fp32 sums; bf16: weights of 11 digits or more, fp32: of 22.  Other arguments, limits, errors and
+ * the workspace as pkv_paged_decode; workspace_bytes of the call's own. */
+size_t pkv_paged_decode_quant_workspace_bytes(const pkv_quant_cache* cache, int num_seqs,
+                                              int num_q_heads, int max_context,
+                                              int partition_blocks);
+pkv_status pkv_paged_decode_quant(const pkv_quant_cache* cache, int dtype, void* out, const void* q,
+                                  const void* k_new, const void* v_new,
+                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* context_lens, int max_context, int num_seqs,
+                                  int num_q_heads, float scale, int partition_blocks,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- device status
  * Synchronises `stream`, returns in *status_out the first error any kernel of this
  * library raised on the current device since the last read (PKV_OK if none), and

@@ -60,6 +60,15 @@ class RopeScaling(ctypes.Structure):
                 ("high", ctypes.c_double), ("original_context", ctypes.c_double)]
 
 
+class QuantCacheDesc(ctypes.Structure):
+    """A quantised cache: sizes, format and the four arrays (pkv_quant_cache)."""
+    _fields_ = [("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("k_codes", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -176,6 +185,26 @@ def _load():
     lib.pkv_evict.restype = ci
     lib.pkv_evict.argtypes = [P(PoolDesc), vp, vp, vp, ci, vp, ci, ci, vp, ci, ci, vp, vp, vp, vp,
                               vp, vp, i64, vp, ci, vp, vp, sz, vp]
+    QC = P(QuantCacheDesc)
+    lib.pkv_quant_codes_bytes.restype = ctypes.c_uint64
+    lib.pkv_quant_codes_bytes.argtypes = [QC]
+    lib.pkv_quant_scales_bytes.restype = ctypes.c_uint64
+    lib.pkv_quant_scales_bytes.argtypes = [QC]
+    lib.pkv_kv_append_quant.restype = ci
+    lib.pkv_kv_append_quant.argtypes = [QC, vp, ci, vp, i64, vp, i64, i64, vp]
+    lib.pkv_kv_read_quant.restype = ci
+    lib.pkv_kv_read_quant.argtypes = [QC, vp, ci, vp, i64, vp, i64, i64, vp]
+    lib.pkv_quantize_blocks.restype = ci
+    lib.pkv_quantize_blocks.argtypes = [QC, P(PoolDesc), vp, vp, vp, ci, vp]
+    lib.pkv_dequantize_blocks.restype = ci
+    lib.pkv_dequantize_blocks.argtypes = [QC, P(PoolDesc), vp, vp, vp, ci, vp]
+    lib.pkv_copy_blocks_quant.restype = ci
+    lib.pkv_copy_blocks_quant.argtypes = [QC, vp, ci, vp]
+    lib.pkv_paged_decode_quant_workspace_bytes.restype = sz
+    lib.pkv_paged_decode_quant_workspace_bytes.argtypes = [QC] + [ci] * 4
+    lib.pkv_paged_decode_quant.restype = ci
+    lib.pkv_paged_decode_quant.argtypes = [QC, ci, vp, vp, vp, vp, vp, ci, vp, ci, ci, ci, f32, ci,
+                                           vp, sz, vp]
     lib.pkv_alloc_privatize.restype = ci
     lib.pkv_alloc_privatize.argtypes = [vp, i64, i64, P(i32), ci, P(ci)]
     lib.pkv_alloc_truncate.restype = ci
@@ -893,6 +922,175 @@ def evict(k_pool, v_pool, block_tables, context_lens, budgets, weights, position
     if st != 0:
         raise PkvError("pkv_evict", st)
     return new_lens
+
+
+QUANT_FORMATS = {"fp8": 0, "fp4": 1}
+
+
+class QuantCache:
+    """A paged cache whose rows are held in 8 or 4 bits (pkv_quant_cache): the blocks, slots and
+    tables of a pool, codes and scales in place of its rows.
+
+    `format` "fp8": e4m3 codes and a power of two per row; "fp4": e2m1 codes with an e4m3 scale
+    per 16 elements, and a power of two per row.  k, v: uint8 [num_blocks, Hkv, B, D] (fp4:
+    [..., D / 2]); k_scales, v_scales: uint8 [num_blocks, Hkv, B], fp4 [num_blocks, Hkv,
+    B / 16 * (D + 16)].  QuantCache.empty makes them; given ones are held, not copied.  Its memory
+    need not be cleared: slots that were never written are not looked at."""
+
+    def __init__(self, k, v, k_scales, v_scales, *, format="fp8"):
+        if format not in QUANT_FORMATS:
+            raise ValueError(f"format must be one of {list(QUANT_FORMATS)}")
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be [num_blocks, num_kv_heads, block_size, bytes of a row]")
+        dev = k.get_device()
+        if dev < 0:
+            raise ValueError("k must be a CUDA tensor")
+        nb, hkv, block, row = k.shape
+        dim = row if format == "fp8" else 2 * row
+        beside = (nb, hkv, block // 16 * (16 if format == "fp8" else dim + 16))
+        u8 = torch.uint8
+        self.desc = QuantCacheDesc(nb, block, hkv, dim, QUANT_FORMATS[format],
+                                   _arg(k, "k", dev, u8, k.shape), _arg(v, "v", dev, u8, k.shape),
+                                   _arg(k_scales, "k_scales", dev, u8, beside),
+                                   _arg(v_scales, "v_scales", dev, u8, beside))
+        if not _load().pkv_quant_codes_bytes(ctypes.byref(self.desc)):
+            raise ValueError("a quantised cache has blocks of 16 or 32 tokens and heads of 64 or "
+                             "128, fewer than 2^31 rows in all")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.format, self.device = format, dev
+        self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim = nb, hkv, block, dim
+        self._ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, num_blocks, num_kv_heads, head_dim, *, block_size=BLOCK_SIZE, format="fp8",
+              device="cuda"):
+        """A cache of `num_blocks` blocks, not initialised."""
+        if format not in QUANT_FORMATS:
+            raise ValueError(f"format must be one of {list(QUANT_FORMATS)}")
+        row = head_dim if format == "fp8" else head_dim // 2
+        beside = block_size // 16 * (16 if format == "fp8" else head_dim + 16)
+        k, v = (torch.empty((num_blocks, num_kv_heads, block_size, row), dtype=torch.uint8,
+                            device=device) for _ in range(2))
+        ks, vs = (torch.empty((num_blocks, num_kv_heads, beside), dtype=torch.uint8,
+                              device=device) for _ in range(2))
+        return cls(k, v, ks, vs, format=format)
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes of the four arrays."""
+        return 2 * (self.k.numel() + self.k_scales.numel())
+
+
+def _quant(cache):
+    """(pointer to the description, device) of a quantised cache on the current device."""
+    dev = cache.device
+    if dev != _cur_device():
+        raise ValueError(f"the cache is on cuda:{dev}, not on the current device")
+    return cache._ref, dev
+
+
+def kv_append_quant(cache, slot_mapping, k, v, stream=None) -> None:
+    """Quantise k / v [T, Hkv, D] (bf16 or fp32) into their slots of a QuantCache (slot < 0 =
+    skip).  k and v may be slices of a fused projection: tokens any multiple of 16 bytes apart.
+    As with every call that writes the cache, no gradient flows."""
+    c, dev = _quant(cache)
+    T, dt = k.shape[0], k.dtype
+    shape = (T, cache.num_kv_heads, cache.head_dim)
+    kp, ks = _rows_arg(k, "k", dev, dt, shape)
+    vp_, vs = _rows_arg(v, "v", dev, dt, shape)
+    st = _load().pkv_kv_append_quant(c, _arg(slot_mapping, "slot_mapping", dev, torch.int64, (T,)),
+                                     _dtype_code(k), kp, ks, vp_, vs, T, _stream_on(stream, dev))
+    if st != 0:
+        raise PkvError("pkv_kv_append_quant", st)
+
+
+def kv_read_quant(cache, slot_mapping, *, dtype=torch.bfloat16, k_out=None, v_out=None,
+                  stream=None):
+    """Rows of the slots [T] of a QuantCache, (k, v) [T, Hkv, D] of `dtype` (or into k_out and
+    v_out, of their type; tokens may be apart as in kv_append_quant).  A negative slot reads
+    zeros."""
+    c, dev = _quant(cache)
+    T = slot_mapping.shape[0]
+    shape = (T, cache.num_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = _fresh(shape, dtype if v_out is None else v_out.dtype, dev, stream)
+    if v_out is None:
+        v_out = _fresh(shape, k_out.dtype, dev, stream)
+    kp, ks = _rows_arg(k_out, "k_out", dev, k_out.dtype, shape)
+    vp_, vs = _rows_arg(v_out, "v_out", dev, k_out.dtype, shape)
+    st = _load().pkv_kv_read_quant(c, _arg(slot_mapping, "slot_mapping", dev, torch.int64, (T,)),
+                                   _dtype_code(k_out), kp, ks, vp_, vs, T, _stream_on(stream, dev))
+    if st != 0:
+        raise PkvError("pkv_kv_read_quant", st)
+    return k_out, v_out
+
+
+def quantize_blocks(cache, k_pool, v_pool, pairs, stream=None) -> None:
+    """Quantise whole blocks of a pool into a QuantCache: cache[dst] = pool[src] for each (src,
+    dst) of pairs (int32 [n, 2])."""
+    _move_blocks("pkv_quantize_blocks", cache, k_pool, v_pool, pairs, stream)
+
+
+def dequantize_blocks(cache, k_pool, v_pool, pairs, stream=None) -> None:
+    """Read whole blocks of a QuantCache into a pool: pool[dst] = cache[src] for each (src, dst)
+    of pairs (int32 [n, 2]).  A prefix read back so is what paged_prefill attends to."""
+    _move_blocks("pkv_dequantize_blocks", cache, k_pool, v_pool, pairs, stream)
+
+
+def _move_blocks(fn, cache, k_pool, v_pool, pairs, stream):
+    c, dev = _quant(cache)
+    d, _, kp, vp_ = _pools(k_pool, v_pool)
+    st = getattr(_load(), fn)(c, ctypes.byref(d), kp, vp_,
+                              _arg(pairs, "pairs", dev, torch.int32, (pairs.shape[0], 2)),
+                              pairs.shape[0], _stream_on(stream, dev))
+    if st != 0:
+        raise PkvError(fn, st)
+
+
+def copy_blocks_quant(cache, pairs, stream=None) -> None:
+    """copy_blocks within a QuantCache: block dst = block src for each (src, dst) of pairs (int32
+    [n, 2]; the allocator's copy-on-write pairs)."""
+    c, dev = _quant(cache)
+    st = _load().pkv_copy_blocks_quant(c, _arg(pairs, "pairs", dev, torch.int32,
+                                               (pairs.shape[0], 2)), pairs.shape[0],
+                                       _stream_on(stream, dev))
+    if st != 0:
+        raise PkvError("pkv_copy_blocks_quant", st)
+
+
+def decode_quant_workspace_bytes(cache, num_seqs, num_q_heads, max_context,
+                                 partition_blocks=0) -> int:
+    """Workspace of paged_decode_quant."""
+    return int(_load().pkv_paged_decode_quant_workspace_bytes(
+        cache._ref, num_seqs, num_q_heads, max_context, partition_blocks))
+
+
+def paged_decode_quant(q, cache, block_tables, context_lens, scale, *, max_context, k_new=None,
+                       v_new=None, out=None, partition_blocks=0, workspace=None, stream=None):
+    """paged_decode over a QuantCache: q [S, Hq, D] (bf16 or fp32) -> out [S, Hq, D].  With k_new
+    / v_new [S, Hkv, D], the rows of each sequence's token context_lens[s] - 1, they are quantised
+    into the slots the block tables give for them first, in the same launch, and attended as
+    they come back from there."""
+    c, dev = _quant(cache)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [num_seqs, heads, head_dim], block_tables [num_seqs, blocks]")
+    S, Hq, _ = q.shape
+    dt, D = q.dtype, cache.head_dim
+    new = (S, cache.num_kv_heads, D)
+    if out is None:
+        out = _fresh((S, Hq, D), dt, dev, stream)
+    _, ws, wsb = _keep = _workspace_arg(
+        workspace, lambda: decode_quant_workspace_bytes(cache, S, Hq, max_context,
+                                                        partition_blocks), dev, stream)
+    st = _load().pkv_paged_decode_quant(
+        c, _dtype_code(q), _arg(out, "out", dev, dt, (S, Hq, D)), _arg(q, "q", dev, dt, (S, Hq, D)),
+        _opt(k_new, "k_new", dev, dt, new), _opt(v_new, "v_new", dev, dt, new),
+        _arg(block_tables, "block_tables", dev, torch.int32, (S, block_tables.shape[1])),
+        block_tables.shape[1], _arg(context_lens, "context_lens", dev, torch.int32, (S,)),
+        max_context, S, Hq, scale, partition_blocks, ws, wsb, _stream_on(stream, dev))
+    if st != 0:
+        raise PkvError("pkv_paged_decode_quant", st)
+    return out
 
 
 def copy_blocks(k_pool, v_pool, pairs, stream=None) -> None:

@@ -132,6 +132,9 @@ bool make_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int head_dim)
 // 2 column halves, rows / 8 row groups}, box {64, 8, 2, 2} = 4 KB, landing in shared
 // memory as [row group][half][8 rows][128 B] with the 128-byte swizzle.
 bool make_pool_block_map(CUtensorMap* m, const void* pool, int64_t rows);
+// The codes of a quantised cache: rows of row_bytes (128, 64 or 32), box 16 rows, swizzled over
+// the length of a row.
+bool make_codes_map(CUtensorMap* m, const void* codes, int64_t rows, int row_bytes);
 // cudaFuncSetAttribute(kern, MaxDynamicSharedMemorySize, bytes), made once per kernel and
 // device (later calls with no more bytes return at once).
 cudaError_t set_smem_once(const void* kern, int bytes);
@@ -305,5 +308,32 @@ struct EvictArgs {
     int recent;
 };
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+
+// Rows and blocks in and out of a quantised cache (quant_cache.cu).
+struct QuantArgs {
+    uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+    const void *k, *v;       // rows or blocks to quantise
+    void *k_out, *v_out;     // rows or blocks to read back into
+    const int64_t* slots;    // rows: each token's slot
+    const int32_t* pairs;    // blocks: (source, destination)
+    int* status;
+    int64_t num_slots, num_blocks, pool_blocks;
+    int64_t k_stride, v_stride;   // rows: elements between tokens
+    uint32_t num_rows;            // rows of K (and of V) in all
+    int num_kv_heads;
+    int block_shift;              // log2 of the block size
+};
+// `blocks`: by pairs, else by slot; `read`: out of the cache, else into it.
+cudaError_t launch_quant_move(const QuantArgs& a, int format, int head_dim, int dtype, bool blocks,
+                              bool read, cudaStream_t stream);
+// Whole blocks of the cache copied within it; bytes of a block's codes and of what lies beside.
+cudaError_t launch_quant_copy(const QuantArgs& a, int num_pairs, int64_t code_bytes,
+                              int64_t side_bytes, cudaStream_t stream);
+// Decode over a quantised cache: DecodeArgs' pools are the codes; `k`, `v` lie beside them.
+struct QuantSides {
+    uint8_t *k, *v;
+};
+cudaError_t launch_quant_decode(const DecodeArgs& a, const QuantSides& sides, int format, int dtype,
+                                int head_dim, int group, cudaStream_t stream);
 
 }  // namespace pkv

@@ -1472,6 +1472,264 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
     return from_cuda(pkv::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- quantised cache
+
+namespace {
+
+pkv_status check_quant(const pkv_quant_cache* c) {
+    if (!c || c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0 || c->block_size <= 0)
+        return PKV_ERR_INVALID;
+    if (c->format != PKV_FP8 && c->format != PKV_FP4) return PKV_ERR_UNSUPPORTED;
+    if (chunk_shift(c->block_size) < 0) return PKV_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (c->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    // a row's index is a TMA coordinate
+    if (c->num_blocks > INT32_MAX / (static_cast<int64_t>(c->num_kv_heads) * c->block_size))
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// Bytes of a block's codes (K or V, all kv heads), and of what lies beside them.
+int64_t quant_code_bytes(const pkv_quant_cache* c) {
+    const int64_t rows = static_cast<int64_t>(c->num_kv_heads) * c->block_size;
+    return rows * (c->format == PKV_FP8 ? c->head_dim : c->head_dim / 2);
+}
+int64_t quant_side_bytes(const pkv_quant_cache* c) {
+    const int64_t runs = static_cast<int64_t>(c->num_kv_heads) * (c->block_size / 16);
+    return runs * (c->format == PKV_FP8 ? 16 : c->head_dim + 16);
+}
+
+// The four arrays, present and aligned.
+bool quant_arrays_ok(const pkv_quant_cache* c) {
+    return c->k_codes && c->v_codes && c->k_scales && c->v_scales && aligned16(c->k_codes) &&
+           aligned16(c->v_codes) && aligned16(c->k_scales) && aligned16(c->v_scales);
+}
+
+pkv::QuantArgs quant_args(const pkv_quant_cache* c, int* status) {
+    pkv::QuantArgs a{};
+    a.k_codes = static_cast<uint8_t*>(c->k_codes);
+    a.v_codes = static_cast<uint8_t*>(c->v_codes);
+    a.k_scales = static_cast<uint8_t*>(c->k_scales);
+    a.v_scales = static_cast<uint8_t*>(c->v_scales);
+    a.status = status;
+    a.num_blocks = c->num_blocks;
+    a.num_slots = c->num_blocks * c->block_size;
+    a.num_kv_heads = c->num_kv_heads;
+    a.block_shift = block_shift(c->block_size);
+    return a;
+}
+
+// pkv_kv_append_quant, and with `read` pkv_kv_read_quant.
+pkv_status quant_rows(const pkv_quant_cache* cache, const int64_t* slot_mapping, int dtype,
+                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      int64_t num_tokens, bool read, void* stream) {
+    pkv_status st = check_quant(cache);
+    if (st != PKV_OK) return st;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens < 0) return PKV_ERR_INVALID;
+    if (num_tokens == 0) return PKV_OK;
+    if (num_tokens > INT32_MAX / cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+    if (!quant_arrays_ok(cache) || !slot_mapping || !k || !v || !aligned16(k) || !aligned16(v) ||
+        !aligned8(slot_mapping))
+        return PKV_ERR_INVALID;
+    const int es = elem_bytes(dtype);
+    const int64_t row = static_cast<int64_t>(cache->num_kv_heads) * cache->head_dim;
+    if (!stride_ok(k_stride, read ? row : 0, es) || !stride_ok(v_stride, read ? row : 0, es))
+        return PKV_ERR_INVALID;
+    if (read && !rows_apart({k, k_stride * es, row * es}, {v, v_stride * es, row * es}, num_tokens))
+        return PKV_ERR_INVALID;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::QuantArgs a = quant_args(cache, status);
+    a.k = k;
+    a.v = v;
+    a.k_out = const_cast<void*>(k);
+    a.v_out = const_cast<void*>(v);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.slots = slot_mapping;
+    a.num_rows = static_cast<uint32_t>(num_tokens * cache->num_kv_heads);
+    return from_cuda(pkv::launch_quant_move(a, cache->format, cache->head_dim, dtype, false, read,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+// pkv_quantize_blocks, and with `read` pkv_dequantize_blocks.
+pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool, const void* k,
+                        const void* v, const int32_t* pairs, int num_pairs, bool read,
+                        void* stream) {
+    pkv_status st = check_quant(cache);
+    if (st == PKV_OK) st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    if (pool->block_size != cache->block_size || pool->num_kv_heads != cache->num_kv_heads ||
+        pool->head_dim != cache->head_dim || num_pairs < 0)
+        return PKV_ERR_INVALID;
+    if (num_pairs == 0) return PKV_OK;
+    const int64_t per = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size;
+    if (num_pairs > INT32_MAX / per) return PKV_ERR_UNSUPPORTED;
+    if (!quant_arrays_ok(cache) || !k || !v || !pairs || !aligned16(k) || !aligned16(v) ||
+        !aligned4(pairs))
+        return PKV_ERR_INVALID;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::QuantArgs a = quant_args(cache, status);
+    a.k = k;
+    a.v = v;
+    a.k_out = const_cast<void*>(k);
+    a.v_out = const_cast<void*>(v);
+    a.pairs = pairs;
+    a.pool_blocks = pool->num_blocks;
+    a.num_rows = static_cast<uint32_t>(num_pairs * per);
+    return from_cuda(pkv::launch_quant_move(a, cache->format, cache->head_dim, pool->dtype, true,
+                                            read, static_cast<cudaStream_t>(stream)));
+}
+
+int quant_partition(const pkv_quant_cache* cache, int num_seqs, int num_q_heads, int max_context,
+                    int partition_blocks) {
+    return partition_blocks ? partition_blocks
+                            : auto_partition(num_seqs, num_q_heads, max_context,
+                                             cache->block_size);
+}
+
+}  // namespace
+
+uint64_t pkv_quant_codes_bytes(const pkv_quant_cache* cache) {
+    if (check_quant(cache) != PKV_OK) return 0;
+    return static_cast<uint64_t>(cache->num_blocks) * quant_code_bytes(cache);
+}
+
+uint64_t pkv_quant_scales_bytes(const pkv_quant_cache* cache) {
+    if (check_quant(cache) != PKV_OK) return 0;
+    return static_cast<uint64_t>(cache->num_blocks) * quant_side_bytes(cache);
+}
+
+pkv_status pkv_kv_append_quant(const pkv_quant_cache* cache, const int64_t* slot_mapping,
+                               int dtype, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int64_t num_tokens, void* stream) {
+    CallRange range("pkv_kv_append_quant");
+    return quant_rows(cache, slot_mapping, dtype, k, k_stride, v, v_stride, num_tokens, false,
+                      stream);
+}
+
+pkv_status pkv_kv_read_quant(const pkv_quant_cache* cache, const int64_t* slot_mapping, int dtype,
+                             void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                             int64_t num_tokens, void* stream) {
+    CallRange range("pkv_kv_read_quant");
+    return quant_rows(cache, slot_mapping, dtype, k_out, k_stride, v_out, v_stride, num_tokens,
+                      true, stream);
+}
+
+pkv_status pkv_quantize_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
+                               const void* k_pool, const void* v_pool, const int32_t* pairs,
+                               int num_pairs, void* stream) {
+    CallRange range("pkv_quantize_blocks");
+    return quant_blocks(cache, pool, k_pool, v_pool, pairs, num_pairs, false, stream);
+}
+
+pkv_status pkv_dequantize_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
+                                 void* k_pool, void* v_pool, const int32_t* pairs, int num_pairs,
+                                 void* stream) {
+    CallRange range("pkv_dequantize_blocks");
+    return quant_blocks(cache, pool, k_pool, v_pool, pairs, num_pairs, true, stream);
+}
+
+pkv_status pkv_copy_blocks_quant(const pkv_quant_cache* cache, const int32_t* pairs,
+                                 int num_pairs, void* stream) {
+    CallRange range("pkv_copy_blocks_quant");
+    pkv_status st = check_quant(cache);
+    if (st != PKV_OK) return st;
+    if (num_pairs < 0) return PKV_ERR_INVALID;
+    if (num_pairs == 0) return PKV_OK;
+    if (!quant_arrays_ok(cache) || !pairs || !aligned4(pairs)) return PKV_ERR_INVALID;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+    pkv::QuantArgs a = quant_args(cache, status);
+    a.pairs = pairs;
+    return from_cuda(pkv::launch_quant_copy(a, num_pairs, quant_code_bytes(cache),
+                                            quant_side_bytes(cache),
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_paged_decode_quant_workspace_bytes(const pkv_quant_cache* cache, int num_seqs,
+                                              int num_q_heads, int max_context,
+                                              int partition_blocks) {
+    if (check_quant(cache) != PKV_OK || num_seqs <= 0 || num_q_heads <= 0 || max_context <= 0 ||
+        partition_blocks < 0)
+        return 0;
+    const int pb = quant_partition(cache, num_seqs, num_q_heads, max_context, partition_blocks);
+    return decode_workspace(num_seqs, num_q_heads, cache->head_dim,
+                            ceil_div(ceil_div(max_context, cache->block_size), pb));
+}
+
+pkv_status pkv_paged_decode_quant(const pkv_quant_cache* cache, int dtype, void* out, const void* q,
+                                  const void* k_new, const void* v_new,
+                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* context_lens, int max_context, int num_seqs,
+                                  int num_q_heads, float scale, int partition_blocks,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range("pkv_paged_decode_quant");
+    pkv_status st = check_quant(cache);
+    if (st != PKV_OK) return st;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_q_heads <= 0 || partition_blocks < 0) return PKV_ERR_INVALID;
+    if (num_seqs == 0) return PKV_OK;
+    if (!quant_arrays_ok(cache) || !out || !q || !block_tables || !context_lens ||
+        !k_new != !v_new)
+        return PKV_ERR_INVALID;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned4(block_tables) || !aligned4(context_lens))
+        return PKV_ERR_INVALID;
+    const int B = cache->block_size;
+    if (max_blocks_per_seq <= 0 || max_context <= 0 ||
+        static_cast<int64_t>(max_context) > static_cast<int64_t>(max_blocks_per_seq) * B)
+        return PKV_ERR_INVALID;
+    if (num_q_heads % cache->num_kv_heads != 0) return PKV_ERR_INVALID;
+    const int group = num_q_heads / cache->num_kv_heads;
+    if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || max_blocks_per_seq > INT32_MAX / 64) return PKV_ERR_UNSUPPORTED;
+    const int pb = quant_partition(cache, num_seqs, num_q_heads, max_context, partition_blocks);
+    if (pb > INT32_MAX / 64) return PKV_ERR_UNSUPPORTED;
+    const int max_parts = ceil_div(ceil_div(max_context, B), pb);
+    if (max_parts > pkv::kMaxParts) return PKV_ERR_UNSUPPORTED;
+    const size_t need = decode_workspace(num_seqs, num_q_heads, cache->head_dim, max_parts);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return PKV_ERR_NOMEM;
+    int* status = status_word();
+    if (!status) return PKV_ERR_CUDA;
+
+    pkv::DecodeArgs a{};
+    a.out = out;
+    a.q = q;
+    a.k_pool = cache->k_codes;
+    a.v_pool = cache->v_codes;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.status = status;
+    a.num_blocks = cache->num_blocks;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.chunk_shift = chunk_shift(B);
+    a.partition_chunks = pb << a.chunk_shift;
+    a.max_parts = max_parts;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.test_stall = decode_test_stall();
+    if (need > 0) {
+        const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * max_parts;
+        char* w = static_cast<char*>(workspace);
+        a.o_part = reinterpret_cast<float*>(w);
+        w += rows * cache->head_dim * sizeof(float);
+        a.m_part = reinterpret_cast<float*>(w);
+        a.l_part = reinterpret_cast<float*>(w + round16(rows * sizeof(float)));
+    }
+    const pkv::QuantSides sides = {static_cast<uint8_t*>(cache->k_scales),
+                                   static_cast<uint8_t*>(cache->v_scales)};
+    return from_cuda(pkv::launch_quant_decode(a, sides, cache->format, dtype, cache->head_dim,
+                                              group, static_cast<cudaStream_t>(stream)));
+}
+
 pkv_status pkv_copy_blocks(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
                            const int32_t* pairs, int num_pairs, void* stream) {
     CallRange range("pkv_copy_blocks");

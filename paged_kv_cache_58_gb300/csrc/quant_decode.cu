@@ -1,0 +1,648 @@
+// Paged decode over a quantised cache (fp8 or fp4 rows), on the tensor cores.
+//
+// The work split is that of the decode over bf16 pools (paged_decode_tc.cu): one CTA per
+// (partition, kv head, sequence), four warps, warp w takes every 4th 16-token chunk of the
+// partition through a ring of stages of its own, keeps its own online softmax, and the states
+// merge at the end; partitions merge in the combine kernel.  A chunk is
+//   S^T[16 tokens x 8 heads] = K[16 x D] . q^T,   O^T[D x 8 heads] += V^T[D x 16] . P^T
+// as fp16 MMAs m16n8k16 with fp32 sums.  fp16, because every e4m3 value is one of fp16, and so is
+// every product of an e2m1 value and its e4m3 scale (6 digits, 2^-10 or more): what the MMAs
+// multiply is the stored row over its power of two, exactly.  The powers of two go where they
+// are exact too:
+//   K's 2^e scales the token's scores (fp32);
+//   V's 2^e goes into the weight: token j adds 2^(s_j + e_j - m) code_j to O and 2^(s_j - m) to
+//     the denominator, s the scores in powers of two.  The reference m follows the largest
+//     s_j + e_j, the size of what the token adds, not the largest s_j, so that the fp16 weights
+//     keep their digits where V's rows differ in size by any power of two.
+// m is a whole number, raised only where a weight would pass 2^15 (exact: the weights stay in
+// fp16's range, the largest at 2^6 or more), and a warp hands on log2 of its denominator's
+// power of two with m, so that neither end of the exponents' range (-90 .. 90) is lost.
+// q is scaled by a power of two into fp16's range; fp32 q, and the weights, are split into two
+// fp16 parts (fp32 output: 22 digits).
+//
+// Fragments.  The index that an MMA sums over may be in any order, if both sides share it.  So
+// lane (g, j) = (lane / 4, lane % 4) takes elements j D / 4 .. of K's row as they lie, and the
+// same of q; V^T comes out of ldmatrix .m16n16.trans.b8 with 4 tokens of one dimension (fp4: of
+// two) in a register, tokens 4 j .. 4 j + 3; row g of S^T is token 4 (g / 2) + g % 2 and row
+// g + 8 the token two further, which is the order in which movmatrix hands the weights on.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "quant.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBlk = 16;
+constexpr float kTop = 15.f;     // weights are at most 2^kTop
+constexpr float kStart = 7.f;    // and the largest one is put at about 2^kStart
+
+template <int FMT, int D, int G>
+struct QuantSmem {
+    using R = QuantRow<FMT, D>;
+    static constexpr int kSlab = kBlk * R::kCodes;
+    static constexpr int kStages = 4;
+    static constexpr int kCodeRing = kWarps * kStages * 2 * kSlab;
+    static constexpr int kSideRing = kWarps * kStages * 2 * R::kSide;
+    static constexpr int kBars = kWarps * kStages * 8;
+    // merge scratch reuses the rings once every warp is done
+    static constexpr int kMerge = kWarps * G * D * 4 + 2 * kWarps * G * 4;
+    static constexpr int kBody = kCodeRing + kSideRing > kMerge ? kCodeRing + kSideRing : kMerge;
+    static constexpr int kTotal = kBody + kBars + 1024;   // + alignment slack
+    static_assert(kBody % 8 == 0 && R::kSide % 16 == 0, "alignment");
+};
+
+PKV_DEVINL void ldsm_t_b8(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                          uint32_t& r3) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr));
+}
+PKV_DEVINL uint4 lds128(uint32_t addr) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(addr));
+    return r;
+}
+PKV_DEVINL uint2 lds64(uint32_t addr) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
+    return r;
+}
+PKV_DEVINL uint32_t lds32(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
+    return r;
+}
+PKV_DEVINL uint32_t lds16(uint32_t addr) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+                 : "=r"(r)
+                 : "r"(addr));
+    return r;
+}
+PKV_DEVINL uint32_t lds8(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+    return r;
+}
+PKV_DEVINL uint32_t movm_t(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+PKV_DEVINL uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+PKV_DEVINL uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// D = A (16x16 fp16, row) * B (16x8 fp16, col) + D, fp32 accumulate.
+PKV_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Where the 16-byte piece c of row t of a slab lies: the copy's swizzle (128, 64 or 32 bytes,
+// the length of a row).
+template <int ROW>
+PKV_DEVINL uint32_t piece_at(uint32_t base, int t, int c) {
+    const int f = ROW == 128 ? t & 7 : ROW == 64 ? (t >> 1) & 3 : (t >> 2) & 1;
+    return base + t * ROW + ((c ^ f) << 4);
+}
+
+// Two neighbouring elements of q.
+PKV_DEVINL float2 load_pair(const uint16_t* p) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
+    return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+}
+PKV_DEVINL float2 load_pair(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
+PKV_DEVINL void store_out(uint16_t* p, float x) {
+    *p = static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xffffu);
+}
+PKV_DEVINL void store_out(float* p, float x) { *p = x; }
+
+template <int FMT, int D, int G, typename T>
+__global__ void __launch_bounds__(kThreads, 3)
+quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a,
+                    const QuantSides qs) {
+    using SM = QuantSmem<FMT, D, G>;
+    using R = QuantRow<FMT, D>;
+    constexpr int KS = D / 16;            // k-steps of the scores, m-tiles of P.V
+    constexpr int kStages = SM::kStages;
+    constexpr bool kSplitQ = sizeof(T) == 4;
+    constexpr int E = D / 4;              // elements of a K row in one lane
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+
+    griddep_wait();
+    griddep_launch_dependents();
+    const int kvh = blockIdx.x;
+    const int seq = blockIdx.y;
+    const int part = blockIdx.z;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.max_blocks_per_seq;
+    const int b0 = part * a.partition_chunks;
+    const int my_first = b0 + warp;
+    int ids0;
+    {
+        const int e = (my_first + lane * kWarps) >> a.chunk_shift;
+        ids0 = e < a.max_blocks_per_seq ? __ldg(bt + e) : -1;
+    }
+    int L = a.context_lens[seq];
+    const int span = a.max_parts * a.partition_chunks;
+    const int max_chunks = a.max_blocks_per_seq << a.chunk_shift;
+    bool append = a.k_new != nullptr;
+    if (L > min(max_chunks, span) * static_cast<int64_t>(kBlk)) {
+        if (part == 0 && threadIdx.x == 0) raise_status(a.status, PKV_ERR_OOB);
+        L = static_cast<int>(min(min(max_chunks, span) * static_cast<int64_t>(kBlk),
+                                 static_cast<int64_t>(0x7ffffff0)));
+        append = false;   // the clamped end is not the new token
+    }
+    const int nblk = (L + kBlk - 1) / kBlk;
+    if (L <= 0 || b0 >= nblk) {   // uniform over the CTA, before any barrier
+        if (L <= 0 && part == 0) {
+            if (threadIdx.x == 0) raise_status(a.status, PKV_ERR_INVALID);
+            zero_invalid_rows(a, seq, kvh, G, D, sizeof(T));
+        }
+        return;
+    }
+    const int b1 = min(nblk, b0 + a.partition_chunks);
+    const int my_count = my_first < b1 ? (b1 - my_first + kWarps - 1) / kWarps : 0;
+
+    uint8_t* ring = smem + warp * kStages * 2 * SM::kSlab;
+    uint8_t* sides = smem + SM::kCodeRing + warp * kStages * 2 * R::kSide;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBody) + warp * kStages;
+    if (lane == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncwarp();
+
+    const uint64_t stream_policy = l2_policy_evict_first();   // each byte is read once
+    int ids = lane < my_count ? ids0 : -1;
+    auto fetch_ids = [&](int base) {
+        const int i = base + lane;
+        ids = (i < my_count) ? __ldg(bt + ((my_first + i * kWarps) >> a.chunk_shift)) : -1;
+    };
+    // Stage i: lanes 0 and 1 copy K's and V's codes, lanes 2 and 3 what lies beside them.
+    auto issue = [&](int i, int phys, bool on) {
+        const int st = i % kStages;
+        uint64_t* bar = &bars[st];
+        const bool bad = phys < 0 || phys >= a.num_blocks;
+        if (on && bad && lane == 0) raise_status(a.status, PKV_ERR_OOB);
+        mbar_arrive_if(on && bad && lane == 0, bar);   // complete the phase without data
+        const int ci = my_first + i * kWarps;
+        const int half = ci & ((1 << a.chunk_shift) - 1);
+        const int chunk = ((bad ? kvh : phys * a.num_kv_heads + kvh) << a.chunk_shift) + half;
+        const bool stall = a.test_stall && i == 0 && warp == 0 && blockIdx.x == 0 &&
+                           blockIdx.y == 0 && blockIdx.z == 0;
+        mbar_arrive_expect_tx_if(on && !bad && lane == 0, bar,
+                                 2 * (SM::kSlab + R::kSide) + (stall ? 16u : 0u));
+        const bool second = lane & 1;
+        const void* map = second ? static_cast<const void*>(&tm_v) : &tm_k;
+        tma_load_2d_hint_if(on && !bad && lane < 2, ring + (2 * st + second) * SM::kSlab, map, 0,
+                            chunk * kBlk, bar, stream_policy);
+        const uint8_t* side = (second ? qs.v : qs.k) + static_cast<size_t>(chunk) * R::kSide;
+        bulk_g2s_hint_if(on && !bad && (lane & ~1) == 2, sides + (2 * st + second) * R::kSide,
+                         side, R::kSide, bar, stream_policy);
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) issue(i, __shfl_sync(0xffffffffu, ids, i), i < my_count);
+
+    // q: head g, elements j E ..; scaled by 2^up into [2^14, 2^15) at its largest.
+    const int g8 = lane >> 2;
+    const int j4 = lane & 3;
+    uint32_t qb[KS][2], ql[kSplitQ ? KS : 1][2];
+    float q_unit;
+    {
+        float x[E];
+        float top = 0.f;
+        const T* qrow = static_cast<const T*>(a.q) +
+                        (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + (g8 < G ? g8 : 0)) *
+                            D + j4 * E;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 w = g8 < G ? load_pair(qrow + 2 * i) : make_float2(0.f, 0.f);
+            x[2 * i] = w.x;
+            x[2 * i + 1] = w.y;
+            top = fmaxf(top, fmaxf(fabsf(w.x), fabsf(w.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int up = min(126, 14 + 127 - (__float_as_int(top) >> 23));   // -114 .. 126
+        q_unit = pow2f(max(-126, -up));
+        const float f = pow2f(up);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float u = x[4 * ks + 2 * h] * f, v = x[4 * ks + 2 * h + 1] * f;
+                qb[ks][h] = pack_f16x2(u, v);
+                if constexpr (kSplitQ)
+                    ql[ks][h] = pack_f16x2(u - f16lo_to_f32(qb[ks][h]),
+                                           v - f16hi_to_f32(qb[ks][h]));
+            }
+    }
+    // Scores are held for heads 2 j, 2 j + 1 of tokens t_lo and t_lo + 2.
+    const int t_lo = 4 * (g8 >> 1) + (g8 & 1);
+    float hs[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        hs[h] = a.scale_log2 * __shfl_sync(0xffffffffu, q_unit, (2 * j4 + h) * 4);
+
+    float acc[KS][4];
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
+    float m_ref[2] = {-1e30f, -1e30f};   // finite: a chunk of -inf scores adds zeros
+    float l_part[2] = {0.f, 0.f};   // this lane's share of the denominators, over 2^m_ref
+
+    // ldmatrix row of this lane: token lane % 16, piece 2 i + lane / 16
+    const int v_tok = lane & 15;
+    const int v_pc = lane >> 4;
+
+    int failed_at = -1;
+    for (int i = 0; i < my_count; ++i) {
+        const int st_i = i % kStages;
+        if (!mbar_wait_warp(&bars[st_i], (i / kStages) & 1, a.status)) {
+            failed_at = i;
+            break;
+        }
+        uint8_t* kst = ring + 2 * st_i * SM::kSlab;
+        uint8_t* vst = kst + SM::kSlab;
+        uint8_t* ksd = sides + 2 * st_i * R::kSide;
+        uint8_t* vsd = ksd + R::kSide;
+        const uint32_t kbase = smem_u32(kst), vbase = smem_u32(vst);
+        const uint32_t ksb = smem_u32(ksd), vsb = smem_u32(vsd);
+        const int blk = my_first + i * kWarps;
+        const int valid = min(kBlk, L - blk * kBlk);
+
+        const bool fuse = append && blk == nblk - 1;   // holds the new token, row valid - 1
+        if (valid < kBlk || fuse) {
+            // Rows past the context may hold anything (an fp8 NaN, an fp4 scale that is one):
+            // zero V's, so that a weight of zero adds zero.
+            constexpr int kPieces = R::kCodes / 16;
+            for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
+                *reinterpret_cast<uint4*>(vst + (piece_at<R::kCodes>(0, valid + idx / kPieces,
+                                                                     idx % kPieces))) =
+                    make_uint4(0, 0, 0, 0);
+            if constexpr (FMT == PKV_FP4) {
+                for (int idx = lane; idx < (kBlk - valid) * KS; idx += 32)
+                    vsd[scale_at<D>(true, valid + idx / KS, idx % KS)] = 0;
+            }
+            if (fuse) {
+                // The new token's rows are quantised here, K's by lanes 0 .. D / 16 - 1 and V's
+                // by as many after them: into the stage and into the pool.
+                constexpr int RL = R::kLanes;
+                const int which = lane / RL, ln = lane % RL, t = valid - 1;
+                const bool mine = which < 2, v = which == 1;
+                float x[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = 0.f;
+                if (mine) {
+                    Elems16<T> in;
+                    in.load(static_cast<const T*>(v ? a.v_new : a.k_new) +
+                            (static_cast<size_t>(seq) * a.num_kv_heads + kvh) * D + 16 * ln);
+                    in.values(x);
+                }
+                const Quantised q = quantise<FMT, D, sizeof(T) == 4>(x);
+                if (mine) {
+                    const int phys = __ldg(bt + (blk >> a.chunk_shift));
+                    const bool there = phys >= 0 && phys < a.num_blocks;
+                    const size_t chunk =
+                        ((static_cast<size_t>(there ? phys : 0) * a.num_kv_heads + kvh)
+                         << a.chunk_shift) + (blk & ((1 << a.chunk_shift) - 1));
+                    uint8_t* pool = static_cast<uint8_t*>(const_cast<void*>(v ? a.v_pool
+                                                                              : a.k_pool)) +
+                                    (chunk * kBlk + t) * R::kCodes + ln * R::kLaneBytes;
+                    uint8_t* pside = (v ? qs.v : qs.k) + chunk * R::kSide;
+                    uint8_t* slab = v ? vst : kst;
+                    uint8_t* side = v ? vsd : ksd;
+                    if constexpr (FMT == PKV_FP8) {
+                        const uint4 w = make_uint4(q.codes[0], q.codes[1], q.codes[2], q.codes[3]);
+                        *reinterpret_cast<uint4*>(slab + piece_at<R::kCodes>(0, t, ln)) = w;
+                        if (there) *reinterpret_cast<uint4*>(pool) = w;
+                    } else {
+                        const uint2 w = make_uint2(q.codes[0], q.codes[1]);
+                        *reinterpret_cast<uint2*>(slab + piece_at<R::kCodes>(0, t, ln >> 1) +
+                                                  8 * (ln & 1)) = w;
+                        const int at = scale_at<D>(v, t, ln);
+                        side[at] = static_cast<uint8_t>(q.scale);
+                        if (there) {
+                            *reinterpret_cast<uint2*>(pool) = w;
+                            pside[at] = static_cast<uint8_t>(q.scale);
+                        }
+                    }
+                    if (ln == 0) {
+                        side[R::kScales + t] = static_cast<uint8_t>(q.exp);
+                        if (there) pside[R::kScales + t] = static_cast<uint8_t>(q.exp);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+
+        // S^T = K . q^T
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (FMT == PKV_FP8) {
+#pragma unroll
+            for (int p = 0; p < E / 16; ++p) {
+                const uint4 wa = lds128(piece_at<R::kCodes>(kbase, t_lo, j4 * (E / 16) + p));
+                const uint4 wb = lds128(piece_at<R::kCodes>(kbase, t_lo + 2, j4 * (E / 16) + p));
+                const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w};
+                const uint32_t vb[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x4(va[w], a0, a2);
+                    e4m3x4_to_f16x4(vb[w], a1, a3);
+                    const int ks = 4 * p + w;
+                    mma_f16(s, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+                    if constexpr (kSplitQ) mma_f16(s, a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
+                }
+            }
+        } else {
+            uint32_t va[E / 8], vb[E / 8], sa[E / 16], sb[E / 16];
+            if constexpr (D == 128) {
+                const uint4 wa = lds128(piece_at<R::kCodes>(kbase, t_lo, j4));
+                const uint4 wb = lds128(piece_at<R::kCodes>(kbase, t_lo + 2, j4));
+                va[0] = wa.x; va[1] = wa.y; va[2] = wa.z; va[3] = wa.w;
+                vb[0] = wb.x; vb[1] = wb.y; vb[2] = wb.z; vb[3] = wb.w;
+                const uint32_t ua = e4m3x2_to_f16x2(lds16(ksb + t_lo * 8 + 2 * j4));
+                const uint32_t ub = e4m3x2_to_f16x2(lds16(ksb + (t_lo + 2) * 8 + 2 * j4));
+                sa[0] = prmt(ua, ua, 0x1010); sa[1] = prmt(ua, ua, 0x3232);
+                sb[0] = prmt(ub, ub, 0x1010); sb[1] = prmt(ub, ub, 0x3232);
+            } else {
+                const uint2 wa = lds64(piece_at<R::kCodes>(kbase, t_lo, j4 >> 1) + 8 * (j4 & 1));
+                const uint2 wb =
+                    lds64(piece_at<R::kCodes>(kbase, t_lo + 2, j4 >> 1) + 8 * (j4 & 1));
+                va[0] = wa.x; va[1] = wa.y;
+                vb[0] = wb.x; vb[1] = wb.y;
+                const uint32_t ua = e4m3x2_to_f16x2(lds8(ksb + t_lo * 4 + j4));
+                const uint32_t ub = e4m3x2_to_f16x2(lds8(ksb + (t_lo + 2) * 4 + j4));
+                sa[0] = prmt(ua, ua, 0x1010);
+                sb[0] = prmt(ub, ub, 0x1010);
+            }
+#pragma unroll
+            for (int w = 0; w < E / 8; ++w) {
+                uint32_t xa[4], xb[4];
+                e2m1x8_to_f16x8(va[w], xa);
+                e2m1x8_to_f16x8(vb[w], xb);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    xa[e] = hmul2(xa[e], sa[w / 2]);
+                    xb[e] = hmul2(xb[e], sb[w / 2]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int ks = 2 * w + h;
+                    mma_f16(s, xa[2 * h], xb[2 * h], xa[2 * h + 1], xb[2 * h + 1], qb[ks][0],
+                            qb[ks][1]);
+                    if constexpr (kSplitQ)
+                        mma_f16(s, xa[2 * h], xb[2 * h], xa[2 * h + 1], xb[2 * h + 1], ql[ks][0],
+                                ql[ks][1]);
+                }
+            }
+        }
+        // scores in powers of two, and what the token adds: s + e
+        float t[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int tk = t_lo + 2 * h;
+            const float unit = __int_as_float(lds8(ksb + R::kScales + tk) << 23);
+            const float ve =
+                static_cast<float>(static_cast<int>(lds8(vsb + R::kScales + tk)) - 127);
+            const bool in = tk < valid;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = in ? s[2 * h + e] * unit * hs[e] : -INFINITY;
+                s[2 * h + e] = x;
+                t[2 * h + e] = x + (in ? ve : 0.f);
+            }
+        }
+        float mx[2] = {fmaxf(t[0], t[2]), fmaxf(t[1], t[3])};
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+        }
+        const bool grow0 = mx[0] > m_ref[0] + kTop, grow1 = mx[1] > m_ref[1] + kTop;
+        if (__any_sync(0xffffffffu, grow0 || grow1)) {
+            // In two steps for the denominator: 2^180 times smaller may still count there.
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float m_new = (h ? grow1 : grow0) ? ceilf(mx[h]) - kStart : m_ref[h];
+                const float half = m_ref[h] == m_new ? 1.f : fast_exp2((m_ref[h] - m_new) * 0.5f);
+                m_ref[h] = m_new;
+                l_part[h] = l_part[h] * half * half;
+                const float al = half * half;
+#pragma unroll
+                for (int mt = 0; mt < KS; ++mt) {
+                    acc[mt][h] *= al;
+                    acc[mt][2 + h] *= al;
+                }
+            }
+        }
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = fast_exp2(t[e] - m_ref[e & 1]);
+            l_part[e & 1] += fast_exp2(s[e] - m_ref[e & 1]);
+        }
+        const uint32_t h01 = pack_f16x2(p[0], p[1]);
+        const uint32_t h23 = pack_f16x2(p[2], p[3]);
+        const uint32_t l01 = pack_f16x2(p[0] - f16lo_to_f32(h01), p[1] - f16hi_to_f32(h01));
+        const uint32_t l23 = pack_f16x2(p[2] - f16lo_to_f32(h23), p[3] - f16hi_to_f32(h23));
+        const uint32_t bh0 = movm_t(h01), bh1 = movm_t(h23);
+        const uint32_t bl0 = movm_t(l01), bl1 = movm_t(l23);
+        // O^T += V^T . P^T
+        if constexpr (FMT == PKV_FP8) {
+#pragma unroll
+            for (int p2 = 0; p2 < KS / 2; ++p2) {   // 32 dimensions
+                uint32_t r[4];
+                ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x4(r[2 * h], a0, a2);
+                    e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
+                    mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, bh0, bh1);
+                    mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, bl0, bl1);
+                }
+            }
+        } else {
+            uint32_t sc[KS];
+            if constexpr (D == 128) {
+                const uint4 u0 = lds128(vsb + j4 * 32), u1 = lds128(vsb + j4 * 32 + 16);
+                sc[0] = u0.x; sc[1] = u0.y; sc[2] = u0.z; sc[3] = u0.w;
+                sc[4] = u1.x; sc[5] = u1.y; sc[6] = u1.z; sc[7] = u1.w;
+            } else {
+                const uint4 u0 = lds128(vsb + j4 * 16);
+                sc[0] = u0.x; sc[1] = u0.y; sc[2] = u0.z; sc[3] = u0.w;
+            }
+#pragma unroll
+            for (int p2 = 0; p2 < KS / 4; ++p2) {   // 64 dimensions
+                uint32_t r[4];
+                ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {       // 16 dimensions: one scale a token
+                    const int mt = 4 * p2 + h;
+                    uint32_t x[4], s01, s23;
+                    e2m1x8_to_f16x8(r[h], x);       // (d, d + 1) of four tokens
+                    e4m3x4_to_f16x4(sc[mt], s01, s23);
+                    const uint32_t a0 = hmul2(prmt(x[0], x[1], 0x5410), s01);
+                    const uint32_t a1 = hmul2(prmt(x[0], x[1], 0x7632), s01);
+                    const uint32_t a2 = hmul2(prmt(x[2], x[3], 0x5410), s23);
+                    const uint32_t a3 = hmul2(prmt(x[2], x[3], 0x7632), s23);
+                    mma_f16(acc[mt], a0, a1, a2, a3, bh0, bh1);
+                    mma_f16(acc[mt], a0, a1, a2, a3, bl0, bl1);
+                }
+            }
+        }
+        __syncwarp();
+        const int nxt = i + kStages;
+        if ((nxt & 31) == 0 && nxt < my_count) fetch_ids(nxt);
+        issue(nxt, __shfl_sync(0xffffffffu, ids, nxt & 31), nxt < my_count);
+    }
+    if (failed_at >= 0) {
+        for (int k = failed_at + 1; k < my_count && k < failed_at + kStages; ++k)
+            mbar_wait_warp(&bars[k % kStages], (k / kStages) & 1, a.status);
+    }
+
+    // This warp's denominators: their power of two joins m, and the output is over them.
+    float inv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+            l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], o);
+        inv[h] = l_part[h] == 0.f ? 0.f : 1.f / l_part[h];   // zero: no tokens, or none with weight
+        if (l_part[h] > 0.f && l_part[h] < INFINITY) {
+            const int e = (__float_as_int(l_part[h]) >> 23) - 127;
+            m_ref[h] += static_cast<float>(e);
+            l_part[h] *= pow2f(max(-126, min(126, -e)));
+        }
+    }
+    __syncthreads();  // every warp is done with its ring: reuse it as merge scratch
+    float* macc = reinterpret_cast<float*>(smem);            // [W][G][D], over the denominator
+    float* mm = macc + kWarps * G * D;                       // [W][G]
+    float* ml = mm + kWarps * G;                             // [W][G]
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        const int h = 2 * j4 + hh;
+        if (h < G) {
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+                float* row = macc + (warp * G + h) * D;
+                // fp4 hands out two neighbouring dimensions a register, fp8 two 8 apart
+                const int d0 = FMT == PKV_FP8 ? 16 * mt + g8 : 16 * mt + 2 * g8;
+                row[d0] = acc[mt][hh] * inv[hh];
+                row[d0 + (FMT == PKV_FP8 ? 8 : 1)] = acc[mt][2 + hh] * inv[hh];
+            }
+            if (g8 == 0) {
+                mm[warp * G + h] = my_count > 0 ? m_ref[hh] : -INFINITY;
+                ml[warp * G + h] = my_count > 0 ? l_part[hh] : 0.f;
+            }
+        }
+    }
+    __syncthreads();
+
+    for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
+        const int g = idx / D;
+        const int d = idx % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * G + g]);
+        float o = 0.f, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = fast_exp2(mm[w * G + g] - M) * ml[w * G + g];
+            o = fmaf(f, macc[(w * G + g) * D + d], o);
+            l += f;
+        }
+        const size_t row = static_cast<size_t>(seq) * a.num_q_heads + kvh * G + g;
+        if (a.max_parts == 1) {
+            store_out(static_cast<T*>(a.out) + row * D + d, o / l);
+        } else {
+            const size_t pr = row * a.max_parts + part;
+            a.o_part[pr * D + d] = l == 0.f ? 0.f : o / l;
+            if (d == 0) {
+                a.m_part[pr] = M;
+                a.l_part[pr] = l;
+            }
+        }
+    }
+}
+
+template <int FMT, int D, int G, typename T>
+cudaError_t launch_quant(const DecodeArgs& a, const QuantSides& qs, cudaStream_t stream) {
+    using SM = QuantSmem<FMT, D, G>;
+    CUtensorMap mk, mv;
+    const int64_t rows = a.num_blocks * a.num_kv_heads * (kBlk << a.chunk_shift);
+    if (!make_codes_map(&mk, a.k_pool, rows, QuantRow<FMT, D>::kCodes) ||
+        !make_codes_map(&mv, a.v_pool, rows, QuantRow<FMT, D>::kCodes))
+        return cudaErrorInvalidValue;
+    auto kern = quant_decode_kernel<FMT, D, G, T>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), SM::kTotal);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(a.num_kv_heads, a.num_seqs, a.max_parts), dim3(kThreads), SM::kTotal,
+                   stream, mk, mv, a, qs);
+    if (e != cudaSuccess || a.max_parts == 1) return e;
+    return launch_decode_combine(a, sizeof(T) == 4 ? PKV_F32 : PKV_BF16, D, stream);
+}
+
+template <int FMT, int D, typename T>
+cudaError_t launch_group(const DecodeArgs& a, const QuantSides& qs, int G, cudaStream_t stream) {
+    switch (G) {
+        case 1: return launch_quant<FMT, D, 1, T>(a, qs, stream);
+        case 2: return launch_quant<FMT, D, 2, T>(a, qs, stream);
+        case 4: return launch_quant<FMT, D, 4, T>(a, qs, stream);
+        case 8: return launch_quant<FMT, D, 8, T>(a, qs, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int FMT, typename T>
+cudaError_t launch_dim(const DecodeArgs& a, const QuantSides& qs, int D, int G,
+                       cudaStream_t stream) {
+    return D == 128 ? launch_group<FMT, 128, T>(a, qs, G, stream)
+                    : launch_group<FMT, 64, T>(a, qs, G, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_decode(const DecodeArgs& a, const QuantSides& qs, int format, int dtype,
+                                int head_dim, int group, cudaStream_t stream) {
+    if (format == PKV_FP8)
+        return dtype == PKV_BF16 ? launch_dim<PKV_FP8, uint16_t>(a, qs, head_dim, group, stream)
+                                 : launch_dim<PKV_FP8, float>(a, qs, head_dim, group, stream);
+    return dtype == PKV_BF16 ? launch_dim<PKV_FP4, uint16_t>(a, qs, head_dim, group, stream)
+                             : launch_dim<PKV_FP4, float>(a, qs, head_dim, group, stream);
+}
+
+}  // namespace pkv
