@@ -181,9 +181,9 @@ PKV_DEVINL Quantised quantise(const float (&x)[16]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) nan |= x[i] != x[i];
         const float a = fminf(amax * unit, 2688.f);
-        // a / 6 rounds to a midpoint of e4m3 only where it is one: where a differs from 6 m by a
-        // unit in its last place, the quotient differs from m by more than half of m's.
-        r.scale = to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xffu;
+        // A sixth in fp32: a product, exact where a sixth is a midpoint of e4m3 (6 m (1 / 6) is off
+        // by 2^-25 of m before it is rounded, to m), so that ties stay ties.
+        r.scale = to_e4m3x2(a * (1.f / 6.f), 0.f) & 0xffu;
         const float s = f16lo_to_f32(e4m3x2_to_f16x2(r.scale));
         if (nan) r.scale = 0x7fu;
         const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
@@ -192,7 +192,9 @@ PKV_DEVINL Quantised quantise(const float (&x)[16]) {
         for (int i = 0; i < 16; ++i) {
             const float y = x[i] * unit;
             if constexpr (EXACT_DIV) {
-                u[i] = s > 0.f ? __fdiv_rn(y, s) : 0.f;   // as above: on no border by rounding
+                // On a border only where y / s is: where y is a unit in its last place
+                // off it, the quotient is off by more than half of its own.
+                u[i] = s > 0.f ? __fdiv_rn(y, s) : 0.f;
             } else {
                 // y and border * s have at most 8 digits: y inv is within 2 units of a border
                 // where y / s is on it and 2^15 away where it is not.  Dropping four digits

@@ -47,7 +47,7 @@ def kept(x, fmt):
     y = y.unflatten(-1, (-1, 16))
     nan = y.isnan().any(-1, keepdim=True)
     a = y.abs().nan_to_num(0.0, posinf=1e300).clamp(max=top).amax(-1, keepdim=True)
-    s = nearest(a / 6, pos)
+    s = nearest((a.float() * torch.tensor(1 / 6)).double(), pos)   # an fp32 product
     z = torch.where(s > 0, y.abs() / s, torch.zeros_like(y))
     out = nearest(z.nan_to_num(0.0, posinf=1e300), torch.tensor(E2M1, dtype=torch.float64)) * s
     out = torch.where(nan, torch.full_like(out, math.nan), out * y.sign().nan_to_num(0.0))
