@@ -46,9 +46,11 @@ template <int FMT, int D, int G>
 struct QuantSmem {
     using R = QuantRow<FMT, D>;
     static constexpr int kSlab = kBlk * R::kCodes;
-    static constexpr int kStages = 4;
-    static constexpr int kCodeRing = kWarps * kStages * 2 * kSlab;
-    static constexpr int kSideRing = kWarps * kStages * 2 * R::kSide;
+    static constexpr int kStageBytes = 4 * (kSlab + R::kSide);   // K and V of two chunks
+    // Three CTAs share an SM: as many stages as fit 64 KB or so.
+    static constexpr int kStages = kStageBytes > 8000 ? 2 : kStageBytes > 4000 ? 3 : 6;
+    static constexpr int kCodeRing = kWarps * kStages * 4 * kSlab;
+    static constexpr int kSideRing = kWarps * kStages * 4 * R::kSide;
     static constexpr int kBars = kWarps * kStages * 8;
     // merge scratch reuses the rings once every warp is done
     static constexpr int kMerge = kWarps * G * D * 4 + 2 * kWarps * G * 4;
@@ -73,11 +75,6 @@ PKV_DEVINL uint4 lds128(uint32_t addr) {
 PKV_DEVINL uint2 lds64(uint32_t addr) {
     uint2 r;
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
-    return r;
-}
-PKV_DEVINL uint32_t lds32(uint32_t addr) {
-    uint32_t r;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
     return r;
 }
 PKV_DEVINL uint32_t lds16(uint32_t addr) {
@@ -136,6 +133,55 @@ PKV_DEVINL void store_out(uint16_t* p, float x) {
 }
 PKV_DEVINL void store_out(float* p, float x) { *p = x; }
 
+// The new token's rows, quantised: into the stage (row t of the slabs and of what lies beside
+// them) and into the cache.  K's by lanes 0 .. D / 16 - 1, V's by as many after them.
+template <int FMT, int D, typename T>
+__device__ __noinline__ void append_row(const DecodeArgs& a, const QuantSides& qs, int seq, int kvh,
+                                        int blk, int t, const int32_t* bt, int lane, uint8_t* kst,
+                                        uint8_t* vst, uint8_t* ksd, uint8_t* vsd) {
+    using R = QuantRow<FMT, D>;
+    const int which = lane / R::kLanes, ln = lane % R::kLanes;
+    const bool mine = which < 2, v = which == 1;
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    if (mine) {
+        Elems16<T> in;
+        in.load(static_cast<const T*>(v ? a.v_new : a.k_new) +
+                (static_cast<size_t>(seq) * a.num_kv_heads + kvh) * D + 16 * ln);
+        in.values(x);
+    }
+    const Quantised q = quantise<FMT, D, sizeof(T) == 4>(x);
+    if (!mine) return;
+    const int phys = __ldg(bt + (blk >> a.chunk_shift));
+    const bool there = phys >= 0 && phys < a.num_blocks;
+    const size_t chunk = ((static_cast<size_t>(there ? phys : 0) * a.num_kv_heads + kvh)
+                          << a.chunk_shift) + (blk & ((1 << a.chunk_shift) - 1));
+    uint8_t* pool = static_cast<uint8_t*>(const_cast<void*>(v ? a.v_pool : a.k_pool)) +
+                    (chunk * kBlk + t) * R::kCodes + ln * R::kLaneBytes;
+    uint8_t* pside = (v ? qs.v : qs.k) + chunk * R::kSide;
+    uint8_t* slab = v ? vst : kst;
+    uint8_t* side = v ? vsd : ksd;
+    if constexpr (FMT == PKV_FP8) {
+        const uint4 w = make_uint4(q.codes[0], q.codes[1], q.codes[2], q.codes[3]);
+        *reinterpret_cast<uint4*>(slab + piece_at<R::kCodes>(0, t, ln)) = w;
+        if (there) *reinterpret_cast<uint4*>(pool) = w;
+    } else {
+        const uint2 w = make_uint2(q.codes[0], q.codes[1]);
+        *reinterpret_cast<uint2*>(slab + piece_at<R::kCodes>(0, t, ln >> 1) + 8 * (ln & 1)) = w;
+        const int at = scale_at<D>(v, t, ln);
+        side[at] = static_cast<uint8_t>(q.scale);
+        if (there) {
+            *reinterpret_cast<uint2*>(pool) = w;
+            pside[at] = static_cast<uint8_t>(q.scale);
+        }
+    }
+    if (ln == 0) {
+        side[R::kScales + t] = static_cast<uint8_t>(q.exp);
+        if (there) pside[R::kScales + t] = static_cast<uint8_t>(q.exp);
+    }
+}
+
 template <int FMT, int D, int G, typename T>
 __global__ void __launch_bounds__(kThreads, 3)
 quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -145,7 +191,7 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     using R = QuantRow<FMT, D>;
     constexpr int KS = D / 16;            // k-steps of the scores, m-tiles of P.V
     constexpr int kStages = SM::kStages;
-    constexpr bool kSplitQ = sizeof(T) == 4;
+    constexpr bool kSplit = sizeof(T) == 4;   // fp32: q and the weights in two fp16 parts
     constexpr int E = D / 4;              // elements of a K row in one lane
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -161,10 +207,12 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.max_blocks_per_seq;
     const int b0 = part * a.partition_chunks;
-    const int my_first = b0 + warp;
+    // Warp w takes the pairs of chunks w, w + 4, ...; lane l keeps the block id of chunk l % 2 of
+    // pair l / 2 of 16 pairs.  The first ones do not wait for the length.
+    const int my_first = b0 + 2 * warp + 2 * kWarps * (lane >> 1) + (lane & 1);
     int ids0;
     {
-        const int e = (my_first + lane * kWarps) >> a.chunk_shift;
+        const int e = my_first >> a.chunk_shift;
         ids0 = e < a.max_blocks_per_seq ? __ldg(bt + e) : -1;
     }
     int L = a.context_lens[seq];
@@ -186,10 +234,10 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         return;
     }
     const int b1 = min(nblk, b0 + a.partition_chunks);
-    const int my_count = my_first < b1 ? (b1 - my_first + kWarps - 1) / kWarps : 0;
+    const int my_count = max(0, (b1 - b0 - 2 * warp + 2 * kWarps - 1) / (2 * kWarps));   // pairs
 
-    uint8_t* ring = smem + warp * kStages * 2 * SM::kSlab;
-    uint8_t* sides = smem + SM::kCodeRing + warp * kStages * 2 * R::kSide;
+    uint8_t* ring = smem + warp * kStages * 4 * SM::kSlab;
+    uint8_t* sides = smem + SM::kCodeRing + warp * kStages * 4 * R::kSide;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBody) + warp * kStages;
     if (lane == 0) {
         prefetch_tmap(&tm_k);
@@ -202,40 +250,45 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncwarp();
 
     const uint64_t stream_policy = l2_policy_evict_first();   // each byte is read once
-    int ids = lane < my_count ? ids0 : -1;
+    int ids = my_first < b1 ? ids0 : -1;
     auto fetch_ids = [&](int base) {
-        const int i = base + lane;
-        ids = (i < my_count) ? __ldg(bt + ((my_first + i * kWarps) >> a.chunk_shift)) : -1;
+        const int c = my_first + 2 * kWarps * base;
+        ids = c < b1 ? __ldg(bt + (c >> a.chunk_shift)) : -1;
     };
-    // Stage i: lanes 0 and 1 copy K's and V's codes, lanes 2 and 3 what lies beside them.
-    auto issue = [&](int i, int phys, bool on) {
+    // Stage i: lanes 0 .. 3 copy the first chunk's K and V codes and what lies beside each, lanes
+    // 4 .. 7 the second one's.
+    auto issue = [&](int i) {
         const int st = i % kStages;
         uint64_t* bar = &bars[st];
+        const int u = (lane >> 2) & 1;
+        const int c = b0 + 2 * (warp + kWarps * i) + u;
+        const int phys = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + u);
         const bool bad = phys < 0 || phys >= a.num_blocks;
-        if (on && bad && lane == 0) raise_status(a.status, PKV_ERR_OOB);
-        mbar_arrive_if(on && bad && lane == 0, bar);   // complete the phase without data
-        const int ci = my_first + i * kWarps;
-        const int half = ci & ((1 << a.chunk_shift) - 1);
-        const int chunk = ((bad ? kvh : phys * a.num_kv_heads + kvh) << a.chunk_shift) + half;
+        if (c < b1 && bad && (lane & ~4) == 0) raise_status(a.status, PKV_ERR_OOB);
+        const bool go = c < b1 && !bad;
+        const uint32_t going = __ballot_sync(0xffffffffu, go);
+        const uint32_t chunks = (going & 1) + ((going >> 4) & 1);
         const bool stall = a.test_stall && i == 0 && warp == 0 && blockIdx.x == 0 &&
                            blockIdx.y == 0 && blockIdx.z == 0;
-        mbar_arrive_expect_tx_if(on && !bad && lane == 0, bar,
-                                 2 * (SM::kSlab + R::kSide) + (stall ? 16u : 0u));
-        const bool second = lane & 1;
-        const void* map = second ? static_cast<const void*>(&tm_v) : &tm_k;
-        tma_load_2d_hint_if(on && !bad && lane < 2, ring + (2 * st + second) * SM::kSlab, map, 0,
+        mbar_arrive_expect_tx_if(i < my_count && lane == 0, bar,   // none: completes the phase
+                                 chunks * (2 * (SM::kSlab + R::kSide)) + (stall ? 16u : 0u));
+        const int chunk = (((bad ? 0 : phys) * a.num_kv_heads + kvh) << a.chunk_shift) +
+                          (c & ((1 << a.chunk_shift) - 1));
+        const int at = 4 * st + 2 * u + (lane & 1);
+        const void* map = lane & 1 ? static_cast<const void*>(&tm_v) : &tm_k;
+        tma_load_2d_hint_if(go && lane < 8 && !(lane & 2), ring + at * SM::kSlab, map, 0,
                             chunk * kBlk, bar, stream_policy);
-        const uint8_t* side = (second ? qs.v : qs.k) + static_cast<size_t>(chunk) * R::kSide;
-        bulk_g2s_hint_if(on && !bad && (lane & ~1) == 2, sides + (2 * st + second) * R::kSide,
-                         side, R::kSide, bar, stream_policy);
+        const uint8_t* side = (lane & 1 ? qs.v : qs.k) + static_cast<int64_t>(chunk) * R::kSide;
+        bulk_g2s_hint_if(go && lane < 8 && (lane & 2), sides + at * R::kSide, side, R::kSide, bar,
+                         stream_policy);
     };
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) issue(i, __shfl_sync(0xffffffffu, ids, i), i < my_count);
+    for (int i = 0; i < kStages; ++i) issue(i);
 
     // q: head g, elements j E ..; scaled by 2^up into [2^14, 2^15) at its largest.
     const int g8 = lane >> 2;
     const int j4 = lane & 3;
-    uint32_t qb[KS][2], ql[kSplitQ ? KS : 1][2];
+    uint32_t qb[KS][2], ql[kSplit ? KS : 1][2];
     float q_unit;
     {
         float x[E];
@@ -261,7 +314,7 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int h = 0; h < 2; ++h) {
                 const float u = x[4 * ks + 2 * h] * f, v = x[4 * ks + 2 * h + 1] * f;
                 qb[ks][h] = pack_f16x2(u, v);
-                if constexpr (kSplitQ)
+                if constexpr (kSplit)
                     ql[ks][h] = pack_f16x2(u - f16lo_to_f32(qb[ks][h]),
                                            v - f16hi_to_f32(qb[ks][h]));
             }
@@ -292,160 +345,144 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
             failed_at = i;
             break;
         }
-        uint8_t* kst = ring + 2 * st_i * SM::kSlab;
-        uint8_t* vst = kst + SM::kSlab;
-        uint8_t* ksd = sides + 2 * st_i * R::kSide;
-        uint8_t* vsd = ksd + R::kSide;
-        const uint32_t kbase = smem_u32(kst), vbase = smem_u32(vst);
-        const uint32_t ksb = smem_u32(ksd), vsb = smem_u32(vsd);
-        const int blk = my_first + i * kWarps;
-        const int valid = min(kBlk, L - blk * kBlk);
+        const int c0 = b0 + 2 * (warp + kWarps * i);
+        uint8_t* slabs = ring + 4 * st_i * SM::kSlab;     // K, V of the first chunk, of the second
+        uint8_t* besides = sides + 4 * st_i * R::kSide;
+        const uint32_t slab0 = smem_u32(slabs), side0 = smem_u32(besides);
+        const bool full = c0 + 1 < b1 && (c0 + 2) * kBlk <= L;
 
-        const bool fuse = append && blk == nblk - 1;   // holds the new token, row valid - 1
-        if (valid < kBlk || fuse) {
-            // Rows past the context may hold anything (an fp8 NaN, an fp4 scale that is one):
-            // zero V's, so that a weight of zero adds zero.
-            constexpr int kPieces = R::kCodes / 16;
-            for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
-                *reinterpret_cast<uint4*>(vst + (piece_at<R::kCodes>(0, valid + idx / kPieces,
-                                                                     idx % kPieces))) =
-                    make_uint4(0, 0, 0, 0);
-            if constexpr (FMT == PKV_FP4) {
-                for (int idx = lane; idx < (kBlk - valid) * KS; idx += 32)
-                    vsd[scale_at<D>(true, valid + idx / KS, idx % KS)] = 0;
-            }
-            if (fuse) {
-                // The new token's rows are quantised here, K's by lanes 0 .. D / 16 - 1 and V's
-                // by as many after them: into the stage and into the pool.
-                constexpr int RL = R::kLanes;
-                const int which = lane / RL, ln = lane % RL, t = valid - 1;
-                const bool mine = which < 2, v = which == 1;
-                float x[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = 0.f;
-                if (mine) {
-                    Elems16<T> in;
-                    in.load(static_cast<const T*>(v ? a.v_new : a.k_new) +
-                            (static_cast<size_t>(seq) * a.num_kv_heads + kvh) * D + 16 * ln);
-                    in.values(x);
+        if (!full || (append && c0 + 2 >= nblk)) {
+            for (int u = 0; u < 2; ++u) {
+                const int blk = c0 + u;
+                const int valid = blk < b1 ? min(kBlk, L - blk * kBlk) : 0;
+                uint8_t* kst = slabs + 2 * u * SM::kSlab;
+                uint8_t* vst = kst + SM::kSlab;
+                uint8_t* ksd = besides + 2 * u * R::kSide;
+                uint8_t* vsd = ksd + R::kSide;
+                // Rows past the context may hold anything (an fp8 NaN, an fp4 scale that is
+                // one): zero V's, so that a weight of zero adds zero.
+                constexpr int kPieces = R::kCodes / 16;
+                for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
+                    *reinterpret_cast<uint4*>(vst + piece_at<R::kCodes>(0, valid + idx / kPieces,
+                                                                        idx % kPieces)) =
+                        make_uint4(0, 0, 0, 0);
+                if constexpr (FMT == PKV_FP4) {
+                    for (int idx = lane; idx < (kBlk - valid) * KS; idx += 32)
+                        vsd[scale_at<D>(true, valid + idx / KS, idx % KS)] = 0;
                 }
-                const Quantised q = quantise<FMT, D, sizeof(T) == 4>(x);
-                if (mine) {
-                    const int phys = __ldg(bt + (blk >> a.chunk_shift));
-                    const bool there = phys >= 0 && phys < a.num_blocks;
-                    const size_t chunk =
-                        ((static_cast<size_t>(there ? phys : 0) * a.num_kv_heads + kvh)
-                         << a.chunk_shift) + (blk & ((1 << a.chunk_shift) - 1));
-                    uint8_t* pool = static_cast<uint8_t*>(const_cast<void*>(v ? a.v_pool
-                                                                              : a.k_pool)) +
-                                    (chunk * kBlk + t) * R::kCodes + ln * R::kLaneBytes;
-                    uint8_t* pside = (v ? qs.v : qs.k) + chunk * R::kSide;
-                    uint8_t* slab = v ? vst : kst;
-                    uint8_t* side = v ? vsd : ksd;
-                    if constexpr (FMT == PKV_FP8) {
-                        const uint4 w = make_uint4(q.codes[0], q.codes[1], q.codes[2], q.codes[3]);
-                        *reinterpret_cast<uint4*>(slab + piece_at<R::kCodes>(0, t, ln)) = w;
-                        if (there) *reinterpret_cast<uint4*>(pool) = w;
-                    } else {
-                        const uint2 w = make_uint2(q.codes[0], q.codes[1]);
-                        *reinterpret_cast<uint2*>(slab + piece_at<R::kCodes>(0, t, ln >> 1) +
-                                                  8 * (ln & 1)) = w;
-                        const int at = scale_at<D>(v, t, ln);
-                        side[at] = static_cast<uint8_t>(q.scale);
-                        if (there) {
-                            *reinterpret_cast<uint2*>(pool) = w;
-                            pside[at] = static_cast<uint8_t>(q.scale);
-                        }
-                    }
-                    if (ln == 0) {
-                        side[R::kScales + t] = static_cast<uint8_t>(q.exp);
-                        if (there) pside[R::kScales + t] = static_cast<uint8_t>(q.exp);
-                    }
-                }
+                if (append && blk == nblk - 1 && blk < b1)   // holds the new token, row valid - 1
+                    append_row<FMT, D, T>(a, qs, seq, kvh, blk, valid - 1, bt, lane, kst, vst, ksd,
+                                          vsd);
             }
             fence_proxy_async_smem();
             __syncwarp();
         }
 
         // S^T = K . q^T
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        float s[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
         if constexpr (FMT == PKV_FP8) {
 #pragma unroll
             for (int p = 0; p < E / 16; ++p) {
-                const uint4 wa = lds128(piece_at<R::kCodes>(kbase, t_lo, j4 * (E / 16) + p));
-                const uint4 wb = lds128(piece_at<R::kCodes>(kbase, t_lo + 2, j4 * (E / 16) + p));
-                const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w};
-                const uint32_t vb[4] = {wb.x, wb.y, wb.z, wb.w};
+                uint32_t va[2][4], vb[2][4];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_f16x4(va[w], a0, a2);
-                    e4m3x4_to_f16x4(vb[w], a1, a3);
-                    const int ks = 4 * p + w;
-                    mma_f16(s, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
-                    if constexpr (kSplitQ) mma_f16(s, a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t kb = slab0 + 2 * u * SM::kSlab;
+                    const uint4 wa = lds128(piece_at<R::kCodes>(kb, t_lo, j4 * (E / 16) + p));
+                    const uint4 wb = lds128(piece_at<R::kCodes>(kb, t_lo + 2, j4 * (E / 16) + p));
+                    va[u][0] = wa.x; va[u][1] = wa.y; va[u][2] = wa.z; va[u][3] = wa.w;
+                    vb[u][0] = wb.x; vb[u][1] = wb.y; vb[u][2] = wb.z; vb[u][3] = wb.w;
                 }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_f16x4(va[u][w], a0, a2);
+                        e4m3x4_to_f16x4(vb[u][w], a1, a3);
+                        const int ks = 4 * p + w;
+                        mma_f16(s[u], a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+                        if constexpr (kSplit) mma_f16(s[u], a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
+                    }
             }
         } else {
-            uint32_t va[E / 8], vb[E / 8], sa[E / 16], sb[E / 16];
-            if constexpr (D == 128) {
-                const uint4 wa = lds128(piece_at<R::kCodes>(kbase, t_lo, j4));
-                const uint4 wb = lds128(piece_at<R::kCodes>(kbase, t_lo + 2, j4));
-                va[0] = wa.x; va[1] = wa.y; va[2] = wa.z; va[3] = wa.w;
-                vb[0] = wb.x; vb[1] = wb.y; vb[2] = wb.z; vb[3] = wb.w;
-                const uint32_t ua = e4m3x2_to_f16x2(lds16(ksb + t_lo * 8 + 2 * j4));
-                const uint32_t ub = e4m3x2_to_f16x2(lds16(ksb + (t_lo + 2) * 8 + 2 * j4));
-                sa[0] = prmt(ua, ua, 0x1010); sa[1] = prmt(ua, ua, 0x3232);
-                sb[0] = prmt(ub, ub, 0x1010); sb[1] = prmt(ub, ub, 0x3232);
-            } else {
-                const uint2 wa = lds64(piece_at<R::kCodes>(kbase, t_lo, j4 >> 1) + 8 * (j4 & 1));
-                const uint2 wb =
-                    lds64(piece_at<R::kCodes>(kbase, t_lo + 2, j4 >> 1) + 8 * (j4 & 1));
-                va[0] = wa.x; va[1] = wa.y;
-                vb[0] = wb.x; vb[1] = wb.y;
-                const uint32_t ua = e4m3x2_to_f16x2(lds8(ksb + t_lo * 4 + j4));
-                const uint32_t ub = e4m3x2_to_f16x2(lds8(ksb + (t_lo + 2) * 4 + j4));
-                sa[0] = prmt(ua, ua, 0x1010);
-                sb[0] = prmt(ub, ub, 0x1010);
-            }
+            uint32_t va[2][E / 8], vb[2][E / 8], sa[2][E / 16], sb[2][E / 16];
 #pragma unroll
-            for (int w = 0; w < E / 8; ++w) {
-                uint32_t xa[4], xb[4];
-                e2m1x8_to_f16x8(va[w], xa);
-                e2m1x8_to_f16x8(vb[w], xb);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    xa[e] = hmul2(xa[e], sa[w / 2]);
-                    xb[e] = hmul2(xb[e], sb[w / 2]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int ks = 2 * w + h;
-                    mma_f16(s, xa[2 * h], xb[2 * h], xa[2 * h + 1], xb[2 * h + 1], qb[ks][0],
-                            qb[ks][1]);
-                    if constexpr (kSplitQ)
-                        mma_f16(s, xa[2 * h], xb[2 * h], xa[2 * h + 1], xb[2 * h + 1], ql[ks][0],
-                                ql[ks][1]);
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t kb = slab0 + 2 * u * SM::kSlab, ksb = side0 + 2 * u * R::kSide;
+                if constexpr (D == 128) {
+                    const uint4 wa = lds128(piece_at<R::kCodes>(kb, t_lo, j4));
+                    const uint4 wb = lds128(piece_at<R::kCodes>(kb, t_lo + 2, j4));
+                    va[u][0] = wa.x; va[u][1] = wa.y; va[u][2] = wa.z; va[u][3] = wa.w;
+                    vb[u][0] = wb.x; vb[u][1] = wb.y; vb[u][2] = wb.z; vb[u][3] = wb.w;
+                    const uint32_t ua = e4m3x2_to_f16x2(lds16(ksb + t_lo * 8 + 2 * j4));
+                    const uint32_t ub = e4m3x2_to_f16x2(lds16(ksb + (t_lo + 2) * 8 + 2 * j4));
+                    sa[u][0] = prmt(ua, ua, 0x1010); sa[u][1] = prmt(ua, ua, 0x3232);
+                    sb[u][0] = prmt(ub, ub, 0x1010); sb[u][1] = prmt(ub, ub, 0x3232);
+                } else {
+                    const uint2 wa =
+                        lds64(piece_at<R::kCodes>(kb, t_lo, j4 >> 1) + 8 * (j4 & 1));
+                    const uint2 wb =
+                        lds64(piece_at<R::kCodes>(kb, t_lo + 2, j4 >> 1) + 8 * (j4 & 1));
+                    va[u][0] = wa.x; va[u][1] = wa.y;
+                    vb[u][0] = wb.x; vb[u][1] = wb.y;
+                    const uint32_t ua = e4m3x2_to_f16x2(lds8(ksb + t_lo * 4 + j4));
+                    const uint32_t ub = e4m3x2_to_f16x2(lds8(ksb + (t_lo + 2) * 4 + j4));
+                    sa[u][0] = prmt(ua, ua, 0x1010);
+                    sb[u][0] = prmt(ub, ub, 0x1010);
                 }
             }
+#pragma unroll
+            for (int w = 0; w < E / 8; ++w)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t xa[4], xb[4];
+                    e2m1x8_to_f16x8(va[u][w], xa);
+                    e2m1x8_to_f16x8(vb[u][w], xb);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        xa[e] = hmul2(xa[e], sa[u][w / 2]);
+                        xb[e] = hmul2(xb[e], sb[u][w / 2]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int ks = 2 * w + h;
+                        mma_f16(s[u], xa[2 * h], xb[2 * h], xa[2 * h + 1], xb[2 * h + 1],
+                                qb[ks][0], qb[ks][1]);
+                        if constexpr (kSplit)
+                            mma_f16(s[u], xa[2 * h], xb[2 * h], xa[2 * h + 1], xb[2 * h + 1],
+                                    ql[ks][0], ql[ks][1]);
+                    }
+                }
         }
         // scores in powers of two, and what the token adds: s + e
-        float t[4];
+        float t[2][4];
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int tk = t_lo + 2 * h;
-            const float unit = __int_as_float(lds8(ksb + R::kScales + tk) << 23);
-            const float ve =
-                static_cast<float>(static_cast<int>(lds8(vsb + R::kScales + tk)) - 127);
-            const bool in = tk < valid;
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float x = in ? s[2 * h + e] * unit * hs[e] : -INFINITY;
-                s[2 * h + e] = x;
-                t[2 * h + e] = x + (in ? ve : 0.f);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = side0 + 2 * u * R::kSide + R::kScales + t_lo + 2 * h;
+                const float unit = __int_as_float(lds8(at) << 23);
+                float ve = static_cast<float>(static_cast<int>(lds8(at + R::kSide)) - 127);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) s[u][2 * h + e] *= unit * hs[e];
+                if (!full) {
+                    const int blk = c0 + u;
+                    if (t_lo + 2 * h >= (blk < b1 ? L - blk * kBlk : 0)) {
+                        s[u][2 * h] = s[u][2 * h + 1] = -INFINITY;
+                        ve = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    t[u][2 * h + e] = s[u][2 * h + e] + ve;
+                    mx[e] = fmaxf(mx[e], t[u][2 * h + e]);
+                }
             }
-        }
-        float mx[2] = {fmaxf(t[0], t[2]), fmaxf(t[1], t[3])};
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
@@ -468,66 +505,80 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
             }
         }
-        float p[4];
+        // P^T fragments: [token][head] 8x8 tiles transposed in registers
+        uint32_t ph[2][2], pl[kSplit ? 2 : 1][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            p[e] = fast_exp2(t[e] - m_ref[e & 1]);
-            l_part[e & 1] += fast_exp2(s[e] - m_ref[e & 1]);
+        for (int u = 0; u < 2; ++u) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[e] = fast_exp2(t[u][e] - m_ref[e & 1]);
+                l_part[e & 1] += fast_exp2(s[u][e] - m_ref[e & 1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t hi = pack_f16x2(p[2 * h], p[2 * h + 1]);
+                ph[u][h] = movm_t(hi);
+                if constexpr (kSplit)
+                    pl[u][h] = movm_t(pack_f16x2(p[2 * h] - f16lo_to_f32(hi),
+                                                 p[2 * h + 1] - f16hi_to_f32(hi)));
+            }
         }
-        const uint32_t h01 = pack_f16x2(p[0], p[1]);
-        const uint32_t h23 = pack_f16x2(p[2], p[3]);
-        const uint32_t l01 = pack_f16x2(p[0] - f16lo_to_f32(h01), p[1] - f16hi_to_f32(h01));
-        const uint32_t l23 = pack_f16x2(p[2] - f16lo_to_f32(h23), p[3] - f16hi_to_f32(h23));
-        const uint32_t bh0 = movm_t(h01), bh1 = movm_t(h23);
-        const uint32_t bl0 = movm_t(l01), bl1 = movm_t(l23);
         // O^T += V^T . P^T
-        if constexpr (FMT == PKV_FP8) {
 #pragma unroll
-            for (int p2 = 0; p2 < KS / 2; ++p2) {   // 32 dimensions
-                uint32_t r[4];
-                ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2], r[3]);
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t vbase = slab0 + (2 * u + 1) * SM::kSlab;
+            if constexpr (FMT == PKV_FP8) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_f16x4(r[2 * h], a0, a2);
-                    e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
-                    mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, bh0, bh1);
-                    mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, bl0, bl1);
+                for (int p2 = 0; p2 < KS / 2; ++p2) {   // 32 dimensions
+                    uint32_t r[4];
+                    ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2],
+                              r[3]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_f16x4(r[2 * h], a0, a2);
+                        e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
+                        mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, ph[u][0], ph[u][1]);
+                        if constexpr (kSplit)
+                            mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, pl[u][0], pl[u][1]);
+                    }
                 }
-            }
-        } else {
-            uint32_t sc[KS];
-            if constexpr (D == 128) {
-                const uint4 u0 = lds128(vsb + j4 * 32), u1 = lds128(vsb + j4 * 32 + 16);
-                sc[0] = u0.x; sc[1] = u0.y; sc[2] = u0.z; sc[3] = u0.w;
-                sc[4] = u1.x; sc[5] = u1.y; sc[6] = u1.z; sc[7] = u1.w;
             } else {
-                const uint4 u0 = lds128(vsb + j4 * 16);
-                sc[0] = u0.x; sc[1] = u0.y; sc[2] = u0.z; sc[3] = u0.w;
-            }
+                const uint32_t vsb = side0 + (2 * u + 1) * R::kSide;
+                uint32_t sc[KS];
 #pragma unroll
-            for (int p2 = 0; p2 < KS / 4; ++p2) {   // 64 dimensions
-                uint32_t r[4];
-                ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2], r[3]);
+                for (int q4 = 0; q4 < KS / 4; ++q4) {
+                    const uint4 w = lds128(vsb + j4 * (D / 4) + 16 * q4);
+                    sc[4 * q4] = w.x; sc[4 * q4 + 1] = w.y;
+                    sc[4 * q4 + 2] = w.z; sc[4 * q4 + 3] = w.w;
+                }
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {       // 16 dimensions: one scale a token
-                    const int mt = 4 * p2 + h;
-                    uint32_t x[4], s01, s23;
-                    e2m1x8_to_f16x8(r[h], x);       // (d, d + 1) of four tokens
-                    e4m3x4_to_f16x4(sc[mt], s01, s23);
-                    const uint32_t a0 = hmul2(prmt(x[0], x[1], 0x5410), s01);
-                    const uint32_t a1 = hmul2(prmt(x[0], x[1], 0x7632), s01);
-                    const uint32_t a2 = hmul2(prmt(x[2], x[3], 0x5410), s23);
-                    const uint32_t a3 = hmul2(prmt(x[2], x[3], 0x7632), s23);
-                    mma_f16(acc[mt], a0, a1, a2, a3, bh0, bh1);
-                    mma_f16(acc[mt], a0, a1, a2, a3, bl0, bl1);
+                for (int p2 = 0; p2 < KS / 4; ++p2) {   // 64 dimensions
+                    uint32_t r[4];
+                    ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2],
+                              r[3]);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {       // 16 dimensions: one scale a token
+                        const int mt = 4 * p2 + h;
+                        uint32_t x[4], s01, s23;
+                        e2m1x8_to_f16x8(r[h], x);       // (d, d + 1) of four tokens
+                        e4m3x4_to_f16x4(sc[mt], s01, s23);
+                        const uint32_t a0 = hmul2(prmt(x[0], x[1], 0x5410), s01);
+                        const uint32_t a1 = hmul2(prmt(x[0], x[1], 0x7632), s01);
+                        const uint32_t a2 = hmul2(prmt(x[2], x[3], 0x5410), s23);
+                        const uint32_t a3 = hmul2(prmt(x[2], x[3], 0x7632), s23);
+                        mma_f16(acc[mt], a0, a1, a2, a3, ph[u][0], ph[u][1]);
+                        if constexpr (kSplit)
+                            mma_f16(acc[mt], a0, a1, a2, a3, pl[u][0], pl[u][1]);
+                    }
                 }
             }
         }
         __syncwarp();
         const int nxt = i + kStages;
-        if ((nxt & 31) == 0 && nxt < my_count) fetch_ids(nxt);
-        issue(nxt, __shfl_sync(0xffffffffu, ids, nxt & 31), nxt < my_count);
+        if ((nxt & 15) == 0 && nxt < my_count) fetch_ids(nxt);
+        issue(nxt);
     }
     if (failed_at >= 0) {
         for (int k = failed_at + 1; k < my_count && k < failed_at + kStages; ++k)
