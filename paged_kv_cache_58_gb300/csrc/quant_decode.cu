@@ -122,12 +122,6 @@ PKV_DEVINL uint32_t piece_at(uint32_t base, int t, int c) {
     return base + t * ROW + ((c ^ f) << 4);
 }
 
-// Two neighbouring elements of q.
-PKV_DEVINL float2 load_pair(const uint16_t* p) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-    return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
-}
-PKV_DEVINL float2 load_pair(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
 PKV_DEVINL void store_out(uint16_t* p, float x) {
     *p = static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xffffu);
 }
@@ -180,6 +174,46 @@ __device__ __noinline__ void append_row(const DecodeArgs& a, const QuantSides& q
         side[R::kScales + t] = static_cast<uint8_t>(q.exp);
         if (there) pside[R::kScales + t] = static_cast<uint8_t>(q.exp);
     }
+}
+
+// q of one head: E elements from p on, scaled by the power of two that puts the head's largest
+// element into [2^14, 2^15), as fp16 pairs (and what they leave, for fp32).  Returns the scale's
+// inverse.  The four lanes of a head call together.
+template <typename T, int E, bool SPLIT>
+PKV_DEVINL float load_q(const T* p, bool there, uint32_t (&hi)[E / 4][2],
+                        uint32_t (&lo)[SPLIT ? E / 4 : 1][2]) {
+    float x[E];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < E / 16; ++i) {
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = 0.f;
+        if (there) {
+            Elems16<T> in;
+            in.load(p + 16 * i);
+            in.values(v);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            x[16 * i + k] = v[k];
+            top = fmaxf(top, fabsf(v[k]));
+        }
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int up = min(126, 14 + 127 - (__float_as_int(top) >> 23));   // -114 .. 126
+    const float f = pow2f(up);
+#pragma unroll
+    for (int ks = 0; ks < E / 4; ++ks)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float u = x[4 * ks + 2 * h] * f, v = x[4 * ks + 2 * h + 1] * f;
+            hi[ks][h] = pack_f16x2(u, v);
+            if constexpr (SPLIT)
+                lo[ks][h] = pack_f16x2(u - f16lo_to_f32(hi[ks][h]), v - f16hi_to_f32(hi[ks][h]));
+        }
+    return pow2f(max(-126, -up));
 }
 
 template <int FMT, int D, int G, typename T>
@@ -255,70 +289,48 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int c = my_first + 2 * kWarps * base;
         ids = c < b1 ? __ldg(bt + (c >> a.chunk_shift)) : -1;
     };
-    // Stage i: lanes 0 .. 3 copy the first chunk's K and V codes and what lies beside each, lanes
-    // 4 .. 7 the second one's.
-    auto issue = [&](int i) {
-        const int st = i % kStages;
+    // Stage st, pair i: lanes 0 .. 3 copy the first chunk's K and V codes and what lies beside each,
+    // lanes 4 .. 7 the second one's.  What does not change from pair to pair is kept.
+    const int cu = (lane >> 2) & 1;
+    const bool lane_tma = lane < 8 && !(lane & 2), lane_side = lane < 8 && (lane & 2);
+    const void* lane_map = lane & 1 ? static_cast<const void*>(&tm_v) : &tm_k;
+    const uint8_t* lane_sides = lane & 1 ? qs.v : qs.k;
+    const int lane_at = 2 * cu + (lane & 1);
+    const int block_step = a.num_kv_heads << a.chunk_shift;
+    const int block_at = (kvh << a.chunk_shift) + (a.chunk_shift & cu);   // b0 is even there
+    bool lost = false;   // a block id outside the pool
+    int next = b0 + 2 * warp + cu;   // the lane's chunk of the next pair
+    auto issue = [&](int st, int i, uint32_t extra) {
+        const int phys = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + cu);
+        const bool ok = static_cast<uint32_t>(phys) < static_cast<uint32_t>(a.num_blocks);
+        const bool go = ok && next < b1;
+        lost |= !ok && next < b1;
+        const uint32_t going = __ballot_sync(0xffffffffu, go) & 0x11u;
         uint64_t* bar = &bars[st];
-        const int u = (lane >> 2) & 1;
-        const int c = b0 + 2 * (warp + kWarps * i) + u;
-        const int phys = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + u);
-        const bool bad = phys < 0 || phys >= a.num_blocks;
-        if (c < b1 && bad && (lane & ~4) == 0) raise_status(a.status, PKV_ERR_OOB);
-        const bool go = c < b1 && !bad;
-        const uint32_t going = __ballot_sync(0xffffffffu, go);
-        const uint32_t chunks = (going & 1) + ((going >> 4) & 1);
-        const bool stall = a.test_stall && i == 0 && warp == 0 && blockIdx.x == 0 &&
-                           blockIdx.y == 0 && blockIdx.z == 0;
-        mbar_arrive_expect_tx_if(i < my_count && lane == 0, bar,   // none: completes the phase
-                                 chunks * (2 * (SM::kSlab + R::kSide)) + (stall ? 16u : 0u));
-        const int chunk = (((bad ? 0 : phys) * a.num_kv_heads + kvh) << a.chunk_shift) +
-                          (c & ((1 << a.chunk_shift) - 1));
-        const int at = 4 * st + 2 * u + (lane & 1);
-        const void* map = lane & 1 ? static_cast<const void*>(&tm_v) : &tm_k;
-        tma_load_2d_hint_if(go && lane < 8 && !(lane & 2), ring + at * SM::kSlab, map, 0,
+        mbar_arrive_expect_tx_if(lane == 0, bar,   // of nothing: completes the phase
+                                 __popc(going) * (2 * (SM::kSlab + R::kSide)) + extra);
+        const int chunk = static_cast<int>(static_cast<uint32_t>(phys) * block_step + block_at);
+        tma_load_2d_hint_if(go && lane_tma, ring + (4 * st + lane_at) * SM::kSlab, lane_map, 0,
                             chunk * kBlk, bar, stream_policy);
-        const uint8_t* side = (lane & 1 ? qs.v : qs.k) + static_cast<int64_t>(chunk) * R::kSide;
-        bulk_g2s_hint_if(go && lane < 8 && (lane & 2), sides + at * R::kSide, side, R::kSide, bar,
+        bulk_g2s_hint_if(go && lane_side, sides + (4 * st + lane_at) * R::kSide,
+                         lane_sides + static_cast<int64_t>(chunk) * R::kSide, R::kSide, bar,
                          stream_policy);
+        next += 2 * kWarps;
     };
+    const bool stall = a.test_stall && warp == 0 && blockIdx.x == 0 && blockIdx.y == 0 &&
+                       blockIdx.z == 0;
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) issue(i);
+    for (int i = 0; i < kStages; ++i)
+        if (i < my_count) issue(i, i, stall && i == 0 ? 16u : 0u);
 
-    // q: head g, elements j E ..; scaled by 2^up into [2^14, 2^15) at its largest.
+    // q: head g, elements j E ..
     const int g8 = lane >> 2;
     const int j4 = lane & 3;
     uint32_t qb[KS][2], ql[kSplit ? KS : 1][2];
-    float q_unit;
-    {
-        float x[E];
-        float top = 0.f;
-        const T* qrow = static_cast<const T*>(a.q) +
-                        (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + (g8 < G ? g8 : 0)) *
-                            D + j4 * E;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            const float2 w = g8 < G ? load_pair(qrow + 2 * i) : make_float2(0.f, 0.f);
-            x[2 * i] = w.x;
-            x[2 * i + 1] = w.y;
-            top = fmaxf(top, fmaxf(fabsf(w.x), fabsf(w.y)));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int up = min(126, 14 + 127 - (__float_as_int(top) >> 23));   // -114 .. 126
-        q_unit = pow2f(max(-126, -up));
-        const float f = pow2f(up);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float u = x[4 * ks + 2 * h] * f, v = x[4 * ks + 2 * h + 1] * f;
-                qb[ks][h] = pack_f16x2(u, v);
-                if constexpr (kSplit)
-                    ql[ks][h] = pack_f16x2(u - f16lo_to_f32(qb[ks][h]),
-                                           v - f16hi_to_f32(qb[ks][h]));
-            }
-    }
+    const float q_unit = load_q<T, E, kSplit>(
+        static_cast<const T*>(a.q) +
+            (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + (g8 < G ? g8 : 0)) * D + j4 * E,
+        g8 < G, qb, ql);
     // Scores are held for heads 2 j, 2 j + 1 of tokens t_lo and t_lo + 2.
     const int t_lo = 4 * (g8 >> 1) + (g8 & 1);
     float hs[2];
@@ -338,20 +350,24 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int v_tok = lane & 15;
     const int v_pc = lane >> 4;
 
+    const int full_end = min(b1, L / kBlk);
+    // Pairs that reach past this have rows to clear, or the new token.
+    const int plain_end = append && b1 == nblk ? min(full_end, nblk - 1) : full_end;
     int failed_at = -1;
-    for (int i = 0; i < my_count; ++i) {
-        const int st_i = i % kStages;
-        if (!mbar_wait_warp(&bars[st_i], (i / kStages) & 1, a.status)) {
+    int st_i = 0;
+    uint32_t phase = 0;
+    int c0 = b0 + 2 * warp;
+    for (int i = 0; i < my_count; ++i, c0 += 2 * kWarps) {
+        if (!mbar_wait_warp(&bars[st_i], phase, a.status)) {
             failed_at = i;
             break;
         }
-        const int c0 = b0 + 2 * (warp + kWarps * i);
         uint8_t* slabs = ring + 4 * st_i * SM::kSlab;     // K, V of the first chunk, of the second
         uint8_t* besides = sides + 4 * st_i * R::kSide;
         const uint32_t slab0 = smem_u32(slabs), side0 = smem_u32(besides);
-        const bool full = c0 + 1 < b1 && (c0 + 2) * kBlk <= L;
+        const bool full = c0 + 2 <= full_end;
 
-        if (!full || (append && c0 + 2 >= nblk)) {
+        if (c0 + 2 > plain_end) {
             for (int u = 0; u < 2; ++u) {
                 const int blk = c0 + u;
                 const int valid = blk < b1 ? min(kBlk, L - blk * kBlk) : 0;
@@ -467,7 +483,8 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int h = 0; h < 2; ++h) {
                 const uint32_t at = side0 + 2 * u * R::kSide + R::kScales + t_lo + 2 * h;
                 const float unit = __int_as_float(lds8(at) << 23);
-                float ve = static_cast<float>(static_cast<int>(lds8(at + R::kSide)) - 127);
+                // the byte as the low digits of 2^23: one subtraction makes it a number
+                float ve = __int_as_float(lds8(at + R::kSide) | 0x4b000000) - 8388735.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) s[u][2 * h + e] *= unit * hs[e];
                 if (!full) {
@@ -577,9 +594,14 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         __syncwarp();
         const int nxt = i + kStages;
-        if ((nxt & 15) == 0 && nxt < my_count) fetch_ids(nxt);
-        issue(nxt);
+        if (nxt < my_count) {
+            if ((nxt & 15) == 0) fetch_ids(nxt);
+            issue(st_i, nxt, 0);
+        }
+        st_i = st_i + 1 < kStages ? st_i + 1 : 0;
+        phase ^= st_i == 0;
     }
+    if (lost && lane < 8 && (lane & 3) == 0) raise_status(a.status, PKV_ERR_OOB);
     if (failed_at >= 0) {
         for (int k = failed_at + 1; k < my_count && k < failed_at + kStages; ++k)
             mbar_wait_warp(&bars[k % kStages], (k / kStages) & 1, a.status);
