@@ -48,7 +48,7 @@ struct QuantSmem {
     static constexpr int kSlab = kBlk * R::kCodes;
     static constexpr int kStageBytes = 4 * (kSlab + R::kSide);   // K and V of two chunks
     // Three CTAs share an SM: as many stages as fit 64 KB or so.
-    static constexpr int kStages = kStageBytes > 8000 ? 2 : kStageBytes > 4000 ? 3 : 6;
+    static constexpr int kStages = kStageBytes > 8000 ? 2 : kStageBytes > 4000 ? (FMT == PKV_FP4 ? 2 : 3) : (FMT == PKV_FP4 ? 4 : 6);
     static constexpr int kCodeRing = kWarps * kStages * 4 * kSlab;
     static constexpr int kSideRing = kWarps * kStages * 4 * R::kSide;
     static constexpr int kBars = kWarps * kStages * 8;
@@ -217,7 +217,7 @@ PKV_DEVINL float load_q(const T* p, bool there, uint32_t (&hi)[E / 4][2],
 }
 
 template <int FMT, int D, int G, typename T>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, FMT == PKV_FP4 && sizeof(T) == 2 ? 4 : 3)
 quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a,
                     const QuantSides qs) {
