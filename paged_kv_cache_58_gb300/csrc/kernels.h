@@ -322,6 +322,9 @@ struct QuantArgs {
     uint32_t num_rows;            // rows of K (and of V) in all
     int num_kv_heads;
     int block_shift;              // log2 of the block size
+    uint32_t div_mul;             // rows to tokens or pairs (launch_quant_move fills these)
+    int div_shift;
+    bool wide;                    // rows outside the cache begin at multiples of 32 bytes
 };
 // `blocks`: by pairs, else by slot; `read`: out of the cache, else into it.
 cudaError_t launch_quant_move(const QuantArgs& a, int format, int head_dim, int dtype, bool blocks,

@@ -80,6 +80,7 @@ cudaStream_t copy_stream(int which) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // An NVTX range around each call that enqueues GPU work, named after the call, so that
@@ -1549,6 +1550,7 @@ pkv_status quant_rows(const pkv_quant_cache* cache, const int64_t* slot_mapping,
     a.v_stride = v_stride;
     a.slots = slot_mapping;
     a.num_rows = static_cast<uint32_t>(num_tokens * cache->num_kv_heads);
+    a.wide = aligned32(k) && aligned32(v) && (k_stride * es) % 32 == 0 && (v_stride * es) % 32 == 0;
     return from_cuda(pkv::launch_quant_move(a, cache->format, cache->head_dim, dtype, false, read,
                                             static_cast<cudaStream_t>(stream)));
 }
@@ -1579,6 +1581,7 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
     a.pairs = pairs;
     a.pool_blocks = pool->num_blocks;
     a.num_rows = static_cast<uint32_t>(num_pairs * per);
+    a.wide = aligned32(k) && aligned32(v);
     return from_cuda(pkv::launch_quant_move(a, cache->format, cache->head_dim, pool->dtype, true,
                                             read, static_cast<cudaStream_t>(stream)));
 }

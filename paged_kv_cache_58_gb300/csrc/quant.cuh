@@ -72,7 +72,7 @@ PKV_DEVINL float f16hi_to_f32(uint32_t w) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "r"(w));
     return r;
 }
-// Two fp32 values to the nearest e4m3 / e2m1 (ties to even, beyond the largest to the largest).
+// Two fp32 values to the nearest e4m3 (ties to even, beyond the largest to the largest).
 PKV_DEVINL uint32_t to_e4m3x2(float lo, float hi) {
     uint32_t r;
     asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %1, %2;\n\tcvt.u32.u16 %0, h;\n\t}"
@@ -80,12 +80,31 @@ PKV_DEVINL uint32_t to_e4m3x2(float lo, float hi) {
         : "f"(hi), "f"(lo));
     return r;
 }
-PKV_DEVINL uint32_t to_e2m1x2(float lo, float hi) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
-        : "=r"(r)
-        : "f"(hi), "f"(lo));
-    return r;
+// 32 bytes at once (`wide`: p is 32-byte aligned), or 16 and 16.  A lane that moves its 32 bytes in
+// two halves leaves half-written sectors to L2 (reading back 8192 tokens of 8 heads of 128 to bf16:
+// 13.5 us, 11.1 in whole sectors).
+PKV_DEVINL void load32(const void* p, bool wide, uint32_t* w) {
+    if (wide) {
+        asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+              "=r"(w[7])
+            : "l"(p));
+    } else {
+        const uint4 u = __ldg(static_cast<const uint4*>(p));
+        const uint4 v = __ldg(static_cast<const uint4*>(p) + 1);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    }
+}
+PKV_DEVINL void store32(void* p, bool wide, const uint32_t* w) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // 16 elements of a row: bf16 bits or fp32.
@@ -93,53 +112,60 @@ template <typename T>
 struct Elems16;
 template <>
 struct Elems16<uint16_t> {
-    uint4 w[2];
-    PKV_DEVINL void load(const void* p) {
-        w[0] = __ldg(static_cast<const uint4*>(p));
-        w[1] = __ldg(static_cast<const uint4*>(p) + 1);
+    uint32_t w[8];
+    PKV_DEVINL void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0;
     }
+    PKV_DEVINL void load(const void* p, bool wide) { load32(p, wide, w); }
     PKV_DEVINL void values(float (&x)[16]) const {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[8 * i + 2 * k] = bf16lo_to_f32(q[k]);
-                x[8 * i + 2 * k + 1] = bf16hi_to_f32(q[k]);
-            }
+        for (int k = 0; k < 8; ++k) {
+            x[2 * k] = bf16lo_to_f32(w[k]);
+            x[2 * k + 1] = bf16hi_to_f32(w[k]);
         }
     }
-    PKV_DEVINL static void store(void* p, const float (&x)[16]) {
+    // The largest magnitude's bits as fp32: above 0x7f800000 where there is a NaN.
+    PKV_DEVINL uint32_t top_bits() const {
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            static_cast<uint4*>(p)[i] =
-                make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]),
-                           pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                           pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
-                           pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+        for (int k = 0; k < 8; ++k) m = __vmaxu2(m, w[k] & 0x7fff7fffu);
+        return max(m << 16, m & 0xffff0000u);
+    }
+    PKV_DEVINL static void store(void* p, bool wide, const float (&x)[16]) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+        store32(p, wide, w);
     }
 };
 template <>
 struct Elems16<float> {
-    float4 w[4];
-    PKV_DEVINL void load(const void* p) {
+    uint32_t w[16];
+    PKV_DEVINL void clear() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(static_cast<const float4*>(p) + i);
+        for (int i = 0; i < 16; ++i) w[i] = 0;
+    }
+    PKV_DEVINL void load(const void* p, bool wide) {
+        load32(p, wide, w);
+        load32(static_cast<const char*>(p) + 32, wide, w + 8);
     }
     PKV_DEVINL void values(float (&x)[16]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[4 * i] = w[i].x;
-            x[4 * i + 1] = w[i].y;
-            x[4 * i + 2] = w[i].z;
-            x[4 * i + 3] = w[i].w;
-        }
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]);
     }
-    PKV_DEVINL static void store(void* p, const float (&x)[16]) {
+    PKV_DEVINL uint32_t top_bits() const {
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            static_cast<float4*>(p)[i] =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7fffffffu);
+        return m;
+    }
+    PKV_DEVINL static void store(void* p, bool wide, const float (&x)[16]) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
+        store32(p, wide, w);
+        store32(static_cast<char*>(p) + 32, wide, w + 8);
     }
 };
 
@@ -150,23 +176,53 @@ struct Quantised {
     uint32_t scale, exp;
 };
 
-// Quantises a row whose 16 elements per lane lie in x; the lanes of a row are neighbours and all
-// 32 lanes of the warp call.  EXACT_DIV: x has more than bf16's digits.
-//   NaN stays NaN (fp4: its 16 elements do); infinities take the largest value.
-template <int FMT, int D, bool EXACT_DIV>
-PKV_DEVINL Quantised quantise(const float (&x)[16]) {
+PKV_DEVINL uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+PKV_DEVINL uint32_t to_e2m1x8(const float* u) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3]), "f"(u[4]), "f"(u[5]), "f"(u[6]), "f"(u[7]));
+    return r;
+}
+
+// The least e with top <= 448 2^e = 1.75 2^(e + 8), or 2688 2^e = 1.3125 2^(e + 11), top of these
+// bits: the exponent of top less that of the largest value, one more where top's digits pass its.
+template <int FMT>
+PKV_DEVINL int row_exponent(uint32_t top) {
+    const int e = FMT == PKV_FP8 ? (static_cast<int>(top + 0x1fffffu) >> 23) - 135
+                                 : (static_cast<int>(top + 0x57ffffu) >> 23) - 138;
+    return max(-90, min(90, e));
+}
+
+// Quantises a row, 16 elements per lane; the lanes of a row are neighbours and all 32 lanes of the
+// warp call.  NaN stays NaN (fp4: its 16 elements do); infinities take the largest value.
+template <int FMT, int D, typename T>
+PKV_DEVINL Quantised quantise(const Elems16<T>& in) {
     constexpr int L = QuantRow<FMT, D>::kLanes;
-    float amax = 0.f;
+    float x[16];
+    in.values(x);
+    uint32_t own = in.top_bits();
+    const bool nan = own > 0x7f800000u;
+    if (__any_sync(0xffffffffu, nan)) {   // the others' largest, then
+        float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));   // passes over NaN
-    float top = amax;
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+        own = __float_as_uint(m);
+    }
+    uint32_t top = own;
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // The least e with top <= 448 2^e = 1.75 2^(e + 8), or 2688 2^e = 1.3125 2^(e + 11): the
-    // exponent of top less that of the largest value, one more where top's digits pass its.
-    const int bits = __float_as_int(top);
-    int e = FMT == PKV_FP8 ? ((bits + 0x1fffff) >> 23) - 135 : ((bits + 0x57ffff) >> 23) - 138;
-    e = max(-90, min(90, e));
+    for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = row_exponent<FMT>(top);
     const float unit = pow2f(-e);
     Quantised r;
     r.exp = static_cast<uint32_t>(e + 127);
@@ -174,40 +230,41 @@ PKV_DEVINL Quantised quantise(const float (&x)[16]) {
     if constexpr (FMT == PKV_FP8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r.codes[i] = to_e4m3x2(x[4 * i] * unit, x[4 * i + 1] * unit) |
-                         to_e4m3x2(x[4 * i + 2] * unit, x[4 * i + 3] * unit) << 16;
+            r.codes[i] = to_e4m3x4(x[4 * i] * unit, x[4 * i + 1] * unit, x[4 * i + 2] * unit,
+                                   x[4 * i + 3] * unit);
     } else {
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) nan |= x[i] != x[i];
-        const float a = fminf(amax * unit, 2688.f);
+        const float a = fminf(__uint_as_float(own) * unit, 2688.f);
         // A sixth in fp32: a product, exact where a sixth is a midpoint of e4m3 (6 m (1 / 6) is off
         // by 2^-25 of m before it is rounded, to m), so that ties stay ties.
         r.scale = to_e4m3x2(a * (1.f / 6.f), 0.f) & 0xffu;
         const float s = f16lo_to_f32(e4m3x2_to_f16x2(r.scale));
         if (nan) r.scale = 0x7fu;
-        const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+        // Multiplied by the scale's inverse and the row's unit, the border is met up to two units in
+        // the last place.  In bf16 an element on a border and one next to it are 2^-8 apart, so
+        // both are told apart on a grid of 2^-12 (1.5 2^11 + u), which has every border.  An fp32
+        // element may lie closer: where one is within 2^-18 of the grid of the borders, 1 / 4, all
+        // are divided (a quotient rounds to a border only where it is one: where y is a unit in its
+        // last place off b s, y / s is off b by more than half of b's).
+        const float f = s > 0.f ? unit * __fdiv_rn(1.f, s) : 0.f;
         float u[16];
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float y = x[i] * unit;
-            if constexpr (EXACT_DIV) {
-                // On a border only where y / s is: where y is a unit in its last place
-                // off it, the quotient is off by more than half of its own.
-                u[i] = s > 0.f ? __fdiv_rn(y, s) : 0.f;
-            } else {
-                // y and border * s have at most 8 digits: y inv is within 2 units of a border
-                // where y / s is on it and 2^15 away where it is not.  Dropping four digits
-                // tells the two apart.
-                u[i] = __int_as_float((__float_as_int(y * inv) + 8) & ~15);
+            for (int i = 0; i < 16; ++i) u[i] = __fadd_rn(__fmaf_rn(x[i], f, 3072.f), -3072.f);
+        } else {
+            float near = 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                u[i] = x[i] * f;
+                const float grid = __fadd_rn(__fadd_rn(u[i], 3145728.f), -3145728.f);   // of 1 / 4
+                near = fminf(near, fabsf(u[i] - grid));
+            }
+            if (__any_sync(0xffffffffu, near < 0x1p-18f)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = s > 0.f ? __fdiv_rn(x[i] * unit, s) : 0.f;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float* v = u + 8 * i;
-            r.codes[i] = to_e2m1x2(v[0], v[1]) | to_e2m1x2(v[2], v[3]) << 8 |
-                         to_e2m1x2(v[4], v[5]) << 16 | to_e2m1x2(v[6], v[7]) << 24;
-        }
+        r.codes[0] = to_e2m1x8(u);
+        r.codes[1] = to_e2m1x8(u + 8);
         r.codes[2] = r.codes[3] = 0;
     }
     return r;

@@ -136,16 +136,12 @@ __device__ __noinline__ void append_row(const DecodeArgs& a, const QuantSides& q
     using R = QuantRow<FMT, D>;
     const int which = lane / R::kLanes, ln = lane % R::kLanes;
     const bool mine = which < 2, v = which == 1;
-    float x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    if (mine) {
-        Elems16<T> in;
+    Elems16<T> in;
+    in.clear();
+    if (mine)
         in.load(static_cast<const T*>(v ? a.v_new : a.k_new) +
-                (static_cast<size_t>(seq) * a.num_kv_heads + kvh) * D + 16 * ln);
-        in.values(x);
-    }
-    const Quantised q = quantise<FMT, D, sizeof(T) == 4>(x);
+                    (static_cast<size_t>(seq) * a.num_kv_heads + kvh) * D + 16 * ln, false);
+    const Quantised q = quantise<FMT, D>(in);
     if (!mine) return;
     const int phys = __ldg(bt + (blk >> a.chunk_shift));
     const bool there = phys >= 0 && phys < a.num_blocks;
@@ -187,13 +183,10 @@ PKV_DEVINL float load_q(const T* p, bool there, uint32_t (&hi)[E / 4][2],
 #pragma unroll
     for (int i = 0; i < E / 16; ++i) {
         float v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = 0.f;
-        if (there) {
-            Elems16<T> in;
-            in.load(p + 16 * i);
-            in.values(v);
-        }
+        Elems16<T> in;
+        in.clear();
+        if (there) in.load(p + 16 * i, false);
+        in.values(v);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             x[16 * i + k] = v[k];
