@@ -62,6 +62,23 @@ PKV_DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// Both halves of a times the low (high) half of b.
+PKV_DEVINL uint32_t hmul2_lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 d;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 d, {l, l};\n\t"
+        "mul.rn.f16x2 %0, %1, d;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
+PKV_DEVINL uint32_t hmul2_hi(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 d;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 d, {h, h};\n\t"
+        "mul.rn.f16x2 %0, %1, d;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
 PKV_DEVINL float f16lo_to_f32(uint32_t w) {
     float r;
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(r) : "r"(w));

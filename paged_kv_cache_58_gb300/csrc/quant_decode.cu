@@ -94,11 +94,6 @@ PKV_DEVINL uint32_t movm_t(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-PKV_DEVINL uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-    return r;
-}
 PKV_DEVINL uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -226,9 +221,12 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     griddep_wait();
     griddep_launch_dependents();
+    // Partitions before sequences: with the first partitions of all sequences first, as the pools'
+    // decode has them, the CTAs of a wave are equally long, end together, and leave HBM idle
+    // while the next ones start (64 sequences of 512 .. 4096 tokens, fp8: 59.2 us; 56.0 so).
     const int kvh = blockIdx.x;
-    const int seq = blockIdx.y;
-    const int part = blockIdx.z;
+    const int part = blockIdx.y;
+    const int seq = blockIdx.z;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -418,7 +416,7 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
             }
         } else {
-            uint32_t va[2][E / 8], vb[2][E / 8], sa[2][E / 16], sb[2][E / 16];
+            uint32_t va[2][E / 8], vb[2][E / 8], sa[2], sb[2];   // scales: of a group, or two
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint32_t kb = slab0 + 2 * u * SM::kSlab, ksb = side0 + 2 * u * R::kSide;
@@ -427,10 +425,8 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const uint4 wb = lds128(piece_at<R::kCodes>(kb, t_lo + 2, j4));
                     va[u][0] = wa.x; va[u][1] = wa.y; va[u][2] = wa.z; va[u][3] = wa.w;
                     vb[u][0] = wb.x; vb[u][1] = wb.y; vb[u][2] = wb.z; vb[u][3] = wb.w;
-                    const uint32_t ua = e4m3x2_to_f16x2(lds16(ksb + t_lo * 8 + 2 * j4));
-                    const uint32_t ub = e4m3x2_to_f16x2(lds16(ksb + (t_lo + 2) * 8 + 2 * j4));
-                    sa[u][0] = prmt(ua, ua, 0x1010); sa[u][1] = prmt(ua, ua, 0x3232);
-                    sb[u][0] = prmt(ub, ub, 0x1010); sb[u][1] = prmt(ub, ub, 0x3232);
+                    sa[u] = e4m3x2_to_f16x2(lds16(ksb + t_lo * 8 + 2 * j4));
+                    sb[u] = e4m3x2_to_f16x2(lds16(ksb + (t_lo + 2) * 8 + 2 * j4));
                 } else {
                     const uint2 wa =
                         lds64(piece_at<R::kCodes>(kb, t_lo, j4 >> 1) + 8 * (j4 & 1));
@@ -438,10 +434,8 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         lds64(piece_at<R::kCodes>(kb, t_lo + 2, j4 >> 1) + 8 * (j4 & 1));
                     va[u][0] = wa.x; va[u][1] = wa.y;
                     vb[u][0] = wb.x; vb[u][1] = wb.y;
-                    const uint32_t ua = e4m3x2_to_f16x2(lds8(ksb + t_lo * 4 + j4));
-                    const uint32_t ub = e4m3x2_to_f16x2(lds8(ksb + (t_lo + 2) * 4 + j4));
-                    sa[u][0] = prmt(ua, ua, 0x1010);
-                    sb[u][0] = prmt(ub, ub, 0x1010);
+                    sa[u] = e4m3x2_to_f16x2(lds8(ksb + t_lo * 4 + j4));
+                    sb[u] = e4m3x2_to_f16x2(lds8(ksb + (t_lo + 2) * 4 + j4));
                 }
             }
 #pragma unroll
@@ -453,8 +447,8 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     e2m1x8_to_f16x8(vb[u][w], xb);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        xa[e] = hmul2(xa[e], sa[u][w / 2]);
-                        xb[e] = hmul2(xb[e], sb[u][w / 2]);
+                        xa[e] = w < 2 ? hmul2_lo(xa[e], sa[u]) : hmul2_hi(xa[e], sa[u]);
+                        xb[e] = w < 2 ? hmul2_lo(xb[e], sb[u]) : hmul2_hi(xb[e], sb[u]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -515,8 +509,21 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
             }
         }
-        // P^T fragments: [token][head] 8x8 tiles transposed in registers
-        uint32_t ph[2][2], pl[kSplit ? 2 : 1][2];
+        // P^T fragments: [token][head] 8x8 tiles transposed in registers, (4 j, 4 j + 1) and the two
+        // tokens after them of head g.  fp4 takes a token's weight in the low or the high half, a
+        // zero in the other: its V pairs two dimensions of a token, and each takes one of them.
+        constexpr int kPar = FMT == PKV_FP8 ? 1 : 2, kTok = FMT == PKV_FP8 ? 1 : 2;
+        uint32_t ph[2][kTok][kPar][2], pl[kSplit ? 2 : 1][kTok][kPar][2];
+        auto place = [](uint32_t (&f)[kTok][kPar][2], int h, uint32_t p) {
+            if constexpr (FMT == PKV_FP8) {
+                f[0][0][h] = p;
+            } else {
+                f[h][0][0] = p & 0xffffu;
+                f[h][0][1] = p >> 16;
+                f[h][1][0] = p << 16;
+                f[h][1][1] = p & 0xffff0000u;
+            }
+        };
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float p[4];
@@ -528,10 +535,10 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t hi = pack_f16x2(p[2 * h], p[2 * h + 1]);
-                ph[u][h] = movm_t(hi);
+                place(ph[u], h, movm_t(hi));
                 if constexpr (kSplit)
-                    pl[u][h] = movm_t(pack_f16x2(p[2 * h] - f16lo_to_f32(hi),
-                                                 p[2 * h + 1] - f16hi_to_f32(hi)));
+                    place(pl[u], h, movm_t(pack_f16x2(p[2 * h] - f16lo_to_f32(hi),
+                                                      p[2 * h + 1] - f16hi_to_f32(hi))));
             }
         }
         // O^T += V^T . P^T
@@ -549,9 +556,10 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         uint32_t a0, a1, a2, a3;
                         e4m3x4_to_f16x4(r[2 * h], a0, a2);
                         e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
-                        mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, ph[u][0], ph[u][1]);
+                        mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, ph[u][0][0][0], ph[u][0][0][1]);
                         if constexpr (kSplit)
-                            mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, pl[u][0], pl[u][1]);
+                            mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, pl[u][0][0][0],
+                                    pl[u][0][0][1]);
                     }
                 }
             } else {
@@ -569,18 +577,28 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     ldsm_t_b8(piece_at<R::kCodes>(vbase, v_tok, 2 * p2 + v_pc), r[0], r[1], r[2],
                               r[3]);
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {       // 16 dimensions: one scale a token
-                        const int mt = 4 * p2 + h;
-                        uint32_t x[4], s01, s23;
-                        e2m1x8_to_f16x8(r[h], x);       // (d, d + 1) of four tokens
-                        e4m3x4_to_f16x4(sc[mt], s01, s23);
-                        const uint32_t a0 = hmul2(prmt(x[0], x[1], 0x5410), s01);
-                        const uint32_t a1 = hmul2(prmt(x[0], x[1], 0x7632), s01);
-                        const uint32_t a2 = hmul2(prmt(x[2], x[3], 0x5410), s23);
-                        const uint32_t a3 = hmul2(prmt(x[2], x[3], 0x7632), s23);
-                        mma_f16(acc[mt], a0, a1, a2, a3, ph[u][0], ph[u][1]);
-                        if constexpr (kSplit)
-                            mma_f16(acc[mt], a0, a1, a2, a3, pl[u][0], pl[u][1]);
+                    for (int h = 0; h < 2; ++h) {       // 32 dimensions: two groups
+                        uint32_t x[4], y[4], s01, s23, z01, z23;
+                        e2m1x8_to_f16x8(r[2 * h], x);       // (d, d + 1) of four tokens
+                        e2m1x8_to_f16x8(r[2 * h + 1], y);   // (d + 16, d + 17)
+                        const int g0 = 4 * p2 + 2 * h;      // scales of those tokens
+                        e4m3x4_to_f16x4(sc[g0], s01, s23);
+                        e4m3x4_to_f16x4(sc[g0 + 1], z01, z23);
+                        x[0] = hmul2_lo(x[0], s01); x[1] = hmul2_hi(x[1], s01);
+                        x[2] = hmul2_lo(x[2], s23); x[3] = hmul2_hi(x[3], s23);
+                        y[0] = hmul2_lo(y[0], z01); y[1] = hmul2_hi(y[1], z01);
+                        y[2] = hmul2_lo(y[2], z23); y[3] = hmul2_hi(y[3], z23);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w)
+#pragma unroll
+                            for (int odd = 0; odd < 2; ++odd) {
+                                float(&o)[4] = acc[g0 + odd];
+                                mma_f16(o, x[2 * w], y[2 * w], x[2 * w + 1], y[2 * w + 1],
+                                        ph[u][w][odd][0], ph[u][w][odd][1]);
+                                if constexpr (kSplit)
+                                    mma_f16(o, x[2 * w], y[2 * w], x[2 * w + 1], y[2 * w + 1],
+                                            pl[u][w][odd][0], pl[u][w][odd][1]);
+                            }
                     }
                 }
             }
@@ -625,10 +643,11 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
                 float* row = macc + (warp * G + h) * D;
-                // fp4 hands out two neighbouring dimensions a register, fp8 two 8 apart
-                const int d0 = FMT == PKV_FP8 ? 16 * mt + g8 : 16 * mt + 2 * g8;
+                // fp8: dimensions 16 mt + g and + 8.  fp4: the even or the odd ones of 32, + 16
+                const int d0 = FMT == PKV_FP8 ? 16 * mt + g8
+                                              : 32 * (mt >> 1) + 2 * g8 + (mt & 1);
                 row[d0] = acc[mt][hh] * inv[hh];
-                row[d0 + (FMT == PKV_FP8 ? 8 : 1)] = acc[mt][2 + hh] * inv[hh];
+                row[d0 + (FMT == PKV_FP8 ? 8 : 16)] = acc[mt][2 + hh] * inv[hh];
             }
             if (g8 == 0) {
                 mm[warp * G + h] = my_count > 0 ? m_ref[hh] : -INFINITY;
@@ -676,7 +695,7 @@ cudaError_t launch_quant(const DecodeArgs& a, const QuantSides& qs, cudaStream_t
     auto kern = quant_decode_kernel<FMT, D, G, T>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), SM::kTotal);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(a.num_kv_heads, a.num_seqs, a.max_parts), dim3(kThreads), SM::kTotal,
+    e = launch_pdl(kern, dim3(a.num_kv_heads, a.max_parts, a.num_seqs), dim3(kThreads), SM::kTotal,
                    stream, mk, mv, a, qs);
     if (e != cudaSuccess || a.max_parts == 1) return e;
     return launch_decode_combine(a, sizeof(T) == 4 ? PKV_F32 : PKV_BF16, D, stream);
