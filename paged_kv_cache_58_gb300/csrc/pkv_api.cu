@@ -1586,11 +1586,24 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
                                             read, static_cast<cudaStream_t>(stream)));
 }
 
-int quant_partition(const pkv_quant_cache* cache, int num_seqs, int num_q_heads, int max_context,
+// Partition of a decode over a quantised cache, in pool blocks.  As long as 256 chunks (4096 tokens)
+// where that leaves 4096 CTAs, about nine for each that is resident: a CTA's start and its merge
+// cost about as much as 16 chunks a warp (16 sequences of 16k .. 128k tokens: 401 us in fp8 and 343 in
+// fp4, with 128 chunks 405 and 353).  Else down to 64 chunks, where more, shorter ones cost more
+// than they balance (64 of 512 .. 4096: 55.4 and 55.9 us; 40 chunks 58.0 and 57.5, 128 chunks 56.3 and
+// 61.3), and below that only while an SM would have fewer than three.  A multiple of 8 chunks (a pair
+// for each warp), and at most 512 partitions.
+int quant_partition(const pkv_quant_cache* cache, int num_seqs, int max_context,
                     int partition_blocks) {
-    return partition_blocks ? partition_blocks
-                            : auto_partition(num_seqs, num_q_heads, max_context,
-                                             cache->block_size);
+    if (partition_blocks) return partition_blocks;
+    const int64_t rows = static_cast<int64_t>(num_seqs) * cache->num_kv_heads;
+    const int chunks = ceil_div(max_context, kChunk);
+    const int least = ceil_div(ceil_div(chunks, 512), 8) * 8;
+    auto halved = [](int pc) { return (pc / 2 + 7) / 8 * 8; };
+    int pc = std::max(256, least);
+    while (pc > 64 && halved(pc) >= least && rows * ceil_div(chunks, pc) < 4096) pc = halved(pc);
+    while (pc > 8 && halved(pc) >= least && rows * ceil_div(chunks, pc) < 3 * 152) pc = halved(pc);
+    return pc >> chunk_shift(cache->block_size);
 }
 
 }  // namespace
@@ -1658,7 +1671,7 @@ size_t pkv_paged_decode_quant_workspace_bytes(const pkv_quant_cache* cache, int 
     if (check_quant(cache) != PKV_OK || num_seqs <= 0 || num_q_heads <= 0 || max_context <= 0 ||
         partition_blocks < 0)
         return 0;
-    const int pb = quant_partition(cache, num_seqs, num_q_heads, max_context, partition_blocks);
+    const int pb = quant_partition(cache, num_seqs, max_context, partition_blocks);
     return decode_workspace(num_seqs, num_q_heads, cache->head_dim,
                             ceil_div(ceil_div(max_context, cache->block_size), pb));
 }
@@ -1689,7 +1702,7 @@ pkv_status pkv_paged_decode_quant(const pkv_quant_cache* cache, int dtype, void*
     const int group = num_q_heads / cache->num_kv_heads;
     if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
     if (num_seqs > 65535 || max_blocks_per_seq > INT32_MAX / 64) return PKV_ERR_UNSUPPORTED;
-    const int pb = quant_partition(cache, num_seqs, num_q_heads, max_context, partition_blocks);
+    const int pb = quant_partition(cache, num_seqs, max_context, partition_blocks);
     if (pb > INT32_MAX / 64) return PKV_ERR_UNSUPPORTED;
     const int max_parts = ceil_div(ceil_div(max_context, B), pb);
     if (max_parts > pkv::kMaxParts) return PKV_ERR_UNSUPPORTED;

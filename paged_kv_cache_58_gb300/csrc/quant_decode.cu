@@ -345,10 +345,13 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     // Pairs that reach past this have rows to clear, or the new token.
     const int plain_end = append && b1 == nblk ? min(full_end, nblk - 1) : full_end;
     int failed_at = -1;
-    int st_i = 0;
     uint32_t phase = 0;
     int c0 = b0 + 2 * warp;
-    for (int i = 0; i < my_count; ++i, c0 += 2 * kWarps) {
+    for (int i0 = 0; i0 < my_count && failed_at < 0; i0 += kStages, phase ^= 1) {
+#pragma unroll
+    for (int st_i = 0; st_i < kStages; ++st_i, c0 += 2 * kWarps) {
+        const int i = i0 + st_i;
+        if (i >= my_count) break;
         if (!mbar_wait_warp(&bars[st_i], phase, a.status)) {
             failed_at = i;
             break;
@@ -609,8 +612,7 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
             if ((nxt & 15) == 0) fetch_ids(nxt);
             issue(st_i, nxt, 0);
         }
-        st_i = st_i + 1 < kStages ? st_i + 1 : 0;
-        phase ^= st_i == 0;
+    }
     }
     if (lost && lane < 8 && (lane & 3) == 0) raise_status(a.status, PKV_ERR_OOB);
     if (failed_at >= 0) {
