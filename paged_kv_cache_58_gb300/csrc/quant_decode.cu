@@ -1,9 +1,11 @@
 // Paged decode over a quantised cache (fp8 or fp4 rows), on the tensor cores.
 //
-// The work split is that of the decode over bf16 pools (paged_decode_tc.cu): one CTA per
-// (partition, kv head, sequence), four warps, warp w takes every 4th 16-token chunk of the
-// partition through a ring of stages of its own, keeps its own online softmax, and the states
-// merge at the end; partitions merge in the combine kernel.  A chunk is
+// One CTA per (partition, kv head, sequence), as over bf16 pools (paged_decode_tc.cu): warp w of four
+// takes the pairs of 16-token chunks w, w + 4, ... of the partition through a ring of stages of its
+// own and keeps its own online softmax, one step for the 32 tokens of a pair; the four states
+// merge at the end, and partitions merge in the combine kernel.  (Chunk by chunk: 16 sequences of
+// 16k .. 128k tokens, 8 query heads to a kv head, 445 us in fp8 and 490 in fp4; 428 and 406 in
+// pairs.)  A chunk is
 //   S^T[16 tokens x 8 heads] = K[16 x D] . q^T,   O^T[D x 8 heads] += V^T[D x 16] . P^T
 // as fp16 MMAs m16n8k16 with fp32 sums.  fp16, because every e4m3 value is one of fp16, and so is
 // every product of an e2m1 value and its e4m3 scale (6 digits, 2^-10 or more): what the MMAs
@@ -17,8 +19,15 @@
 // m is a whole number, raised only where a weight would pass 2^15 (exact: the weights stay in
 // fp16's range, the largest at 2^6 or more), and a warp hands on log2 of its denominator's
 // power of two with m, so that neither end of the exponents' range (-90 .. 90) is lost.
-// q is scaled by a power of two into fp16's range; fp32 q, and the weights, are split into two
-// fp16 parts (fp32 output: 22 digits).
+// q is scaled by a power of two into fp16's range.  For fp32, q and the weights are split into two
+// fp16 parts (22 digits).  A bf16 output takes its weights in one: 11 digits, three more than it
+// has itself, and the denominator sums them unrounded; a second part costs 8 MMAs a chunk.
+//
+// Bound.  fp8: HBM (16 x 16k .. 128k tokens: 401 us, 7.0 TB/s; 64 x 512 .. 4096: 55 us, 5.6 TB/s, a
+// sixth of it the first copies, the ends of CTAs and the combine).  fp4: issue slots.  Its bytes
+// would take 235 us where it takes 343: 390 warp instructions a chunk, 128 of them to make fp16 of
+// 4096 codes (two values each for cvt.f16x2.e2m1x2 and for the product with the scale), issued at
+// 2.7 of 4 a clock.
 //
 // Fragments.  The index that an MMA sums over may be in any order, if both sides share it.  So
 // lane (g, j) = (lane / 4, lane % 4) takes elements j D / 4 .. of K's row as they lie, and the
@@ -46,9 +55,10 @@ template <int FMT, int D, int G>
 struct QuantSmem {
     using R = QuantRow<FMT, D>;
     static constexpr int kSlab = kBlk * R::kCodes;
-    static constexpr int kStageBytes = 4 * (kSlab + R::kSide);   // K and V of two chunks
-    // Three CTAs share an SM: as many stages as fit 64 KB or so.
-    static constexpr int kStages = kStageBytes > 8000 ? 2 : kStageBytes > 4000 ? (FMT == PKV_FP4 ? 2 : 3) : (FMT == PKV_FP4 ? 4 : 6);
+    // A stage: K and V of two chunks.  The loop is unrolled over the stages, and past two its code
+    // costs more than copies further ahead bring (head_dim 64, 64 sequences of 512 .. 4096 tokens,
+    // fp8 and fp4: 39.4 and 39.5 us; 4 and 6 stages 42.2 and 49.0).
+    static constexpr int kStages = 2;
     static constexpr int kCodeRing = kWarps * kStages * 4 * kSlab;
     static constexpr int kSideRing = kWarps * kStages * 4 * R::kSide;
     static constexpr int kBars = kWarps * kStages * 8;
@@ -204,8 +214,14 @@ PKV_DEVINL float load_q(const T* p, bool there, uint32_t (&hi)[E / 4][2],
     return pow2f(max(-126, -up));
 }
 
+// CTAs that share an SM: four where a CTA's rings (66 KB for fp8 rows of 128) and 128 registers a
+// thread leave room for them (fp4, head_dim 128, 16 x 16k .. 128k tokens: 372 us, 388 with three;
+// fp8, head_dim 64, 64 x 512 .. 4096: 36.8 us, 39.4; five, of 96 registers: 417 and 37.5).
+template <int FMT, int D, typename T>
+constexpr int kCtas = sizeof(T) == 2 && (FMT == PKV_FP4 || D == 64) ? 4 : 3;
+
 template <int FMT, int D, int G, typename T>
-__global__ void __launch_bounds__(kThreads, FMT == PKV_FP4 && sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, kCtas<FMT, D, T>)
 quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a,
                     const QuantSides qs) {
