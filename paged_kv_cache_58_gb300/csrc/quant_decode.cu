@@ -63,7 +63,7 @@ struct QuantSmem {
     static constexpr int kSideRing = kWarps * kStages * 4 * R::kSide;
     static constexpr int kBars = kWarps * kStages * 8;
     // merge scratch reuses the rings once every warp is done
-    static constexpr int kMerge = kWarps * G * D * 4 + 2 * kWarps * G * 4;
+    static constexpr int kMerge = kWarps * G * D * 4 + 3 * kWarps * G * 4;
     static constexpr int kBody = kCodeRing + kSideRing > kMerge ? kCodeRing + kSideRing : kMerge;
     static constexpr int kTotal = kBody + kBars + 1024;   // + alignment slack
     static_assert(kBody % 8 == 0 && R::kSide % 16 == 0, "alignment");
@@ -674,31 +674,39 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
     }
     __syncthreads();
-
-    for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
-        const int g = idx / D;
-        const int d = idx % D;
-        float M = -INFINITY;
+    // What each warp's output counts, of all four denominators.
+    const size_t row0 = static_cast<size_t>(seq) * a.num_q_heads + kvh * G;
+    const bool whole = a.max_parts == 1;
+    float* share = ml + kWarps * G;                          // [W][G]
+    if (threadIdx.x < G) {
+        const int g = threadIdx.x;
+        float M = -INFINITY, l = 0.f, f[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * G + g]);
-        float o = 0.f, l = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = fast_exp2(mm[w * G + g] - M) * ml[w * G + g];
-            o = fmaf(f, macc[(w * G + g) * D + d], o);
-            l += f;
+            f[w] = fast_exp2(mm[w * G + g] - M) * ml[w * G + g];
+            l += f[w];
         }
-        const size_t row = static_cast<size_t>(seq) * a.num_q_heads + kvh * G + g;
-        if (a.max_parts == 1) {
-            store_out(static_cast<T*>(a.out) + row * D + d, o / l);
-        } else {
-            const size_t pr = row * a.max_parts + part;
-            a.o_part[pr * D + d] = l == 0.f ? 0.f : o / l;
-            if (d == 0) {
-                a.m_part[pr] = M;
-                a.l_part[pr] = l;
-            }
+        // no weight at all: 0 / 0, as the softmax has it, but in a part of a row zeros
+        const float inv_l = !whole && l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) share[w * G + g] = f[w] * inv_l;
+        if (!whole) {
+            a.m_part[(row0 + g) * a.max_parts + part] = M;
+            a.l_part[(row0 + g) * a.max_parts + part] = l;
         }
+    }
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
+        const int g = idx / D;
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) o = fmaf(share[w * G + g], macc[w * G * D + idx], o);
+        if (whole)
+            store_out(static_cast<T*>(a.out) + row0 * D + idx, o);
+        else
+            a.o_part[((row0 + g) * a.max_parts + part) * D + idx % D] = o;
     }
 }
 
