@@ -102,10 +102,12 @@ PKV_DEVINL uint32_t to_e4m3x2(float lo, float hi) {
 // 13.5 us, 11.1 in whole sectors).
 PKV_DEVINL void load32(const void* p, bool wide, uint32_t* w) {
     if (wide) {
-        asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
-              "=r"(w[7])
-            : "l"(p));
+        // volatile: it stays behind the wait for the kernel before
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                       "=r"(w[6]), "=r"(w[7])
+                     : "l"(p)
+                     : "memory");
     } else {
         const uint4 u = __ldg(static_cast<const uint4*>(p));
         const uint4 v = __ldg(static_cast<const uint4*>(p) + 1);
@@ -266,13 +268,13 @@ PKV_DEVINL Quantised quantise(const Elems16<T>& in) {
         float u[16];
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = __fadd_rn(__fmaf_rn(x[i], f, 3072.f), -3072.f);
+            for (int i = 0; i < 16; ++i) u[i] = __fadd_rn(__fmaf_rn(x[i], f, 0x1.8p11f), -0x1.8p11f);
         } else {
             float near = 1.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 u[i] = x[i] * f;
-                const float grid = __fadd_rn(__fadd_rn(u[i], 3145728.f), -3145728.f);   // of 1 / 4
+                const float grid = __fadd_rn(__fadd_rn(u[i], 0x1.8p21f), -0x1.8p21f);   // of 1 / 4
                 near = fminf(near, fabsf(u[i] - grid));
             }
             if (__any_sync(0xffffffffu, near < 0x1p-18f)) {
