@@ -152,16 +152,6 @@ PKV_DEVINL void bulk_g2s_hint(void* smem_dst, const void* gmem_src, uint32_t byt
         : "memory");
 }
 
-PKV_DEVINL void bulk_g2s_hint_if(bool on, void* smem_dst, const void* gmem_src, uint32_t bytes,
-                                 uint64_t* bar, uint64_t policy) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1], %2, [%3], %4;\n\t}" ::"r"(smem_u32(smem_dst)),
-        "l"(gmem_src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy), "r"(static_cast<uint32_t>(on))
-        : "memory");
-}
-
 // 2-D tiled tensor copy global -> shared through a tensor map (coordinates in
 // elements, innermost first).
 PKV_DEVINL void tma_load_3d(void* smem_dst, const void* tmap, int32_t x, int32_t y, int32_t z,

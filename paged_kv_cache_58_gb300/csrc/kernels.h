@@ -132,9 +132,6 @@ bool make_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int head_dim)
 // 2 column halves, rows / 8 row groups}, box {64, 8, 2, 2} = 4 KB, landing in shared
 // memory as [row group][half][8 rows][128 B] with the 128-byte swizzle.
 bool make_pool_block_map(CUtensorMap* m, const void* pool, int64_t rows);
-// The codes of a quantised cache: rows of row_bytes (128, 64 or 32), box 16 rows, swizzled over
-// the length of a row.
-bool make_codes_map(CUtensorMap* m, const void* codes, int64_t rows, int row_bytes);
 // cudaFuncSetAttribute(kern, MaxDynamicSharedMemorySize, bytes), made once per kernel and
 // device (later calls with no more bytes return at once).
 cudaError_t set_smem_once(const void* kern, int bytes);

@@ -1484,7 +1484,7 @@ pkv_status check_quant(const pkv_quant_cache* c) {
     if (chunk_shift(c->block_size) < 0) return PKV_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (c->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
-    // a row's index is a TMA coordinate
+    // the kernels count rows in 32 bits
     if (c->num_blocks > INT32_MAX / (static_cast<int64_t>(c->num_kv_heads) * c->block_size))
         return PKV_ERR_UNSUPPORTED;
     return PKV_OK;

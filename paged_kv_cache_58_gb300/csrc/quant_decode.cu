@@ -23,18 +23,22 @@
 // fp16 parts (22 digits).  A bf16 output takes its weights in one: 11 digits, three more than it
 // has itself, and the denominator sums them unrounded; a second part costs 8 MMAs a chunk.
 //
-// Bound.  fp8: HBM (16 x 16k .. 128k tokens: 401 us, 7.0 TB/s; 64 x 512 .. 4096: 55 us, 5.6 TB/s, a
+// Copies.  A pair's 4 to 8 KB come 16 bytes a lane (cp.async, swizzled by the lane, counted on an
+// mbarrier), 512 bytes an instruction.  As eight bulk and tensor copies a pair, each lane's own and
+// so issued one after the other, they took 30 instructions more: 402 and 345 us where this takes 397
+// and 336, and tensor maps for every call's arrays.
+//
+// Bound.  fp8: HBM (16 x 16k .. 128k tokens: 397 us, 7.1 TB/s; 64 x 512 .. 4096: 54 us, 5.8 TB/s, a
 // sixth of it the first copies, the ends of CTAs and the combine).  fp4: issue slots.  Its bytes
-// would take 235 us where it takes 343: 390 warp instructions a chunk, 128 of them to make fp16 of
+// would take 235 us where it takes 336: 362 warp instructions a chunk, 128 of them to make fp16 of
 // 4096 codes (two values each for cvt.f16x2.e2m1x2 and for the product with the scale), issued at
-// 2.7 of 4 a clock.
+// 2.6 of 4 a clock.
 //
 // Fragments.  The index that an MMA sums over may be in any order, if both sides share it.  So
 // lane (g, j) = (lane / 4, lane % 4) takes elements j D / 4 .. of K's row as they lie, and the
 // same of q; V^T comes out of ldmatrix .m16n16.trans.b8 with 4 tokens of one dimension (fp4: of
 // two) in a register, tokens 4 j .. 4 j + 3; row g of S^T is token 4 (g / 2) + g % 2 and row
 // g + 8 the token two further, which is the order in which movmatrix hands the weights on.
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -74,6 +78,17 @@ PKV_DEVINL void ldsm_t_b8(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r
     asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                  : "r"(addr));
+}
+// 16 bytes from global to shared memory, or 16 zeros (bytes == 0: src is not read).
+PKV_DEVINL void copy16(uint32_t dst, const uint8_t* src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+                 "l"(src), "r"(bytes), "l"(policy)
+                 : "memory");
+}
+// This thread arrives at `bar` once its copies so far have landed.
+PKV_DEVINL void arrive_with_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 PKV_DEVINL uint4 lds128(uint32_t addr) {
     uint4 r;
@@ -119,8 +134,8 @@ PKV_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Where the 16-byte piece c of row t of a slab lies: the copy's swizzle (128, 64 or 32 bytes,
-// the length of a row).
+// Where the 16-byte piece c of row t of a slab lies: swizzled so that eight rows' pieces c, and four
+// pieces of two rows, lie in banks of their own.
 template <int ROW>
 PKV_DEVINL uint32_t piece_at(uint32_t base, int t, int c) {
     const int f = ROW == 128 ? t & 7 : ROW == 64 ? (t >> 1) & 3 : (t >> 2) & 1;
@@ -222,9 +237,7 @@ constexpr int kCtas = sizeof(T) == 2 && (FMT == PKV_FP4 || D == 64) ? 4 : 3;
 
 template <int FMT, int D, int G, typename T>
 __global__ void __launch_bounds__(kThreads, kCtas<FMT, D, T>)
-quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a,
-                    const QuantSides qs) {
+quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
     using SM = QuantSmem<FMT, D, G>;
     using R = QuantRow<FMT, D>;
     constexpr int KS = D / 16;            // k-steps of the scores, m-tiles of P.V
@@ -281,12 +294,9 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint8_t* sides = smem + SM::kCodeRing + warp * kStages * 4 * R::kSide;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBody) + warp * kStages;
     if (lane == 0) {
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 32);
         fence_mbar_init();
-        fence_proxy_async_smem();
     }
     __syncwarp();
 
@@ -296,39 +306,53 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int c = my_first + 2 * kWarps * base;
         ids = c < b1 ? __ldg(bt + (c >> a.chunk_shift)) : -1;
     };
-    // Stage st, pair i: lanes 0 .. 3 copy the first chunk's K and V codes and what lies beside each,
-    // lanes 4 .. 7 the second one's.  What does not change from pair to pair is kept.
-    const int cu = (lane >> 2) & 1;
-    const bool lane_tma = lane < 8 && !(lane & 2), lane_side = lane < 8 && (lane & 2);
-    const void* lane_map = lane & 1 ? static_cast<const void*>(&tm_v) : &tm_k;
-    const uint8_t* lane_sides = lane & 1 ? qs.v : qs.k;
-    const int lane_at = 2 * cu + (lane & 1);
+    // Pair i into stage st, 16 bytes a lane and copy: 512 bytes of codes lie in 4, 8 or 16 rows.
+    constexpr int kPieces = R::kCodes / 16;    // of a row
+    const int lane_row = lane / kPieces, lane_pc = lane % kPieces;
+    const uint8_t* codes[2] = {static_cast<const uint8_t*>(a.k_pool) + 16 * lane,
+                               static_cast<const uint8_t*>(a.v_pool) + 16 * lane};
+    const uint32_t lane_dst = smem_u32(ring) + piece_at<R::kCodes>(0, lane_row, lane_pc);
+    // What lies beside a chunk's K and V: lanes 0 .. and as many after them.
+    constexpr int kSidePieces = R::kSide / 16;
+    const int side_v = lane / kSidePieces, side_pc = lane % kSidePieces;
+    const bool lane_side = side_v < 2;
+    const uint8_t* side_src = (side_v == 1 ? qs.v : qs.k) + 16 * side_pc;
+    const uint32_t side_dst = smem_u32(sides) + (side_v & 1) * R::kSide + 16 * side_pc;
     const int block_step = a.num_kv_heads << a.chunk_shift;
-    const int block_at = (kvh << a.chunk_shift) + (a.chunk_shift & cu);   // b0 is even there
+    const int block_at = kvh << a.chunk_shift;
     bool lost = false;   // a block id outside the pool
-    int next = b0 + 2 * warp + cu;   // the lane's chunk of the next pair
-    auto issue = [&](int st, int i, uint32_t extra) {
-        const int phys = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + cu);
-        const bool ok = static_cast<uint32_t>(phys) < static_cast<uint32_t>(a.num_blocks);
-        const bool go = ok && next < b1;
-        lost |= !ok && next < b1;
-        const uint32_t going = __ballot_sync(0xffffffffu, go) & 0x11u;
-        uint64_t* bar = &bars[st];
-        mbar_arrive_expect_tx_if(lane == 0, bar,   // of nothing: completes the phase
-                                 __popc(going) * (2 * (SM::kSlab + R::kSide)) + extra);
-        const int chunk = static_cast<int>(static_cast<uint32_t>(phys) * block_step + block_at);
-        tma_load_2d_hint_if(go && lane_tma, ring + (4 * st + lane_at) * SM::kSlab, lane_map, 0,
-                            chunk * kBlk, bar, stream_policy);
-        bulk_g2s_hint_if(go && lane_side, sides + (4 * st + lane_at) * R::kSide,
-                         lane_sides + static_cast<int64_t>(chunk) * R::kSide, R::kSide, bar,
-                         stream_policy);
+    int next = b0 + 2 * warp;   // the next pair's first chunk
+    auto issue = [&](int st, int i, bool arrive) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int phys = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + u);
+            const bool there = u == 0 || next + 1 < b1;
+            const bool ok = static_cast<uint32_t>(phys) < static_cast<uint32_t>(a.num_blocks);
+            lost |= there && !ok;
+            const uint32_t bytes = there && ok ? 16u : 0u;
+            // (blocks of two chunks: b0 is even there)
+            const int chunk = (ok ? phys : 0) * block_step + block_at + (a.chunk_shift & u);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint8_t* src = codes[kv] + static_cast<int64_t>(chunk) * SM::kSlab;
+                const uint32_t dst = lane_dst + (4 * st + 2 * u + kv) * SM::kSlab;
+#pragma unroll
+                for (int p = 0; p < SM::kSlab / 512; ++p)   // rows of 128: four on turn the swizzle
+                    copy16((R::kCodes == 128 && (p & 1) ? dst ^ 64 : dst) + 512 * p, src + 512 * p,
+                           bytes, stream_policy);
+            }
+            if (lane_side)
+                copy16(side_dst + (4 * st + 2 * u) * R::kSide,
+                       side_src + static_cast<int64_t>(chunk) * R::kSide, bytes, stream_policy);
+        }
+        if (arrive) arrive_with_copies(&bars[st]);
         next += 2 * kWarps;
     };
     const bool stall = a.test_stall && warp == 0 && blockIdx.x == 0 && blockIdx.y == 0 &&
                        blockIdx.z == 0;
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
-        if (i < my_count) issue(i, i, stall && i == 0 ? 16u : 0u);
+        if (i < my_count) issue(i, i, !(stall && i == 0 && lane == 0));
 
     // q: head g, elements j E ..
     const int g8 = lane >> 2;
@@ -387,8 +411,7 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                 uint8_t* vsd = ksd + R::kSide;
                 // Rows past the context may hold anything (an fp8 NaN, an fp4 scale that is
                 // one): zero V's, so that a weight of zero adds zero.
-                constexpr int kPieces = R::kCodes / 16;
-                for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
+                    for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
                     *reinterpret_cast<uint4*>(vst + piece_at<R::kCodes>(0, valid + idx / kPieces,
                                                                         idx % kPieces)) =
                         make_uint4(0, 0, 0, 0);
@@ -400,7 +423,6 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                     append_row<FMT, D, T>(a, qs, seq, kvh, blk, valid - 1, bt, lane, kst, vst, ksd,
                                           vsd);
             }
-            fence_proxy_async_smem();
             __syncwarp();
         }
 
@@ -626,12 +648,13 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int nxt = i + kStages;
         if (nxt < my_count) {
             if ((nxt & 15) == 0) fetch_ids(nxt);
-            issue(st_i, nxt, 0);
+            issue(st_i, nxt, true);
         }
     }
     }
-    if (lost && lane < 8 && (lane & 3) == 0) raise_status(a.status, PKV_ERR_OOB);
+    if (lost && lane == 0) raise_status(a.status, PKV_ERR_OOB);
     if (failed_at >= 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
         for (int k = failed_at + 1; k < my_count && k < failed_at + kStages; ++k)
             mbar_wait_warp(&bars[k % kStages], (k / kStages) & 1, a.status);
     }
@@ -713,16 +736,11 @@ quant_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 template <int FMT, int D, int G, typename T>
 cudaError_t launch_quant(const DecodeArgs& a, const QuantSides& qs, cudaStream_t stream) {
     using SM = QuantSmem<FMT, D, G>;
-    CUtensorMap mk, mv;
-    const int64_t rows = a.num_blocks * a.num_kv_heads * (kBlk << a.chunk_shift);
-    if (!make_codes_map(&mk, a.k_pool, rows, QuantRow<FMT, D>::kCodes) ||
-        !make_codes_map(&mv, a.v_pool, rows, QuantRow<FMT, D>::kCodes))
-        return cudaErrorInvalidValue;
     auto kern = quant_decode_kernel<FMT, D, G, T>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), SM::kTotal);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(a.num_kv_heads, a.max_parts, a.num_seqs), dim3(kThreads), SM::kTotal,
-                   stream, mk, mv, a, qs);
+                   stream, a, qs);
     if (e != cudaSuccess || a.max_parts == 1) return e;
     return launch_decode_combine(a, sizeof(T) == 4 ? PKV_F32 : PKV_BF16, D, stream);
 }

@@ -32,7 +32,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // path.  A map holds only the address, sizes and box, so it does not depend on the
 // device, and a reused address with the same sizes encodes to the same map.
 struct MapEntry {
-    int kind;   // 0: make_pool_map, 1: make_pool_block_map, 2: make_codes_map
+    int kind;   // 0: make_pool_map, 1: make_pool_block_map
     const void* ptr;
     int64_t rows;
     int head_dim;
@@ -101,25 +101,6 @@ bool make_pool_block_map(CUtensorMap* m, const void* pool, int64_t rows) {
     if (cached_map(1, pool, rows, 128, m)) return true;
     if (!encode_pool_block_map(m, pool, rows)) return false;
     remember_map(1, pool, rows, 128, *m);
-    return true;
-}
-
-bool make_codes_map(CUtensorMap* m, const void* codes, int64_t rows, int row_bytes) {
-    if (cached_map(2, codes, rows, row_bytes, m)) return true;
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), 16};
-    cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapSwizzle swizzle = row_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                       : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                         : CU_TENSOR_MAP_SWIZZLE_32B;
-    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    remember_map(2, codes, rows, row_bytes, *m);
     return true;
 }
 
