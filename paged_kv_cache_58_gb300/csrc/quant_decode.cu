@@ -411,7 +411,7 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
                 uint8_t* vsd = ksd + R::kSide;
                 // Rows past the context may hold anything (an fp8 NaN, an fp4 scale that is
                 // one): zero V's, so that a weight of zero adds zero.
-                    for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
+                for (int idx = lane; idx < (kBlk - valid) * kPieces; idx += 32)
                     *reinterpret_cast<uint4*>(vst + piece_at<R::kCodes>(0, valid + idx / kPieces,
                                                                         idx % kPieces)) =
                         make_uint4(0, 0, 0, 0);
