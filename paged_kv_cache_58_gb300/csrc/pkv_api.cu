@@ -1588,10 +1588,10 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
 
 // Partition of a decode over a quantised cache, in pool blocks.  As long as 256 chunks (4096 tokens)
 // where that leaves 4096 CTAs, about nine for each that is resident: a CTA's start and its merge
-// cost about as much as 16 chunks a warp (16 sequences of 16k .. 128k tokens: 401 us in fp8 and 343 in
-// fp4, with 128 chunks 405 and 353).  Else down to 64 chunks, where more, shorter ones cost more
-// than they balance (64 of 512 .. 4096: 55.4 and 55.9 us; 40 chunks 58.0 and 57.5, 128 chunks 56.3 and
-// 61.3), and below that only while an SM would have fewer than three.  A multiple of 8 chunks (a pair
+// cost about as much as 16 chunks a warp (16 sequences of 16k .. 128k tokens: 401 us in fp8 and 335 in
+// fp4, with 128 chunks 407 and 347).  Else down to 64 chunks, where more, shorter ones cost more
+// than they balance (64 of 512 .. 4096: 54.4 and 54.9 us; 40 chunks 56.0 and 56.6, 128 chunks 55.4 and
+// 59.1), and below that only while an SM would have fewer than three.  A multiple of 8 chunks (a pair
 // for each warp), and at most 512 partitions.
 int quant_partition(const pkv_quant_cache* cache, int num_seqs, int max_context,
                     int partition_blocks) {
