@@ -19,9 +19,10 @@
 // m is a whole number, raised only where a weight would pass 2^15 (exact: the weights stay in
 // fp16's range, the largest at 2^6 or more), and a warp hands on log2 of its denominator's
 // power of two with m, so that neither end of the exponents' range (-90 .. 90) is lost.
-// q is scaled by a power of two into fp16's range.  For fp32, q and the weights are split into two
-// fp16 parts (22 digits).  A bf16 output takes its weights in one: 11 digits, three more than it
-// has itself, and the denominator sums them unrounded; a second part costs 8 MMAs a chunk.
+// q is scaled by a power of two into fp16's range, for fp32 in two fp16 parts.  A weight is two
+// fp16 parts (22 digits; in one it was off by up to 2^-12, and V's of one sign add that up).  The
+// low parts take MMAs of their own for groups of 8 heads, and for smaller ones the idle columns 4 ..
+// 7, whose sums join at the end.
 //
 // Copies.  A pair's 4 to 8 KB come 16 bytes a lane (cp.async, swizzled by the lane, counted on an
 // mbarrier), 512 bytes an instruction.  As eight bulk and tensor copies a pair, each lane's own and
@@ -142,6 +143,13 @@ PKV_DEVINL uint32_t piece_at(uint32_t base, int t, int c) {
     return base + t * ROW + ((c ^ f) << 4);
 }
 
+// Four tokens' bytes of two fp4 codes (dimensions d, d + 1): the codes in pairs of tokens, of d and of
+// d + 1 in turn (a swap of the middle two codes of each half).
+PKV_DEVINL uint32_t pair_tokens(uint32_t r) {
+    const uint32_t t = (r ^ (r >> 4)) & 0x00f000f0u;
+    return r ^ (t * 17u);
+}
+
 PKV_DEVINL void store_out(uint16_t* p, float x) {
     *p = static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xffffu);
 }
@@ -242,7 +250,8 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
     using R = QuantRow<FMT, D>;
     constexpr int KS = D / 16;            // k-steps of the scores, m-tiles of P.V
     constexpr int kStages = SM::kStages;
-    constexpr bool kSplit = sizeof(T) == 4;   // fp32: q and the weights in two fp16 parts
+    constexpr bool kSplit = sizeof(T) == 4;   // fp32: q in two fp16 parts
+    constexpr bool kBeside = G <= 4;      // a weight's low part: in column g + 4, or in MMAs of its own
     constexpr int E = D / 4;              // elements of a K row in one lane
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -354,14 +363,15 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
     for (int i = 0; i < kStages; ++i)
         if (i < my_count) issue(i, i, !(stall && i == 0 && lane == 0));
 
-    // q: head g, elements j E ..
+    // q: head g, elements j E ..  (kBeside: columns 4 .. 7 take the heads of 0 .. 3 again)
     const int g8 = lane >> 2;
     const int j4 = lane & 3;
+    const int head = kBeside ? g8 & 3 : g8;
     uint32_t qb[KS][2], ql[kSplit ? KS : 1][2];
     const float q_unit = load_q<T, E, kSplit>(
         static_cast<const T*>(a.q) +
-            (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + (g8 < G ? g8 : 0)) * D + j4 * E,
-        g8 < G, qb, ql);
+            (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + (head < G ? head : 0)) * D + j4 * E,
+        head < G, qb, ql);
     // Scores are held for heads 2 j, 2 j + 1 of tokens t_lo and t_lo + 2.
     const int t_lo = 4 * (g8 >> 1) + (g8 & 1);
     float hs[2];
@@ -551,20 +561,8 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
             }
         }
         // P^T fragments: [token][head] 8x8 tiles transposed in registers, (4 j, 4 j + 1) and the two
-        // tokens after them of head g.  fp4 takes a token's weight in the low or the high half, a
-        // zero in the other: its V pairs two dimensions of a token, and each takes one of them.
-        constexpr int kPar = FMT == PKV_FP8 ? 1 : 2, kTok = FMT == PKV_FP8 ? 1 : 2;
-        uint32_t ph[2][kTok][kPar][2], pl[kSplit ? 2 : 1][kTok][kPar][2];
-        auto place = [](uint32_t (&f)[kTok][kPar][2], int h, uint32_t p) {
-            if constexpr (FMT == PKV_FP8) {
-                f[0][0][h] = p;
-            } else {
-                f[h][0][0] = p & 0xffffu;
-                f[h][0][1] = p >> 16;
-                f[h][1][0] = p << 16;
-                f[h][1][1] = p & 0xffff0000u;
-            }
-        };
+        // tokens after them of head g.  A weight is two fp16 parts, 22 digits.
+        uint32_t ph[2][2], pl[kBeside ? 1 : 2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float p[4];
@@ -576,10 +574,14 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t hi = pack_f16x2(p[2 * h], p[2 * h + 1]);
-                place(ph[u], h, movm_t(hi));
-                if constexpr (kSplit)
-                    place(pl[u], h, movm_t(pack_f16x2(p[2 * h] - f16lo_to_f32(hi),
-                                                      p[2 * h + 1] - f16hi_to_f32(hi))));
+                const uint32_t lo = pack_f16x2(p[2 * h] - f16lo_to_f32(hi),
+                                               p[2 * h + 1] - f16hi_to_f32(hi));
+                if constexpr (kBeside) {
+                    ph[u][h] = movm_t(j4 < 2 ? hi : lo);
+                } else {
+                    ph[u][h] = movm_t(hi);
+                    pl[u][h] = movm_t(lo);
+                }
             }
         }
         // O^T += V^T . P^T
@@ -597,10 +599,9 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
                         uint32_t a0, a1, a2, a3;
                         e4m3x4_to_f16x4(r[2 * h], a0, a2);
                         e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
-                        mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, ph[u][0][0][0], ph[u][0][0][1]);
-                        if constexpr (kSplit)
-                            mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, pl[u][0][0][0],
-                                    pl[u][0][0][1]);
+                        mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, ph[u][0], ph[u][1]);
+                        if constexpr (!kBeside)
+                            mma_f16(acc[2 * p2 + h], a0, a1, a2, a3, pl[u][0], pl[u][1]);
                     }
                 }
             } else {
@@ -619,27 +620,22 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
                               r[3]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {       // 32 dimensions: two groups
+                        // Dimensions d and d + 1 of four tokens, d + 16 and d + 17: as pairs of
+                        // tokens, of d and of d + 1 in turn.
                         uint32_t x[4], y[4], s01, s23, z01, z23;
-                        e2m1x8_to_f16x8(r[2 * h], x);       // (d, d + 1) of four tokens
-                        e2m1x8_to_f16x8(r[2 * h + 1], y);   // (d + 16, d + 17)
+                        e2m1x8_to_f16x8(pair_tokens(r[2 * h]), x);
+                        e2m1x8_to_f16x8(pair_tokens(r[2 * h + 1]), y);
                         const int g0 = 4 * p2 + 2 * h;      // scales of those tokens
                         e4m3x4_to_f16x4(sc[g0], s01, s23);
                         e4m3x4_to_f16x4(sc[g0 + 1], z01, z23);
-                        x[0] = hmul2_lo(x[0], s01); x[1] = hmul2_hi(x[1], s01);
-                        x[2] = hmul2_lo(x[2], s23); x[3] = hmul2_hi(x[3], s23);
-                        y[0] = hmul2_lo(y[0], z01); y[1] = hmul2_hi(y[1], z01);
-                        y[2] = hmul2_lo(y[2], z23); y[3] = hmul2_hi(y[3], z23);
 #pragma unroll
-                        for (int w = 0; w < 2; ++w)
-#pragma unroll
-                            for (int odd = 0; odd < 2; ++odd) {
-                                float(&o)[4] = acc[g0 + odd];
-                                mma_f16(o, x[2 * w], y[2 * w], x[2 * w + 1], y[2 * w + 1],
-                                        ph[u][w][odd][0], ph[u][w][odd][1]);
-                                if constexpr (kSplit)
-                                    mma_f16(o, x[2 * w], y[2 * w], x[2 * w + 1], y[2 * w + 1],
-                                            pl[u][w][odd][0], pl[u][w][odd][1]);
-                            }
+                        for (int odd = 0; odd < 2; ++odd) {
+                            const uint32_t a0 = hmul2(x[odd], s01), a2 = hmul2(x[2 + odd], s23);
+                            const uint32_t a1 = hmul2(y[odd], z01), a3 = hmul2(y[2 + odd], z23);
+                            mma_f16(acc[g0 + odd], a0, a1, a2, a3, ph[u][0], ph[u][1]);
+                            if constexpr (!kBeside)
+                                mma_f16(acc[g0 + odd], a0, a1, a2, a3, pl[u][0], pl[u][1]);
+                        }
                     }
                 }
             }
@@ -659,6 +655,12 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
             mbar_wait_warp(&bars[k % kStages], (k / kStages) & 1, a.status);
     }
 
+    if constexpr (kBeside) {   // what the low parts summed, two lanes further
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[mt][e] += __shfl_xor_sync(0xffffffffu, acc[mt][e], 2);
+    }
     // This warp's denominators: their power of two joins m, and the output is over them.
     float inv[2];
 #pragma unroll
