@@ -12,13 +12,14 @@
 // multiply is the stored row over its power of two, exactly.  The powers of two go where they
 // are exact too:
 //   K's 2^e scales the token's scores (fp32);
-//   V's 2^e goes into the weight: token j adds 2^(s_j + e_j - m) code_j to O and 2^(s_j - m) to
-//     the denominator, s the scores in powers of two.  The reference m follows the largest
-//     s_j + e_j, the size of what the token adds, not the largest s_j, so that the fp16 weights
-//     keep their digits where V's rows differ in size by any power of two.
-// m is a whole number, raised only where a weight would pass 2^15 (exact: the weights stay in
-// fp16's range, the largest at 2^6 or more), and a warp hands on log2 of its denominator's
-// power of two with m, so that neither end of the exponents' range (-90 .. 90) is lost.
+//   V's 2^e goes into the weight: token j adds 2^((s_j - a) + (e_j - b)) code_j to O and 2^(s_j - a)
+//     to the denominator, s the scores in powers of two.  a + b follows the largest s_j + e_j, the
+//     size of what the token adds, so that the fp16 weights keep their digits where V's rows
+//     differ in size by any power of two; a alone follows the largest score, so that s_j - a loses
+//     nothing beside an exponent, and an exponent nothing beside a score of any size.
+// a and b are whole numbers, raised only where a score would pass 2^8 or a weight 2^15 (the weights
+// stay in fp16's range, the largest at 2^6 or more): one vote a pair, and the maxima over lanes only
+// then.
 // q is scaled by a power of two into fp16's range, for fp32 in two fp16 parts.  A weight is two
 // fp16 parts (22 digits; in one it was off by up to 2^-12, and V's of one sign add that up).  The
 // low parts take MMAs of their own for groups of 8 heads, and for smaller ones the idle columns 4 ..
@@ -55,6 +56,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlk = 16;
 constexpr float kTop = 15.f;     // weights are at most 2^kTop
 constexpr float kStart = 7.f;    // and the largest one is put at about 2^kStart
+constexpr float kFar = 8.f;      // scores are at most this far above their reference
 
 template <int FMT, int D, int G>
 struct QuantSmem {
@@ -384,8 +386,9 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
     for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
-    float m_ref[2] = {-1e30f, -1e30f};   // finite: a chunk of -inf scores adds zeros
-    float l_part[2] = {0.f, 0.f};   // this lane's share of the denominators, over 2^m_ref
+    // Finite (a chunk of -inf scores adds zeros), and so low that any other score raises them.
+    float a_ref[2] = {-3.4028235e38f, -3.4028235e38f}, b_ref[2] = {-200.f, -200.f};
+    float l_part[2] = {0.f, 0.f};   // this lane's share of the denominators, over 2^a_ref
 
     // ldmatrix row of this lane: token lane % 16, piece 2 i + lane / 16
     const int v_tok = lane & 15;
@@ -512,53 +515,77 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
                     }
                 }
         }
-        // scores in powers of two, and what the token adds: s + e
-        float t[2][4];
-        float mx[2] = {-INFINITY, -INFINITY};
+        // scores in powers of two, and the exponents of V's rows: their bytes as the low digits of
+        // 2^23, from which one subtraction takes kBias and b
+        constexpr float kBias = 8388608.f + 127.f;
+        float ve[2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t at = side0 + 2 * u * R::kSide + R::kScales + t_lo + 2 * h;
                 const float unit = __int_as_float(lds8(at) << 23);
-                // the byte as the low digits of 2^23: one subtraction makes it a number
-                float ve = __int_as_float(lds8(at + R::kSide) | 0x4b000000) - 8388735.f;
+                ve[u][h] = __int_as_float(lds8(at + R::kSide) | 0x4b000000);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) s[u][2 * h + e] *= unit * hs[e];
                 if (!full) {
                     const int blk = c0 + u;
                     if (t_lo + 2 * h >= (blk < b1 ? L - blk * kBlk : 0)) {
                         s[u][2 * h] = s[u][2 * h + 1] = -INFINITY;
-                        ve = 0.f;
+                        ve[u][h] = kBias;
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    t[u][2 * h + e] = s[u][2 * h + e] + ve;
-                    mx[e] = fmaxf(mx[e], t[u][2 * h + e]);
-                }
             }
+        // Over the references: t = (s - a) + (e - b), the first difference and the second each exact
+        // where it counts, and s - a.
+        float d[2][4], t[2][4];
+        float most_d = -INFINITY, most_t = -INFINITY;
+        auto refer = [&] {
+            const float bias[2] = {kBias + b_ref[0], kBias + b_ref[1]};
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-        }
-        const bool grow0 = mx[0] > m_ref[0] + kTop, grow1 = mx[1] > m_ref[1] + kTop;
-        if (__any_sync(0xffffffffu, grow0 || grow1)) {
-            // In two steps for the denominator: 2^180 times smaller may still count there.
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        d[u][2 * h + e] = s[u][2 * h + e] - a_ref[e];
+                        t[u][2 * h + e] = d[u][2 * h + e] + (ve[u][h] - bias[e]);
+                    }
+                    most_d = fmax3(most_d, d[u][2 * h], d[u][2 * h + 1]);
+                    most_t = fmax3(most_t, t[u][2 * h], t[u][2 * h + 1]);
+                }
+        };
+        refer();
+        if (__any_sync(0xffffffffu, most_d > kFar || most_t > kTop)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float m_new = (h ? grow1 : grow0) ? ceilf(mx[h]) - kStart : m_ref[h];
-                const float half = m_ref[h] == m_new ? 1.f : fast_exp2((m_ref[h] - m_new) * 0.5f);
-                m_ref[h] = m_new;
-                l_part[h] = l_part[h] * half * half;
-                const float al = half * half;
+                float ms = fmaxf(fmaxf(s[0][h], s[0][2 + h]), fmaxf(s[1][h], s[1][2 + h]));
 #pragma unroll
-                for (int mt = 0; mt < KS; ++mt) {
-                    acc[mt][h] *= al;
-                    acc[mt][2 + h] *= al;
+                for (int o = 4; o < 32; o <<= 1)
+                    ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o));
+                const float a_new = ms > a_ref[h] + kFar ? ceilf(ms) : a_ref[h];
+                const float shift = a_ref[h] - a_new;
+                const float b_same = b_ref[h] + shift;   // a + b as it was
+                float mt = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    mt = fmax3(mt, (s[u][h] - a_new) + (ve[u][0] - kBias),
+                               (s[u][2 + h] - a_new) + (ve[u][1] - kBias));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+                const float b_new = mt > b_same + kTop ? ceilf(mt) - kStart : b_same;
+                a_ref[h] = a_new;
+                b_ref[h] = b_new;
+                l_part[h] *= fast_exp2(shift);
+                const float al = b_same == b_new ? 1.f : fast_exp2(b_same - b_new);
+#pragma unroll
+                for (int m = 0; m < KS; ++m) {
+                    acc[m][h] *= al;
+                    acc[m][2 + h] *= al;
                 }
             }
+            refer();
         }
         // P^T fragments: [token][head] 8x8 tiles transposed in registers, (4 j, 4 j + 1) and the two
         // tokens after them of head g.  A weight is two fp16 parts, 22 digits.
@@ -568,8 +595,8 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                p[e] = fast_exp2(t[u][e] - m_ref[e & 1]);
-                l_part[e & 1] += fast_exp2(s[u][e] - m_ref[e & 1]);
+                p[e] = fast_exp2(t[u][e]);
+                l_part[e & 1] += fast_exp2(d[u][e]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -661,19 +688,16 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[mt][e] += __shfl_xor_sync(0xffffffffu, acc[mt][e], 2);
     }
-    // This warp's denominators: their power of two joins m, and the output is over them.
-    float inv[2];
+    // This warp's output over its denominators, and over 1.  b is 91 at most (a score 8 above a, an
+    // exponent of 90, less 7) and -106 at least (no weight passes 2^15) once anything counts.
+    float inv[2], unit[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
             l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], o);
         inv[h] = l_part[h] == 0.f ? 0.f : 1.f / l_part[h];   // zero: no tokens, or none with weight
-        if (l_part[h] > 0.f && l_part[h] < INFINITY) {
-            const int e = (__float_as_int(l_part[h]) >> 23) - 127;
-            m_ref[h] += static_cast<float>(e);
-            l_part[h] *= pow2f(max(-126, min(126, -e)));
-        }
+        unit[h] = pow2f(static_cast<int>(fmaxf(-126.f, fminf(126.f, b_ref[h]))));
     }
     __syncthreads();  // every warp is done with its ring: reuse it as merge scratch
     float* macc = reinterpret_cast<float*>(smem);            // [W][G][D], over the denominator
@@ -689,11 +713,11 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
                 // fp8: dimensions 16 mt + g and + 8.  fp4: the even or the odd ones of 32, + 16
                 const int d0 = FMT == PKV_FP8 ? 16 * mt + g8
                                               : 32 * (mt >> 1) + 2 * g8 + (mt & 1);
-                row[d0] = acc[mt][hh] * inv[hh];
-                row[d0 + (FMT == PKV_FP8 ? 8 : 16)] = acc[mt][2 + hh] * inv[hh];
+                row[d0] = acc[mt][hh] * inv[hh] * unit[hh];
+                row[d0 + (FMT == PKV_FP8 ? 8 : 16)] = acc[mt][2 + hh] * inv[hh] * unit[hh];
             }
             if (g8 == 0) {
-                mm[warp * G + h] = my_count > 0 ? m_ref[hh] : -INFINITY;
+                mm[warp * G + h] = my_count > 0 ? a_ref[hh] : -INFINITY;
                 ml[warp * G + h] = my_count > 0 ? l_part[hh] : 0.f;
             }
         }
@@ -718,6 +742,13 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) share[w * G + g] = f[w] * inv_l;
         if (!whole) {
+            // The denominator's power of two joins M where that is exact, so that the combine's
+            // products of l and outputs stay in range; beyond, scores differ by 1 / 2 or not at all.
+            if (fabsf(M) < 0x1p22f && l > 0.f && l < INFINITY) {
+                const int e = (__float_as_int(l) >> 23) - 127;
+                M += static_cast<float>(e);
+                l *= pow2f(max(-126, min(126, -e)));
+            }
             a.m_part[(row0 + g) * a.max_parts + part] = M;
             a.l_part[(row0 + g) * a.max_parts + part] = l;
         }

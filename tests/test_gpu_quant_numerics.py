@@ -71,6 +71,71 @@ def run(pkv, q, c, table, n, scale, parts=0):
 
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_token_comes_back(pkv, fmt, dtype):
+    """One token has all the weight: its V comes back, whatever its exponent and score.
+
+    The weight's argument is below 8 in magnitude and rounded (2^-22, ln 2 times that of the
+    weight), exp2 is off by 2^-22 in weight and denominator, the weight's two parts by U, the two
+    sums by U each, the quotients by 3 U: 12 U in all.  (bf16: a code's value is one of bf16.)"""
+    S, G, d = 512, 8, 64
+    g = gen(1)
+    k = torch.zeros(S, 1, 1, d, device="cuda")
+    k[..., 0] = (1 + torch.randint(0, 8, (S, 1, 1), generator=g, device="cuda") / 8) \
+        * 2.0 ** -torch.randint(0, 2, (S, 1, 1), generator=g, device="cuda")
+    size = torch.randint(-85, 86, (S, 1, 1, 1), generator=g, device="cuda").double()
+    v = (torch.randn(S, 1, 1, d, generator=g, device="cuda").double() * 2.0 ** size).float()
+    c, table, kk, vv = filled(pkv, k, v, fmt)
+    q = torch.zeros(S, G, d, device="cuda", dtype=dtype)
+    q[..., 0] = 1 + torch.arange(G, device="cuda") / 8
+    q[::2] *= -1
+    out = run(pkv, q, c, table, 1, 0.5).double()
+    want = vv.double()[:, 0].expand(S, G, d)
+    if dtype == torch.bfloat16:
+        assert torch.equal(out, want)
+    else:
+        assert bool(((out - want).abs() <= 12 * U * want.abs()).all()), \
+            float(((out - want).abs() / want.abs().clamp(min=1e-300)).max() / U)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("size", [2, 20, 25, 40, 110, 120])
+def test_scores_of_any_size(pkv, fmt, dtype, sign, size):
+    """Two levels of scores of about 2^size (and, at 120, keys whose scores are -inf), V rows whose
+    sizes differ by 2^40: the tokens of the higher level share the weight.
+
+    Scores of a level are equal to the bit; at size 2, where both count, they are off by 2 U of
+    8.  exp2 by 2^-22 in each weight and denominator.  Up to 2 n + 64 roundings of sums.  What is
+    below 2^-31 of the largest contribution may be lost, of n tokens."""
+    n, hkv, G, d = 100, 2, 4, 64
+    g = gen(size + 2 * sign + 7)
+    kexp = min(90, size // 2)
+    k = torch.zeros(2, n, hkv, d, device="cuda")
+    high = torch.rand(2, n, hkv, generator=g, device="cuda") < 0.5
+    high[:, 50] = True
+    k[..., 0] = torch.where(high, 1.0 if sign < 0 else 1.5, 1.5 if sign < 0 else 1.0) * 2.0 ** kexp
+    if size == 120 and sign < 0:
+        k[:, ::7, :, 0] = 2.0 ** 90
+    e = torch.randint(-20, 21, (2, n, hkv, 1), generator=g, device="cuda").float()
+    v = torch.randn(2, n, hkv, d, generator=g, device="cuda") * 2.0 ** e
+    c, table, kk, vv = filled(pkv, k, v, fmt)
+    q = torch.zeros(2, hkv * G, d, device="cuda", dtype=dtype)
+    q[..., 0] = sign * 2.0 ** (size - kexp)
+    x = torch.einsum("shgd,snhd->shgn", q.double().view(2, hkv, G, d), kk.double()) * 0.5
+    x = torch.where(x.abs() > 3.4e38, torch.full_like(x, sign * torch.inf), x)
+    p = weights(x)
+    ref = torch.einsum("shgn,snhd->shgd", p, vv.double()).reshape(2, hkv * G, d)
+    mag = torch.einsum("shgn,snhd->shgd", p, vv.double().abs()).reshape(ref.shape)
+    rel = (2 * n + 64) * U + 2.0 ** -20 + (2 * 2 * 8 * U if size == 2 else 0)
+    top = vv.double().abs().amax(-1).transpose(1, 2)[:, :, None]       # [S, Hkv, 1, n]
+    small = ((p * top).amax(-1) * n * 2.0 ** -30).reshape(2, hkv * G, 1)
+    for parts in (0, 1):
+        check(run(pkv, q, c, table, n, 0.5, parts), ref, mag * rel + small, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("group", [1, 2, 4, 8])
 @pytest.mark.parametrize("how", ["equal", "mixed"])
 def test_weights_keep_their_digits(pkv, fmt, dtype, group, how):
