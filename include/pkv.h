@@ -597,10 +597,10 @@ pkv_status pkv_copy_blocks_quant(const pkv_quant_cache* cache, const int32_t* pa
  * come back from there.  Attention is over the rows as held: products of their fp16 values, exact,
  * summed in fp32, with softmax weights of 22 binary digits.  Scores and V's rows may have any size:
  * what a token adds to an output is off by those digits and by at most 2^-30 of the largest element
- * that any token adds to its head (far smaller ones may be lost); an element of q by at most 2^-39 of
- * its head's largest, and 2^-22 of itself where it is fp32.  Other arguments, limits and errors as pkv_paged_decode; the workspace is
- * pkv_paged_decode_quant_workspace_bytes, 16-byte aligned, and two calls that may overlap need one
- * each. */
+ * that any token adds to its head (far smaller ones may be lost); an element of q by at most 2^-39
+ * of its head's largest, and 2^-22 of itself where it is fp32.  Other arguments, limits and errors
+ * as pkv_paged_decode; the workspace is pkv_paged_decode_quant_workspace_bytes, 16-byte aligned,
+ * and two calls that may overlap need one each. */
 size_t pkv_paged_decode_quant_workspace_bytes(const pkv_quant_cache* cache, int num_seqs,
                                               int num_q_heads, int max_context,
                                               int partition_blocks);

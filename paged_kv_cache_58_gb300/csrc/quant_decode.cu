@@ -527,7 +527,8 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
                 const float unit = __int_as_float(lds8(at) << 23);
                 ve[u][h] = __int_as_float(lds8(at + R::kSide) | 0x4b000000);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s[u][2 * h + e] *= unit * hs[e];
+                for (int e = 0; e < 2; ++e)   // (in this order: unit * hs may pass fp32's range)
+                    s[u][2 * h + e] = s[u][2 * h + e] * unit * hs[e];
                 if (!full) {
                     const int blk = c0 + u;
                     if (t_lo + 2 * h >= (blk < b1 ? L - blk * kBlk : 0)) {

@@ -136,6 +136,25 @@ def test_scores_of_any_size(pkv, fmt, dtype, sign, size):
 
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_keys_beside_large_queries(pkv, fmt, dtype):
+    """Keys of 2^97 in dimensions where a query of 2^60 in another one is zero: scores of zero,
+    so that the output is the mean of V (n + 64 roundings, exp2's 2^-22 twice)."""
+    n, d = 40, 64
+    g = gen(3)
+    k = torch.randn(1, n, 1, d, generator=g, device="cuda") * 2.0 ** 95
+    k[..., :2] = 0
+    v = torch.randn(1, n, 1, d, generator=g, device="cuda")
+    c, table, kk, vv = filled(pkv, k, v, fmt)
+    q = torch.zeros(1, 2, d, device="cuda", dtype=dtype)
+    q[..., 0] = 2.0 ** 60
+    q[:, 1, 1] = -(2.0 ** 100)
+    out = run(pkv, q, c, table, n, 1.0)
+    ref, mag = (x.double()[:, :, 0].mean(1, keepdim=True).expand(1, 2, d) for x in (vv, vv.abs()))
+    check(out, ref, mag * ((n + 64) * U + 2.0 ** -21), dtype)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("group", [1, 2, 4, 8])
 @pytest.mark.parametrize("how", ["equal", "mixed"])
 def test_weights_keep_their_digits(pkv, fmt, dtype, group, how):
