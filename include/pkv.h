@@ -525,9 +525,9 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
  * A row x of D elements (one token, one kv head, K or V) has an exponent e, the least in
  * -90 .. 90 for which no element is beyond the format's largest value times 2^e.
  *   PKV_FP8: x_i = code_i 2^e, code_i the e4m3 value nearest to x_i 2^-e (largest 448).
- *   PKV_FP4: x_i = code_i s 2^e with an e4m3 scale s for each 16 elements, the nearest to their
- *            largest magnitude times 2^-e times 1/6 (an fp32 product); code_i the e2m1 value
- *            nearest to x_i 2^-e / s (largest value 6 * 448).
+ *   PKV_FP4: x_i = code_i s 2^e with an e4m3 scale s for each 16 elements, the nearest to a sixth of
+ *            their largest magnitude times 2^-e; code_i the e2m1 value nearest to x_i 2^-e / s
+ *            (largest value 6 * 448).
  * Ties go to the even code; a magnitude beyond the largest value, an infinity among them, takes
  * it.  A NaN stays one (fp4: so do the other 15 elements that share its scale).  x_i 2^-e is
  * exact, so a code rounds once.  A row's values are relative to its own largest element: off by

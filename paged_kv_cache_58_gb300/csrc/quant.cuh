@@ -253,9 +253,12 @@ PKV_DEVINL Quantised quantise(const Elems16<T>& in) {
                                    x[4 * i + 3] * unit);
     } else {
         const float a = fminf(__uint_as_float(own) * unit, 2688.f);
-        // A sixth in fp32: a product, exact where a sixth is a midpoint of e4m3 (6 m (1 / 6) is off
-        // by 2^-25 of m before it is rounded, to m), so that ties stay ties.
-        r.scale = to_e4m3x2(a * (1.f / 6.f), 0.f) & 0xffu;
+        // A sixth.  fp32: divided (a quotient rounds to a midpoint of e4m3 only where it is one: where a
+        // is a unit off 6 m, a / 6 is off m by two thirds of a unit or more).  bf16: a product, since
+        // values of eight digits on and next to 6 m are 2^-8 apart, and 6 m (1 / 6), off by 2^-25 of m
+        // before it is rounded, rounds to m.
+        const float sixth = sizeof(T) == 2 ? a * (1.f / 6.f) : __fdiv_rn(a, 6.f);
+        r.scale = to_e4m3x2(sixth, 0.f) & 0xffu;
         const float s = f16lo_to_f32(e4m3x2_to_f16x2(r.scale));
         if (nan) r.scale = 0x7fu;
         // Multiplied by the scale's inverse and the row's unit, the border is met up to two units in
