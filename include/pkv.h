@@ -529,10 +529,10 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
  *            their largest magnitude times 2^-e; code_i the e2m1 value nearest to x_i 2^-e / s
  *            (largest value 6 * 448).
  * Ties go to the even code; a magnitude beyond the largest value, an infinity among them, takes
- * it.  A NaN stays one (fp4: so do the other 15 elements that share its scale).  x_i 2^-e is
- * exact, so a code rounds once.  A row's values are relative to its own largest element: off by
- * 2^-4 of themselves at most in fp8 (rows' smallest elements, below 2^-6 in the code, by 2^-10 of
- * the unit 2^e).
+ * it; what rounds to zero has code 0 in fp4, whatever its sign.  A NaN stays one (fp4: so do the
+ * other 15 elements that share its scale).  x_i 2^-e is exact, so a code rounds once.  A row's
+ * values are relative to its own largest element: off by 2^-4 of themselves at most in fp8 (rows'
+ * smallest elements, below 2^-6 in the code, by 2^-10 of the unit 2^e).
  *
  * Layout.  Device pointers, 16-byte aligned, each array its own:
  *   k_codes, v_codes   [num_blocks][num_kv_heads][block_size][D] e4m3 bytes, or [D / 2] pairs of

@@ -214,6 +214,13 @@ PKV_DEVINL uint32_t to_e2m1x8(const float* u) {
     return r;
 }
 
+// Eight e2m1 codes with zeros' signs cleared: the ways to a code keep or lose the sign of what rounds
+// to zero, and the bytes are not to depend on the way.
+PKV_DEVINL uint32_t plain_zeros(uint32_t c) {
+    const uint32_t m = c & 0x77777777u;                    // + 7: bit 3 set where it is not zero
+    return m | (c & (m + 0x77777777u) & 0x88888888u);
+}
+
 // The least e with top <= 448 2^e = 1.75 2^(e + 8), or 2688 2^e = 1.3125 2^(e + 11), top of these
 // bits: the exponent of top less that of the largest value, one more where top's digits pass its.
 template <int FMT>
@@ -285,8 +292,8 @@ PKV_DEVINL Quantised quantise(const Elems16<T>& in) {
                 for (int i = 0; i < 16; ++i) u[i] = s > 0.f ? __fdiv_rn(x[i] * unit, s) : 0.f;
             }
         }
-        r.codes[0] = to_e2m1x8(u);
-        r.codes[1] = to_e2m1x8(u + 8);
+        r.codes[0] = plain_zeros(to_e2m1x8(u));
+        r.codes[1] = plain_zeros(to_e2m1x8(u + 8));
         r.codes[2] = r.codes[3] = 0;
     }
     return r;

@@ -55,3 +55,38 @@ def test_fp4_scales_next_to_every_border(pkv):
                 else (t % 16)[:, None] * 8 + g)
         got = e4m3_values()[side[t // 16][t[:, None], byte].long()]
         assert torch.equal(got[:, 1:], want), (got[:, 1:] - want).abs().max()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_zeros_with_a_sign(pkv, fmt):
+    """Small negative elements, negative zeros, groups and rows of them: rows of bf16 and the same
+    in fp32 leave the same bytes, whatever the other elements of their group are."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(96, 2, 128, generator=g, device="cuda")
+    x[::3] *= 2.0 ** -torch.randint(0, 20, (32, 2, 128), generator=g, device="cuda").float()
+    x[1::3, :, ::2] = -0.0
+    x[4, :, 16:32] = -0.0
+    x[5, :, 16:32] = -1e-6
+    x[6] = -0.0
+    x[8, :, 1:] = -1e-30
+    x = x.bfloat16()
+    caches = [cleared(pkv, 6, 1, 128, fmt) for _ in range(3)]
+    slots = torch.arange(96, device="cuda")
+    y = x.float()
+    z = y.clone()
+    off = torch.rand(96, 2, 8, generator=g, device="cuda") * 1e-6      # off the borders' grid
+    part = z[:, :, 40:48]
+    part += torch.where(part.abs() < 0.5 * z.abs().amax(-1, keepdim=True), off, 0.0)
+    pkv.kv_append_quant(caches[0], slots, x[:, :1], x[:, 1:])
+    pkv.kv_append_quant(caches[1], slots, y[:, :1], y[:, 1:])
+    for name in ("k", "v", "k_scales", "v_scales"):
+        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), name
+    # other groups of the rows that changed keep their bytes
+    pkv.kv_append_quant(caches[2], slots, z[:, :1], z[:, 1:])
+    keep = slice(64, 128) if fmt == "fp8" else slice(32, 64)
+    for a, b in ((caches[1].k, caches[2].k), (caches[1].v, caches[2].v)):
+        assert torch.equal(a.view(96, -1)[:, keep], b.view(96, -1)[:, keep])
+    if fmt == "fp4":
+        for c in caches[:2]:
+            assert not any(bool((t & 15 == 8).any() or (t >> 4 == 8).any()) for t in (c.k, c.v))
+    assert pkv.read_device_status() == 0
