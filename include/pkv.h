@@ -534,7 +534,8 @@ pkv_status pkv_evict(const pkv_pool_desc* pool, void* k_pool, void* v_pool,
  * values are relative to its own largest element: off by 2^-4 of themselves at most in fp8 (rows'
  * smallest elements, below 2^-6 in the code, by 2^-10 of the unit 2^e).
  *
- * Layout.  Device pointers, 16-byte aligned, each array its own:
+ * Layout.  Device pointers, 16-byte aligned, each array its own (PKV_ERR_INVALID where two share
+ * bytes):
  *   k_codes, v_codes   [num_blocks][num_kv_heads][block_size][D] e4m3 bytes, or [D / 2] pairs of
  *                      e2m1 (element 2 i in byte i's low half).
  *   k_scales, v_scales [num_blocks][num_kv_heads][block_size / 16] runs of, for PKV_FP4, the D
@@ -578,6 +579,8 @@ pkv_status pkv_kv_read_quant(const pkv_quant_cache* cache, const int64_t* slot_m
  * times.  Every row of a block is moved, also ones never written.
  *   pool   k_pool / v_pool's description; block_size, num_kv_heads and head_dim as the cache's.
  *   pairs  device int32 [num_pairs][2] = (source block, destination block); destinations distinct.
+ * Pools and the cache's arrays may not share bytes, nor may the two pools that
+ * pkv_dequantize_blocks writes (PKV_ERR_INVALID).
  * An id outside its own side's blocks skips that pair and raises PKV_ERR_OOB in the device status
  * word.  num_pairs * num_kv_heads * block_size below 2^31. */
 pkv_status pkv_quantize_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,

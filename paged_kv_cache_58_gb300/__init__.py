@@ -956,6 +956,9 @@ class QuantCache:
         if not _load().pkv_quant_codes_bytes(ctypes.byref(self.desc)):
             raise ValueError("a quantised cache has blocks of 16 or 32 tokens and heads of 64 or "
                              "128, fewer than 2^31 rows in all")
+        runs = sorted((t.data_ptr(), t.numel()) for t in (k, v, k_scales, v_scales))
+        if any(at + n > after for (at, n), (after, _) in zip(runs, runs[1:])):
+            raise ValueError("the four arrays of a quantised cache may not share memory")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.format, self.device = format, dev
         self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim = nb, hkv, block, dim
@@ -1033,7 +1036,8 @@ def quantize_blocks(cache, k_pool, v_pool, pairs, stream=None) -> None:
 
 def dequantize_blocks(cache, k_pool, v_pool, pairs, stream=None) -> None:
     """Read whole blocks of a QuantCache into a pool: pool[dst] = cache[src] for each (src, dst)
-    of pairs (int32 [n, 2]).  A prefix read back so is what paged_prefill attends to."""
+    of pairs (int32 [n, 2]).  k_pool and v_pool may not overlap.  A prefix read back so is what
+    paged_prefill attends to."""
     _move_blocks("pkv_dequantize_blocks", cache, k_pool, v_pool, pairs, stream)
 
 

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
@@ -1506,6 +1507,32 @@ bool quant_arrays_ok(const pkv_quant_cache* c) {
            aligned16(c->v_codes) && aligned16(c->k_scales) && aligned16(c->v_scales);
 }
 
+// Runs of bytes, one after another in no order: whether none shares a byte with another.
+struct Run {
+    const void* at;
+    uint64_t bytes;
+};
+bool runs_apart(std::initializer_list<Run> runs) {
+    for (const Run* x = runs.begin(); x != runs.end(); ++x)
+        for (const Run* y = runs.begin(); y != x; ++y) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(x->at);
+            const uintptr_t q = reinterpret_cast<uintptr_t>(y->at);
+            if (p < q + y->bytes && q < p + x->bytes) return false;
+        }
+    return true;
+}
+
+// The four arrays apart from one another, and from each of two runs beside them: kernels store to
+// any of them in any order.
+bool quant_arrays_apart(const pkv_quant_cache* c, Run a = {nullptr, 0}, Run b = {nullptr, 0}) {
+    const uint64_t codes = static_cast<uint64_t>(c->num_blocks) * quant_code_bytes(c);
+    const uint64_t side = static_cast<uint64_t>(c->num_blocks) * quant_side_bytes(c);
+    return runs_apart({{c->k_codes, codes}, {c->v_codes, codes}, {c->k_scales, side},
+                       {c->v_scales, side}, a}) &&
+           (!b.bytes || runs_apart({{c->k_codes, codes}, {c->v_codes, codes}, {c->k_scales, side},
+                                    {c->v_scales, side}, b}));
+}
+
 pkv::QuantArgs quant_args(const pkv_quant_cache* c, int* status) {
     pkv::QuantArgs a{};
     a.k_codes = static_cast<uint8_t*>(c->k_codes);
@@ -1539,6 +1566,7 @@ pkv_status quant_rows(const pkv_quant_cache* cache, const int64_t* slot_mapping,
         return PKV_ERR_INVALID;
     if (read && !rows_apart({k, k_stride * es, row * es}, {v, v_stride * es, row * es}, num_tokens))
         return PKV_ERR_INVALID;
+    if (!quant_arrays_apart(cache)) return PKV_ERR_INVALID;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;
     pkv::QuantArgs a = quant_args(cache, status);
@@ -1570,6 +1598,10 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
     if (num_pairs > INT32_MAX / per) return PKV_ERR_UNSUPPORTED;
     if (!quant_arrays_ok(cache) || !k || !v || !pairs || !aligned16(k) || !aligned16(v) ||
         !aligned4(pairs))
+        return PKV_ERR_INVALID;
+    const uint64_t bytes = pkv_pool_bytes(pool);
+    if (!quant_arrays_apart(cache, {k, bytes}, {v, bytes}) ||
+        (read && !runs_apart({{k, bytes}, {v, bytes}})))
         return PKV_ERR_INVALID;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;
@@ -1655,7 +1687,8 @@ pkv_status pkv_copy_blocks_quant(const pkv_quant_cache* cache, const int32_t* pa
     if (st != PKV_OK) return st;
     if (num_pairs < 0) return PKV_ERR_INVALID;
     if (num_pairs == 0) return PKV_OK;
-    if (!quant_arrays_ok(cache) || !pairs || !aligned4(pairs)) return PKV_ERR_INVALID;
+    if (!quant_arrays_ok(cache) || !pairs || !aligned4(pairs) || !quant_arrays_apart(cache))
+        return PKV_ERR_INVALID;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;
     pkv::QuantArgs a = quant_args(cache, status);
@@ -1709,6 +1742,7 @@ pkv_status pkv_paged_decode_quant(const pkv_quant_cache* cache, int dtype, void*
     const size_t need = decode_workspace(num_seqs, num_q_heads, cache->head_dim, max_parts);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return PKV_ERR_NOMEM;
+    if (!quant_arrays_apart(cache)) return PKV_ERR_INVALID;
     int* status = status_word();
     if (!status) return PKV_ERR_CUDA;
 

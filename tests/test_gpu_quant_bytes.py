@@ -90,3 +90,35 @@ def test_zeros_with_a_sign(pkv, fmt):
         for c in caches[:2]:
             assert not any(bool((t & 15 == 8).any() or (t >> 4 == 8).any()) for t in (c.k, c.v))
     assert pkv.read_device_status() == 0
+
+
+def test_fresh_pools_and_arrays_apart(pkv):
+    """One tensor for K and V, or for codes and scales of both, is refused; halves of one are not."""
+    c = cleared(pkv, 3, 2, 64, "fp8")
+    with pytest.raises(ValueError):
+        pkv.QuantCache(c.k, c.k, c.k_scales, c.v_scales)
+    with pytest.raises(ValueError):
+        pkv.QuantCache(c.k, c.v, c.k_scales, c.k_scales)
+    flat = torch.zeros(2 * c.k.numel(), dtype=torch.uint8, device="cuda")
+    n = c.k.numel()
+    with pytest.raises(ValueError):
+        pkv.QuantCache(c.k, flat[64:64 + n].view(c.k.shape), flat[:n].view(c.k.shape)[:, :, :, 0]
+                       .contiguous(), flat[:c.k_scales.numel()].view(c.k_scales.shape))
+    both = pkv.QuantCache(flat[:n].view(c.k.shape), flat[n:].view(c.k.shape), c.k_scales,
+                          c.v_scales)
+    x = torch.randn(5, 2, 64, generator=torch.Generator(device="cuda").manual_seed(1),
+                    device="cuda")
+    pkv.kv_append_quant(both, torch.arange(5, device="cuda"), x, -x)
+    pool = torch.full((3, 2, 16, 64), 7.0, device="cuda")
+    pairs = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.dequantize_blocks(both, pool, pool, pairs)
+    assert e.value.status == 1
+    assert bool((pool == 7.0).all())
+    two = torch.zeros(2, 3, 2, 16, 64, device="cuda")
+    pkv.dequantize_blocks(both, two[0], two[1], pairs)
+    assert torch.equal(two[0, 1, :, :5].double().cpu(),
+                       held(both.k, both.k_scales, "fp8", False)[0, :, :5])
+    assert torch.equal(two[0, 1, :, :5], -two[1, 1, :, :5])
+    pkv.quantize_blocks(both, two[1], two[1], pairs)         # sources may be one pool
+    assert pkv.read_device_status() == 0
