@@ -935,7 +935,8 @@ class QuantCache:
     per 16 elements, and a power of two per row.  k, v: uint8 [num_blocks, Hkv, B, D] (fp4:
     [..., D / 2]); k_scales, v_scales: uint8 [num_blocks, Hkv, B], fp4 [num_blocks, Hkv,
     B / 16 * (D + 16)].  QuantCache.empty makes them; given ones are held, not copied.  Its memory
-    need not be cleared: slots that were never written are not looked at."""
+    need not be cleared: a decode does not look at slots that were never written.  kv_read_quant and
+    the moves of whole blocks do, and carry on what is there, NaN and infinities included."""
 
     def __init__(self, k, v, k_scales, v_scales, *, format="fp8"):
         if format not in QUANT_FORMATS:
@@ -1036,8 +1037,8 @@ def quantize_blocks(cache, k_pool, v_pool, pairs, stream=None) -> None:
 
 def dequantize_blocks(cache, k_pool, v_pool, pairs, stream=None) -> None:
     """Read whole blocks of a QuantCache into a pool: pool[dst] = cache[src] for each (src, dst)
-    of pairs (int32 [n, 2]).  k_pool and v_pool may not overlap.  A prefix read back so is what
-    paged_prefill attends to."""
+    of pairs (int32 [n, 2]), every row of them, also ones never written.  k_pool and v_pool may not
+    overlap.  A prefix read back so is what paged_prefill attends to."""
     _move_blocks("pkv_dequantize_blocks", cache, k_pool, v_pool, pairs, stream)
 
 

@@ -72,9 +72,11 @@ struct DecodeArgs {
     // CTAs take no SM before the stream's previous kernel has ended (the cascade decode:
     // the prefix pass on the side stream is placed first).
     int no_pdl;
-    // Test hook (both decode kernels): nonzero makes warp 0 of CTA (0, 0, 0) arm its first
-    // stage for 16 bytes more than the stage's copies deliver, so that wait runs out of
-    // time (PKV_ERR_TIMEOUT) while every copy still lands.  Zero in normal use.
+    // Test hook (the decode kernels over pools): nonzero makes warp 0 of CTA (0, 0, 0) arm its
+    // first stage for 16 bytes more than the stage's copies deliver, so that wait runs out of
+    // time (PKV_ERR_TIMEOUT) while every copy still lands.  The decode over a quantised cache
+    // counts lanes, not bytes: there lane 0 of that warp does not arrive for its copies, and every
+    // lane waits for its own before the ring is used again.  Zero in normal use.
     int test_stall;
     // Fused append (decode only): non-null k_new / v_new ([num_seqs][Hkv][D], pool
     // dtype) are the K / V of each sequence's newest token, position context_lens[s] - 1.

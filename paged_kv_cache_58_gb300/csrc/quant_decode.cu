@@ -311,7 +311,9 @@ quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
     }
     __syncwarp();
 
-    const uint64_t stream_policy = l2_policy_evict_first();   // each byte is read once
+    // A sequence reads each byte once.  (A block that many tables name is read by each of them, and
+    // under the same policy.)
+    const uint64_t stream_policy = l2_policy_evict_first();
     int ids = my_first < b1 ? ids0 : -1;
     auto fetch_ids = [&](int base) {
         const int c = my_first + 2 * kWarps * base;
