@@ -1618,13 +1618,19 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
                                             read, static_cast<cudaStream_t>(stream)));
 }
 
-// Partition of a decode over a quantised cache, in pool blocks.  As long as 256 chunks (4096 tokens)
-// where that leaves 4096 CTAs, about nine for each that is resident: a CTA's start and its merge
-// cost about as much as 16 chunks a warp (16 sequences of 16k .. 128k tokens: 401 us in fp8 and 335 in
-// fp4, with 128 chunks 407 and 347).  Else down to 64 chunks, where more, shorter ones cost more
-// than they balance (64 of 512 .. 4096: 54.4 and 54.9 us; 40 chunks 56.0 and 56.6, 128 chunks 55.4 and
-// 59.1), and below that only while an SM would have fewer than three.  A multiple of 8 chunks (a pair
-// for each warp), and at most 512 partitions.
+// Partition of a decode over a quantised cache, in pool blocks.  A CTA's start and its merge cost
+// about as much as 16 chunks a warp, so 256 chunks (4096 tokens), or 128, where that leaves 12
+// CTAs an SM, three or four for each that is resident; with fewer the last ones leave SMs idle.  us
+// with 256 / 128 / 64 chunks, 8 kv heads of 128:
+//   12 sequences of 16k .. 128k     fp8 325 / 329 / 352   fp4 292 / 304 / 335   (256: 3072 CTAs)
+//   16                                  402 / 408 / 438       359 / 376 / 417   (4096)
+//   6                                   164 / 158 / 167       147 / 145 / 160   (1536)
+//   100 of 1024 .. 8192                 157 / 153 / 153       146 / 143 / 151   (1600)
+//   32 of 2048 .. 16384                 102 /  92 /  93        88 /  84 /  89   (1024)
+//   64 of 512 .. 4096                  54.5 / 55.5 / 53.6    68.6 / 58.3 / 56.4 (512)
+// Else 64 chunks, where more, shorter ones cost more than they balance (the last row with 32: 55.9 and
+// 59.8), and below that only while there would be fewer than 456 CTAs, three an SM.  A multiple of 8
+// chunks (a pair for each warp), and at most 512 partitions.
 int quant_partition(const pkv_quant_cache* cache, int num_seqs, int max_context,
                     int partition_blocks) {
     if (partition_blocks) return partition_blocks;
@@ -1633,7 +1639,7 @@ int quant_partition(const pkv_quant_cache* cache, int num_seqs, int max_context,
     const int least = ceil_div(ceil_div(chunks, 512), 8) * 8;
     auto halved = [](int pc) { return (pc / 2 + 7) / 8 * 8; };
     int pc = std::max(256, least);
-    while (pc > 64 && halved(pc) >= least && rows * ceil_div(chunks, pc) < 4096) pc = halved(pc);
+    while (pc > 64 && halved(pc) >= least && rows * ceil_div(chunks, pc) < 12 * 152) pc = halved(pc);
     while (pc > 8 && halved(pc) >= least && rows * ceil_div(chunks, pc) < 3 * 152) pc = halved(pc);
     return pc >> chunk_shift(cache->block_size);
 }
