@@ -63,8 +63,9 @@ struct QuantSmem {
     using R = QuantRow<FMT, D>;
     static constexpr int kSlab = kBlk * R::kCodes;
     // A stage: K and V of two chunks.  The loop is unrolled over the stages, and past two its code
-    // costs more than copies further ahead bring (head_dim 64, 64 sequences of 512 .. 4096 tokens,
-    // fp8 and fp4: 39.4 and 39.5 us; 4 and 6 stages 42.2 and 49.0).
+    // costs more than copies further ahead bring (head_dim 64, 64 x 512 .. 4096 and 16 x 16k .. 128k
+    // tokens, fp8: 33.8 and 216 us, four stages 38.9 and 222, six 50.5 and 262; fp4 36.2 and 216, 43.1
+    // and 249, 48.9 and 289).
     static constexpr int kStages = 2;
     static constexpr int kCodeRing = kWarps * kStages * 4 * kSlab;
     static constexpr int kSideRing = kWarps * kStages * 4 * R::kSide;
@@ -239,14 +240,16 @@ PKV_DEVINL float load_q(const T* p, bool there, uint32_t (&hi)[E / 4][2],
     return pow2f(max(-126, -up));
 }
 
-// CTAs that share an SM: four where a CTA's rings (66 KB for fp8 rows of 128) and 128 registers a
-// thread leave room for them (fp4, head_dim 128, 16 x 16k .. 128k tokens: 372 us, 388 with three;
-// fp8, head_dim 64, 64 x 512 .. 4096: 36.8 us, 39.4; five, of 96 registers: 417 and 37.5).
-template <int FMT, int D, typename T>
-constexpr int kCtas = sizeof(T) == 2 && (FMT == PKV_FP4 || D == 64) ? 4 : 3;
+// CTAs that share an SM: four for bf16 rows of 64, three of 168 registers a thread for the others (us
+// with three / four / five, of 168, 128 and 96 registers, 64 x 512 .. 4096 and 16 x 16k .. 128k tokens:
+// head_dim 64 fp8 34.7 / 33.8 / 34.9 and 218 / 216 / 216, fp4 37.4 / 36.2 / 41.1 and 230 / 216 / 249;
+// head_dim 128 fp4, where 128 registers spill, 53.3 / 56.4 / 68.3 and 345 / 359 / 450; fp8 rows of 128
+// have 66 KB of rings a CTA).
+template <int D, typename T>
+constexpr int kCtas = sizeof(T) == 2 && D == 64 ? 4 : 3;
 
 template <int FMT, int D, int G, typename T>
-__global__ void __launch_bounds__(kThreads, kCtas<FMT, D, T>)
+__global__ void __launch_bounds__(kThreads, kCtas<D, T>)
 quant_decode_kernel(const DecodeArgs a, const QuantSides qs) {
     using SM = QuantSmem<FMT, D, G>;
     using R = QuantRow<FMT, D>;
