@@ -1620,16 +1620,16 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
 
 // Partition of a decode over a quantised cache, in pool blocks.  A CTA's start and its merge cost
 // about as much as 16 chunks a warp, so 256 chunks (4096 tokens), or 128, where that leaves 12
-// CTAs an SM, three or four for each that is resident; with fewer the last ones leave SMs idle.  us
+// CTAs an SM, four (three) for each that is resident; with fewer the last ones leave SMs idle.  us
 // with 256 / 128 / 64 chunks, 8 kv heads of 128:
-//   12 sequences of 16k .. 128k     fp8 325 / 329 / 352   fp4 292 / 304 / 335   (256: 3072 CTAs)
-//   16                                  402 / 408 / 438       359 / 376 / 417   (4096)
-//   6                                   164 / 158 / 167       147 / 145 / 160   (1536)
-//   100 of 1024 .. 8192                 157 / 153 / 153       146 / 143 / 151   (1600)
-//   32 of 2048 .. 16384                 102 /  92 /  93        88 /  84 /  89   (1024)
-//   64 of 512 .. 4096                  54.5 / 55.5 / 53.6    68.6 / 58.3 / 56.4 (512)
-// Else 64 chunks, where more, shorter ones cost more than they balance (the last row with 32: 55.9 and
-// 59.8), and below that only while there would be fewer than 456 CTAs, three an SM.  A multiple of 8
+//   12 sequences of 16k .. 128k     fp8 321 / 325 / 348   fp4 279 / 290 / 322   (256: 3072 CTAs)
+//   16                                  398 / 401 / 434       346 / 361 / 405   (4096)
+//   6                                   162 / 155 / 163       147 / 141 / 156   (1536)
+//   100 of 1024 .. 8192                 155 / 150 / 151       138 / 135 / 147   (1600)
+//   32 of 2048 .. 16384                 100 /  91 /  91        93 /  82 /  86   (1024)
+//   64 of 512 .. 4096                  53.8 / 55.0 / 53.0    53.2 / 54.8 / 53.6 (512)
+// Else 64 chunks, where more, shorter ones cost more than they balance (the last row with 32: 55.7 and
+// 60.2), and below that only while there would be fewer than 456 CTAs, three an SM.  A multiple of 8
 // chunks (a pair for each warp), and at most 512 partitions.
 int quant_partition(const pkv_quant_cache* cache, int num_seqs, int max_context,
                     int partition_blocks) {

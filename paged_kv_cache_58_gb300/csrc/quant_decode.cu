@@ -3,9 +3,8 @@
 // One CTA per (partition, kv head, sequence), as over bf16 pools (paged_decode_tc.cu): warp w of four
 // takes the pairs of 16-token chunks w, w + 4, ... of the partition through a ring of stages of its
 // own and keeps its own online softmax, one step for the 32 tokens of a pair; the four states
-// merge at the end, and partitions merge in the combine kernel.  (Chunk by chunk: 16 sequences of
-// 16k .. 128k tokens, 8 query heads to a kv head, 445 us in fp8 and 490 in fp4; 428 and 406 in
-// pairs.)  A chunk is
+// merge at the end, and partitions merge in the combine kernel.  (Chunk by chunk instead of in pairs:
+// 4 % more time in fp8 and 20 % in fp4, before the weights had two parts.)  A chunk is
 //   S^T[16 tokens x 8 heads] = K[16 x D] . q^T,   O^T[D x 8 heads] += V^T[D x 16] . P^T
 // as fp16 MMAs m16n8k16 with fp32 sums.  fp16, because every e4m3 value is one of fp16, and so is
 // every product of an e2m1 value and its e4m3 scale (6 digits, 2^-10 or more): what the MMAs
@@ -27,14 +26,14 @@
 //
 // Copies.  A pair's 4 to 8 KB come 16 bytes a lane (cp.async, swizzled by the lane, counted on an
 // mbarrier), 512 bytes an instruction.  As eight bulk and tensor copies a pair, each lane's own and
-// so issued one after the other, they took 30 instructions more: 402 and 345 us where this takes 397
-// and 336, and tensor maps for every call's arrays.
+// so issued one after the other, they took 30 instructions more (1 % of the time in fp8, 3 in fp4) and
+// tensor maps for every call's arrays.
 //
-// Bound.  fp8: HBM (16 x 16k .. 128k tokens: 397 us, 7.1 TB/s; 64 x 512 .. 4096: 54 us, 5.8 TB/s, a
-// sixth of it the first copies, the ends of CTAs and the combine).  fp4: issue slots.  Its bytes
-// would take 235 us where it takes 336: 362 warp instructions a chunk, 128 of them to make fp16 of
-// 4096 codes (two values each for cvt.f16x2.e2m1x2 and for the product with the scale), issued at
-// 2.6 of 4 a clock.
+// Bound.  fp8: HBM (16 x 16k .. 128k tokens, 8 query heads to a kv head: 407 us a call, 6.9 TB/s; 64 x
+// 512 .. 4096: 53 us, 5.8 TB/s, a sixth of it the first copies, the ends of CTAs and the combine).
+// fp4: its bytes would take 236 us where the long batch takes 346, with 352 warp instructions a chunk,
+// 128 of them to make fp16 of 4096 codes (two values each for cvt.f16x2.e2m1x2 and for the product with
+// the scale), issued at 2.5 of 4 a clock by 12 warps an SM: instructions and their latency both.
 //
 // Fragments.  The index that an MMA sums over may be in any order, if both sides share it.  So
 // lane (g, j) = (lane / 4, lane % 4) takes elements j D / 4 .. of K's row as they lie, and the
