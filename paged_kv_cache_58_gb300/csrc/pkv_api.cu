@@ -1622,8 +1622,8 @@ pkv_status quant_blocks(const pkv_quant_cache* cache, const pkv_pool_desc* pool,
 // about as much as 16 chunks a warp, so 256 chunks (4096 tokens), or 128, where that leaves 12
 // CTAs an SM, four (three) for each that is resident; with fewer the last ones leave SMs idle.  us
 // with 256 / 128 / 64 chunks, 8 kv heads of 128:
-//   12 sequences of 16k .. 128k     fp8 321 / 325 / 348   fp4 279 / 290 / 322   (256: 3072 CTAs)
-//   16                                  398 / 401 / 434       346 / 361 / 405   (4096)
+//   12 sequences of 16k .. 128k     fp8 321 / 325 / 348   fp4 279 / 290 / 322
+//   16                                  398 / 401 / 434       346 / 361 / 405   (256: 4096 CTAs)
 //   6                                   162 / 155 / 163       147 / 141 / 156   (1536)
 //   100 of 1024 .. 8192                 155 / 150 / 151       138 / 135 / 147   (1600)
 //   32 of 2048 .. 16384                 100 /  91 /  91        93 /  82 /  86   (1024)
